@@ -14,9 +14,12 @@ import ctypes
 import os
 import re
 
+from . import decode as _decode
+
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libbq.so")
 HEADER = os.path.join(os.path.dirname(PKG_DIR), "include", "bq.h")
+DECODE_HEADER = os.path.join(os.path.dirname(PKG_DIR), "include", "bq_decode.h")
 
 BQ_OK, BQ_ERR_INVALID_ARG, BQ_ERR_UNSUPPORTED, BQ_ERR_ALIGNMENT, BQ_ERR_CUDA, BQ_ERR_TIMEOUT = range(6)
 BQ_F16, BQ_F32 = 0, 1
@@ -60,6 +63,7 @@ _SIGNATURES = {
                                          _vp, _vp, _vp]),
     "bq_device_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int), ctypes.c_int]),
     "bq_set_wait_timeout_ns": (_c_i64, [_c_i64]),
+    **_decode.SIGNATURES,
 }
 
 _lib = None
@@ -86,9 +90,9 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def header_functions() -> list[str]:
-    """Names of the functions include/bq.h declares."""
-    with open(HEADER, encoding="utf-8") as f:
+def header_functions(header: str = HEADER) -> list[str]:
+    """Names of the functions that include/bq.h (or another header) declares."""
+    with open(header, encoding="utf-8") as f:
         text = f.read()
     return sorted(set(re.findall(r"^\s*(?:const\s+)?[\w]+\*?\s+\*?(bq_\w+)\s*\(", text, re.M)))
 
@@ -443,3 +447,11 @@ def bq_device_status(reset=True) -> int:
 
 def bq_set_wait_timeout_ns(ns: int) -> int:
     return int(lib().bq_set_wait_timeout_ns(int(ns)))
+
+
+# The decoder-layer operators (include/bq_decode.h)
+bq_gemm_f16xi4_group = _decode.bq_gemm_f16xi4_group
+bq_kv4_pool = _decode.bq_kv4_pool
+bq_qk_norm_rope_kv4 = _decode.bq_qk_norm_rope_kv4
+bq_attn_kv4_workspace = _decode.bq_attn_kv4_workspace
+bq_attn_kv4 = _decode.bq_attn_kv4
