@@ -139,13 +139,14 @@ bq_status bq_qk_norm_rope_kv4(const uint16_t* q, int64_t ld_q, const uint16_t* k
  *                is 0); it need not be cleared, and calls that share one run
  *                in stream order
  *   4-byte alignment is enough for block_table, seq_lens and cu_q.
- *   Lengths beyond max_len, more than max_q query tokens, rows outside
- *   [0, T) and pages outside the pool are cut off or treated as not there,
- *   and bq_device_status reports BQ_ERR_INVALID_ARG.
+ *   Lengths beyond max_len and more than max_q query tokens are cut off, a
+ *   sequence whose rows are not in [0, T) is left out, a page outside the pool
+ *   is read as page 0, and bq_device_status reports BQ_ERR_INVALID_ARG.
  *   T = 0 or B = 0 is an empty call.
  *   Errors: INVALID_ARG (null pointers, q_heads not a multiple of kv_heads,
- *   negative sizes, max_len above ld_table * page_size, a workspace that is
- *   too small), ALIGNMENT, UNSUPPORTED, CUDA.
+ *   negative sizes, max_len above ld_table * page_size, an empty pool with
+ *   max_len > 0, a workspace that is too small), ALIGNMENT, UNSUPPORTED (the
+ *   pool's shape, max_len above 2**30), CUDA.
  */
 size_t bq_attn_kv4_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q,
                              int64_t max_len);

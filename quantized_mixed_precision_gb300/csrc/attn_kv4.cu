@@ -1,125 +1,827 @@
 // Attention of new tokens over the 4-bit cache (bq_attn_kv4).
 //
-// One block per (query token, query head): the threads score 128 keys at a
-// time, keep a running maximum and sum, and accumulate one output dim each.
+// A value of the cache is x = low + step * u with a code u in 0..15 for each
+// group of dims, so for a query q and weights p
+//   q . k[t]        = sum_g step[t, g] * (sum_{d in g} q[d] u[t, d]) + low[t, g] * (sum_{d in g} q[d])
+//   sum_t p[t] v[t] = sum_t (p[t] step[t, g]) u[t, d] + sum_t p[t] low[t, g]
+// and the tensor cores multiply the codes themselves: as fp16 subnormals they
+// need one LOP3 per two codes and no arithmetic (kv4_device.cuh).
+//
+// The keys are the rows of the first product's A operand and the dims the
+// rows of the second one's, so 8 query rows (the heads that share a kv head,
+// times the query tokens) are its 8 columns and none of an MMA is idle at
+// q_heads / kv_heads = 8.  Scores leave the first MMA with a key per lane
+// row, where its step and low are applied, and movmatrix turns the weights
+// into the second MMA's B operand.
+//
+// Work is split over warps by tiles of 32 keys.  A unit is one (sequence,
+// kv head, block of query rows); the blocks of the grid take equal contiguous
+// ranges of the tiles of all units, whatever the lengths are, and a unit that
+// falls into several ranges is joined by a second kernel from (maximum, sum,
+// accumulator) parts.  Short caches run one block per unit and no join.
 #include <cuda_fp16.h>
 
 #include "bq_device.cuh"
 #include "decode_internal.h"
+#include "kv4_device.cuh"
 
 namespace bq {
 
 namespace {
 
-constexpr int AT = 128;
+constexpr int AW = 4;             // warps of a block
+constexpr int TILE = 32;          // keys of a warp's tile
+constexpr int64_t DIRECT_LEN = 512;   // up to here one block takes a whole unit
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float M_NONE = -1e30f;  // running maximum before any key
 
-__device__ __forceinline__ float block_reduce(float v, bool max, float* red) {
-  for (int o = 16; o > 0; o >>= 1) {
-    const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = max ? fmaxf(v, u) : v + u;
+struct Meta {
+  int32_t parts;       // 0: nothing to join here
+  int32_t b, head, qt;
+};
+
+struct AttnParams {
+  const __half* q;
+  int64_t ld_q, T;
+  const uint8_t* codes;
+  const uint8_t* params;
+  int64_t num_pages;
+  int page_log2, heads, rep;      // rep = q_heads / kv_heads
+  const int32_t* table;
+  int64_t ld_table;
+  const int32_t *lens, *cu_q;
+  int64_t B;
+  int64_t max_q, max_len, window;
+  int qtiles;                     // blocks of query rows for max_q tokens
+  float scale;
+  __half* out;
+  float* lse;
+  float* parts;                   // [2 * grid][rows][D + 2]
+  Meta* meta;                     // [grid]
+  int* status;
+};
+
+// One sequence as the kernels see it: its query rows and range of keys.
+struct Seq {
+  int64_t first;       // first row of q
+  int n;               // query tokens
+  int len;             // keys
+  int begin;           // first key any row sees, rounded down to 16
+  int tiles;           // tiles of TILE keys from begin (at least 1 where n > 0)
+  int qtiles;
+};
+
+__device__ __forceinline__ Seq load_seq(const AttnParams& a, int64_t b, int rows) {
+  Seq s;
+  s.first = b;
+  int64_t n = 1;
+  bool bad = false;
+  if (a.cu_q) {
+    s.first = a.cu_q[b];
+    n = (int64_t)a.cu_q[b + 1] - s.first;
+    if (n < 0 || s.first < 0 || s.first + n > a.T) {
+      bad = true;
+      n = 0;
+    }
   }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-  for (int w = 1; w < AT / 32; ++w) v = max ? fmaxf(v, red[w]) : v + red[w];
-  return v;
+  if (n > a.max_q) {
+    bad = true;
+    n = a.max_q;
+  }
+  int64_t len = a.lens[b];
+  if (len < 0 || len > a.max_len) {
+    bad = true;
+    len = len < 0 ? 0 : a.max_len;
+  }
+  if (bad) record_error(a.status, BQ_ERR_INVALID_ARG);
+  s.n = (int)n;
+  s.len = (int)len;
+  int64_t begin = 0;
+  if (a.window > 0) {
+    begin = len - n + 1 - a.window;
+    begin = begin > 0 ? begin & ~15 : 0;
+  }
+  s.begin = (int)begin;
+  const int64_t span = len - begin;
+  s.tiles = n == 0 ? 0 : (span <= TILE ? 1 : (int)((span + TILE - 1) / TILE));
+  s.qtiles = (int)((n * a.rep + rows - 1) / rows);
+  return s;
 }
 
-__global__ void __launch_bounds__(AT) attn_kv4_kernel(AttnKv4Args a, int* status) {
-  __shared__ float qs[256], ps[AT], red[AT / 32];
-  __shared__ int64_t rows[AT];
-  const int64_t t = blockIdx.x;
-  const int h = blockIdx.y, tid = threadIdx.x;
-  const int D = a.pool.D, heads = a.pool.heads, P = a.pool.page_size, G = a.pool.group, groups = D / G;
-  const int kvh = h / (a.q_heads / heads);
-  // the token's sequence: the last b with cu_q[b] <= t
-  int64_t b = t, first = t, count = 1;
-  if (a.cu_q) {
-    int64_t lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi + 1) / 2;
-      if (a.cu_q[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    b = lo;
-    first = a.cu_q[b];
-    count = a.cu_q[b + 1] - first;
+__device__ __forceinline__ int64_t seq_cost(const AttnParams& a, const Seq& s) {
+  return (int64_t)s.tiles * s.qtiles * a.heads;
+}
+
+template <int D, int NG, int NT>
+struct Cfg {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int R = D / 2;                     // bytes of a code row
+  static constexpr int G = D / NG;
+  static constexpr int KW = G / 32;                   // key words of a lane in a group
+  static constexpr int MT = G / 16;                   // 16-dim tiles of a group
+  static constexpr int STAGES = D == 256 ? 2 : 3;
+  static constexpr int CODE_B = TILE * R;             // bytes of a tile's keys (or values)
+  static constexpr int PAR_B = TILE * 4 * NG;
+  static constexpr int STAGE_B = 2 * CODE_B + 2 * PAR_B;
+  static constexpr int RING_B = AW * STAGES * STAGE_B;
+  static constexpr int JOIN_B = AW * ROWS * (D + 4) * 4;
+  static constexpr int SMEM = RING_B > JOIN_B ? RING_B : JOIN_B;
+  static constexpr int BLOCKS = NT == 1 ? (D == 256 ? 2 : 4) : (D == 256 ? 1 : 2);   // per SM
+};
+
+// XOR of the address bits of token `tok`'s code row (row bytes D / 2), so that
+// the key loads (8 tokens of a lane row order, 16 / NG bytes each) and the
+// value loads (4 tokens, 8 lanes of 8 / NG bytes) both touch every bank once.
+template <int D>
+__device__ __forceinline__ int row_swizzle(int tok) {
+  const int b0 = tok & 1, b1 = (tok >> 1) & 1, b2 = (tok >> 2) & 1;
+  if (D == 64) return (b2 << 6) | (b2 << 5) | (b1 << 4);
+  if (D == 128) return (b2 << 6) | ((b1 ^ b2) << 5) | (b1 << 4);
+  return ((b0 ^ b2) << 6) | ((b1 ^ b2) << 5) | (b1 << 4);
+}
+
+template <int BYTES>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (BYTES == 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if constexpr (BYTES == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else if constexpr (BYTES == 4) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else {
+    w[0] = *reinterpret_cast<const uint16_t*>(p);
   }
-  if (t < first || t >= first + count) return;
-  int64_t len = a.lens[b];
-  if ((len > a.max_len || count > a.max_q) && tid == 0) record_error(status, BQ_ERR_INVALID_ARG);
-  if (t - first >= a.max_q) return;
-  const int64_t p = len - count + (t - first);
-  int64_t end = p + 1 < a.max_len ? p + 1 : a.max_len;
-  int64_t begin = a.window > 0 && p + 1 - a.window > 0 ? p + 1 - a.window : 0;
-  for (int d = tid; d < D; d += AT) qs[d] = __half2float(reinterpret_cast<const __half*>(a.q)[t * a.ld_q + h * D + d]);
-  float m = -INFINITY, l = 0.0f, acc[2] = {};
-  __syncthreads();
-  for (int64_t k0 = begin; k0 < end; k0 += AT) {
-    const int64_t key = k0 + tid;
-    float s = -INFINITY;
-    int64_t vrow = -1;
-    if (key < end) {
-      const int page = a.table[b * a.ld_table + key / P];
-      if (page >= 0 && page < a.pool.num_pages) {
-        const int64_t krow = (((int64_t)page * 2) * heads + kvh) * P + key % P;
-        vrow = krow + (int64_t)heads * P;
-        const uint8_t* c = a.pool.codes + krow * (D / 2);
-        const __half2* pr = reinterpret_cast<const __half2*>(a.pool.params) + krow * groups;
-        s = 0.0f;
-        for (int g = 0; g < groups; ++g) {
-          float u = 0.0f, qsum = 0.0f;
-          for (int j = 0; j < G / 2; ++j) {
-            const uint32_t byte = c[g * (G / 2) + j];
-            const float q0 = qs[g * G + 2 * j], q1 = qs[g * G + 2 * j + 1];
-            u += q0 * (float)(byte & 15) + q1 * (float)(byte >> 4);
-            qsum += q0 + q1;
-          }
-          s += __low2float(pr[g]) * u + __high2float(pr[g]) * qsum;
+}
+
+template <int D, int NG, int NT, bool SPLIT>
+__global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kernel(const AttnParams a) {
+  using C = Cfg<D, NG, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t scan[AW + 2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+
+  // ---- which tiles are ours ----
+  int64_t at, stop, base = 0;       // tiles [at, stop) of all units; base: the first tile of sequence b
+  int64_t b = 0;
+  Seq s;
+  int64_t total = 0;
+  if constexpr (SPLIT) {
+    // total tiles, then the sequence that holds our first tile: each thread
+    // sums the costs of a contiguous share of the sequences
+    const int64_t per = (a.B + AW * 32 - 1) / (AW * 32);
+    const int64_t b0 = min((int64_t)tid * per, a.B), b1 = min(b0 + per, a.B);
+    int64_t mine = 0;
+    for (int64_t i = b0; i < b1; ++i) mine += seq_cost(a, load_seq(a, i, C::ROWS));
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int64_t before = 0;
+#pragma unroll
+    for (int w = 0; w < AW; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    inc += before;
+    const int64_t each = total / gridDim.x, extra = total % gridDim.x;
+    at = each * blockIdx.x + min((int64_t)blockIdx.x, extra);
+    stop = at + each + (blockIdx.x < extra ? 1 : 0);
+    if (tid == 0) {
+      Meta none{};
+      a.meta[blockIdx.x] = none;
+    }
+    if (at >= stop) return;
+    if (at >= inc - mine && at < inc) {
+      int64_t sum = inc - mine;
+      int64_t i = b0;
+      for (;; ++i) {
+        const int64_t c = seq_cost(a, load_seq(a, i, C::ROWS));
+        if (at < sum + c) break;
+        sum += c;
+      }
+      scan[AW] = i;
+      scan[AW + 1] = sum;
+    }
+    __syncthreads();
+    b = scan[AW];
+    base = scan[AW + 1];
+    s = load_seq(a, b, C::ROWS);
+  } else {
+    const int64_t per_b = (int64_t)a.qtiles * a.heads;
+    b = blockIdx.x / per_b;
+    const int unit = (int)(blockIdx.x - b * per_b);
+    s = load_seq(a, b, C::ROWS);
+    if (unit >= s.qtiles * a.heads) return;
+    at = (int64_t)unit * s.tiles;
+    stop = at + s.tiles;
+  }
+  const int64_t at0 = at;
+
+  // lane row g of an MMA is key (g >> 1) + 4 (g & 1) of 16 (row g + 8: 8 more), so
+  // that the k columns 2t, 2t + 1 (+ 8) of the second MMA are keys t, t + 4 (+ 8)
+  const int ktok = (g >> 1) + 4 * (g & 1);
+  uint8_t* const ring = smem + warp * C::STAGES * C::STAGE_B;
+  const uint32_t ring_u = smem_u32(ring);
+  const int P = 1 << a.page_log2;
+  const int64_t head_b = (int64_t)P * C::R;            // bytes of one head's codes in a page
+  constexpr int PR = 4 * NG;                           // bytes of a token's params
+
+  while (at < stop) {
+    while (at >= base + seq_cost(a, s)) {              // the next sequence with work
+      base += seq_cost(a, s);
+      s = load_seq(a, ++b, C::ROWS);
+    }
+    const int unit = (int)((at - base) / s.tiles);
+    const int64_t u0 = base + (int64_t)unit * s.tiles;
+    const int first_tile = (int)(at - u0);
+    const int last_tile = (int)min((int64_t)s.tiles, stop - u0);
+    const bool whole = !SPLIT || (first_tile == 0 && last_tile == s.tiles);
+    const int qt = unit / a.heads, head = unit - qt * a.heads;
+    const int row0 = qt * C::ROWS, rows = min(C::ROWS, s.n * a.rep - row0);
+    const int ntile = last_tile - first_tile;
+    const int mytiles = ntile > warp ? (ntile - warp + AW - 1) / AW : 0;
+
+    // keys past `end` are seen by no row of this block; rows see [lo, hi]
+    const int end = min(s.len, s.len - s.n + (row0 + rows - 1) / a.rep + 1);
+    const int all_end = s.len - s.n + row0 / a.rep + 1;                 // every row sees below this
+    const int all_begin = a.window > 0 ? max((int64_t)0, (int64_t)end - a.window) : 0;   // ... and from here on
+    const int key0 = s.begin + first_tile * TILE;
+
+    // pages of this warp's next 16 tiles: lane holds the page of 16 keys
+    const int32_t* trow = a.table + b * a.ld_table;
+    auto load_page = [&](int k0) -> int {
+      const int key = key0 + (warp + AW * (k0 + (lane >> 1))) * TILE + (lane & 1) * 16;
+      int page = 0;
+      if (key < end && k0 + (lane >> 1) < mytiles) {
+        page = trow[key >> a.page_log2];
+        if (page < 0 || page >= a.num_pages) {
+          record_error(a.status, BQ_ERR_INVALID_ARG);
+          page = 0;
         }
-        s *= a.scale;
-      } else {
-        record_error(status, BQ_ERR_INVALID_ARG);
+      }
+      return page;
+    };
+    int pages = load_page(0), pages_next = load_page(16);
+
+    // ---- copy tile k of this warp into its ring ----
+    auto issue = [&](int k) {
+      if (k < mytiles) {
+        if (k > 0 && (k & 15) == 0) {
+          pages = pages_next;
+          pages_next = load_page(k + 16);
+        }
+        const int key = key0 + (warp + AW * k) * TILE;
+        const uint32_t st = ring_u + (k % C::STAGES) * C::STAGE_B;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t page = __shfl_sync(0xffffffffu, pages, 2 * (k & 15) + h);
+          const bool take = key + 16 * h < end;
+          const int off = (key + 16 * h) & (P - 1);
+          const int64_t row = (page * 2 * a.heads + head) * P + off;     // code row of the 16 keys
+          const uint8_t* kc = a.codes + row * C::R;
+          const uint8_t* vc = kc + a.heads * head_b;
+          constexpr int PER = C::R / 16;                                // 16-byte pieces of a row
+#pragma unroll
+          for (int i = 0; i < PER / 2; ++i) {
+            const int c = lane + 32 * i;
+            const int tok = 16 * h + c / PER;
+            const uint32_t dst = (uint32_t)((tok * C::R + (c % PER) * 16) ^ row_swizzle<D>(tok));
+            cp_async_16_pred(st + dst, take ? kc + c * 16 : a.codes, take);
+            cp_async_16_pred(st + C::CODE_B + dst, take ? vc + c * 16 : a.codes, take);
+          }
+          // params: 16 tokens of PR bytes, keys by the low lanes, values by the high ones
+          constexpr int PC = PR;                                        // 16-byte pieces: 16 PR / 16
+          const int c = lane & 15;
+          if (c < PC) {
+            const uint8_t* src = a.params + (row + (lane >= 16 ? (int64_t)a.heads * P : 0)) * PR + c * 16;
+            cp_async_16_pred(st + 2 * C::CODE_B + (lane >= 16 ? C::PAR_B : 0) + h * 16 * PR + c * 16,
+                             take ? src : a.params, take);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < C::STAGES - 1; ++k) issue(k);
+
+    // ---- query fragments: column g of n-tile nt is row row0 + 8 nt + g ----
+    uint32_t qf[NT][NG][C::KW][4];
+    float cf[NT][2], qs[NT][NG][2];       // for columns 2t, 2t + 1
+    int hi[NT][2], lo[NT][2];             // last and first key those rows see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g;
+      const int tok = (row0 + min(r, rows - 1)) / a.rep;
+      const int hr = (row0 + min(r, rows - 1)) - tok * a.rep;
+      const __half* qp = a.q + (s.first + tok) * a.ld_q + (int64_t)(head * a.rep + hr) * D;
+      uint4 raw[NG][C::KW];
+      float top = 0.0f, part[NG];
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        part[gr] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < C::KW; ++i) {
+          raw[gr][i] = *reinterpret_cast<const uint4*>(qp + gr * C::G + t * (C::G / 4) + 8 * i);
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[gr][i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_h2(w[e]);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            part[gr] += f.x + f.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) part[gr] += __shfl_xor_sync(0xffffffffu, part[gr], o);
+      }
+      // the row times a power of two that brings its largest value to [2**10, 2**11): exact, and the
+      // columns that meet low codes can carry the factor 16 that low and high codes differ by
+      const int e = top > 0.0f ? 10 - ilog2f(top) : 0;
+      const float f1 = pow2f(e);
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+        for (int i = 0; i < C::KW; ++i) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[gr][i]);
+          float2 d01 = unpack_h2(w[0]), d23 = unpack_h2(w[1]), d45 = unpack_h2(w[2]), d67 = unpack_h2(w[3]);
+          qf[nt][gr][i][0] = pack_h2(d01.x * f1 * 16.0f, d45.x * f1 * 16.0f);
+          qf[nt][gr][i][1] = pack_h2(d23.x * f1 * 16.0f, d67.x * f1 * 16.0f);
+          qf[nt][gr][i][2] = pack_h2(d01.y * f1, d45.y * f1);
+          qf[nt][gr][i][3] = pack_h2(d23.y * f1, d67.y * f1);
+        }
+      const float sc = a.scale * LOG2E;
+      const float c1 = sc * pow2f(20 - e);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int src = (2 * t + j) * 4;
+        cf[nt][j] = __shfl_sync(0xffffffffu, c1, src);
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) qs[nt][gr][j] = __shfl_sync(0xffffffffu, part[gr], src) * sc;
+        const int rr = row0 + min(8 * nt + 2 * t + j, rows - 1);
+        hi[nt][j] = s.len - s.n + rr / a.rep;
+        lo[nt][j] = a.window > 0 ? (int)max((int64_t)0, (int64_t)hi[nt][j] + 1 - a.window) : 0;
       }
     }
-    const float mn = fmaxf(m, block_reduce(s, true, red));
-    const float keep = mn == -INFINITY ? 1.0f : __expf(m - mn);
-    const float pe = s == -INFINITY ? 0.0f : __expf(s - mn);
-    ps[tid] = pe;
-    rows[tid] = vrow;
-    l = l * keep + block_reduce(pe, false, red);
-    m = mn;
-    for (int i = 0; i < 2; ++i) {
-      const int d = tid + i * AT;
-      if (d >= D) break;
-      acc[i] *= keep;
-      for (int j = 0; j < AT; ++j) {
-        if (rows[j] < 0) continue;
-        const uint32_t byte = a.pool.codes[rows[j] * (D / 2) + d / 2];
-        const __half2 pr = reinterpret_cast<const __half2*>(a.pool.params)[rows[j] * groups + d / G];
-        acc[i] += ps[j] * (__low2float(pr) * (float)((byte >> (4 * (d & 1))) & 15) + __high2float(pr));
+
+    float o[NT][NG][C::MT][4], lowacc[NT][NG][2], m[NT][2], l[NT][2];
+    float vf = pow2f(30);                 // power of two that the values' steps carry into fp16
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        m[nt][j] = M_NONE;
+        l[nt][j] = 0.0f;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          lowacc[nt][gr][j] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < C::MT; ++i) o[nt][gr][i][2 * j] = o[nt][gr][i][2 * j + 1] = 0.0f;
+        }
       }
+
+#pragma unroll 1
+    for (int k = 0; k < mytiles; ++k) {
+      cp_async_wait<C::STAGES - 2>();
+      __syncwarp();
+      issue(k + C::STAGES - 1);
+      const uint8_t* st = ring + (k % C::STAGES) * C::STAGE_B;
+      const int key = key0 + (warp + AW * k) * TILE;
+
+      // ---- scores (base-2 logits) ----
+      float sv[2][NT][4];
+      uint32_t vp[2][2][NG];              // (step, low) of the values, keys ktok and ktok + 8 of each half
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float acc[NT][NG][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[nt][gr][i] = 0.0f;
+        const int t0 = 16 * h + ktok, t1 = t0 + 8;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          uint32_t w0[C::KW], w1[C::KW];
+          const int off = gr * (C::G / 2) + t * (C::G / 8);
+          load_words<C::G / 8>(st + ((t0 * C::R + off) ^ row_swizzle<D>(t0)), w0);
+          load_words<C::G / 8>(st + ((t1 * C::R + off) ^ row_swizzle<D>(t1)), w1);
+#pragma unroll
+          for (int i = 0; i < C::KW; ++i) {
+            const uint32_t x0 = w0[i] >> 8, x1 = w1[i] >> 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(acc[nt][gr], w0[i] & CODE_LO, w1[i] & CODE_LO, x0 & CODE_LO, x1 & CODE_LO, qf[nt][gr][i][0],
+                      qf[nt][gr][i][1]);
+              mma_f16(acc[nt][gr], w0[i] & CODE_HI, w1[i] & CODE_HI, x0 & CODE_HI, x1 & CODE_HI, qf[nt][gr][i][2],
+                      qf[nt][gr][i][3]);
+            }
+          }
+        }
+        const uint8_t* pk = st + 2 * C::CODE_B;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          uint32_t kp[NG];
+          load_words<PR>(pk + (r ? t1 : t0) * PR, kp);
+          load_words<PR>(pk + C::PAR_B + (r ? t1 : t0) * PR, vp[h][r]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float x = 0.0f, y = 0.0f;
+#pragma unroll
+              for (int gr = 0; gr < NG; ++gr) {
+                const float2 p = unpack_h2(kp[gr]);
+                x = fmaf(p.x, acc[nt][gr][2 * r + j], x);
+                y = fmaf(p.y, qs[nt][gr][j], y);
+              }
+              sv[h][nt][2 * r + j] = fmaf(x, cf[nt][j], y);
+            }
+        }
+      }
+      // keys that some row does not see, and what lies past the last one
+      if (key < all_begin || key + TILE > all_end || key + TILE > end) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int tok = key + 16 * h + ktok + 8 * r;
+            if (tok >= end || tok < s.len - s.n + row0 / a.rep + 1 - (a.window > 0 ? a.window : (int64_t)1 << 40)) {
+#pragma unroll
+              for (int gr = 0; gr < NG; ++gr) vp[h][r][gr] = 0;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (tok > hi[nt][j] || tok < lo[nt][j] || tok >= end) sv[h][nt][2 * r + j] = -INFINITY;
+          }
+      }
+
+      // ---- running maximum, renewed only when a score passes it by 2**8 ----
+      float top[NT][2], step_top = 0.0f;
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          top[nt][j] = fmaxf(fmaxf(sv[0][nt][j], sv[0][nt][2 + j]), fmaxf(sv[1][nt][j], sv[1][nt][2 + j]));
+          over |= top[nt][j] > m[nt][j] + 8.0f;
+        }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) step_top = fmaxf(step_top, fabsf(unpack_h2(vp[h][r][gr]).x));
+      over |= step_top * vf > 240.0f;     // weight < 2**8, so the product stays below fp16's 65504
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) step_top = fmaxf(step_top, __shfl_xor_sync(0xffffffffu, step_top, x));
+        float fv = 1.0f;
+        if (step_top * vf > 240.0f) {     // step_top to [2**6, 2**7)
+          const float nv = pow2f(6 - ilog2f(step_top));
+          fv = nv / vf;
+          vf = nv;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1)
+              top[nt][j] = fmaxf(top[nt][j], __shfl_xor_sync(0xffffffffu, top[nt][j], x));
+            const float mn = fmaxf(m[nt][j], top[nt][j]);
+            const float f = ex2(m[nt][j] - mn);
+            m[nt][j] = mn;
+            l[nt][j] *= f;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+              lowacc[nt][gr][j] *= f;
+#pragma unroll
+              for (int i = 0; i < C::MT; ++i) {
+                o[nt][gr][i][j] *= f * fv;
+                o[nt][gr][i][2 + j] *= f * fv;
+              }
+            }
+          }
+      }
+
+      // ---- weights, their sums, and the second product ----
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pf[NT][NG][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float p0 = ex2(sv[h][nt][2 * r] - m[nt][0]), p1 = ex2(sv[h][nt][2 * r + 1] - m[nt][1]);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+              const float2 v = unpack_h2(vp[h][r][gr]);
+              lowacc[nt][gr][0] = fmaf(p0, v.y, lowacc[nt][gr][0]);
+              lowacc[nt][gr][1] = fmaf(p1, v.y, lowacc[nt][gr][1]);
+              const float stp = v.x * vf;
+              // the only rounding to 16 bits: weight times step, 2**-11 relative
+              pf[nt][gr][r] = movmatrix_trans(pack_h2(p0 * stp, p1 * stp));
+            }
+          }
+        const uint8_t* vs = st + C::CODE_B;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          constexpr int VB = C::G / 16;                      // bytes of a lane in a group: 8, 4 or 2
+          constexpr int VW = VB > 4 ? VB / 4 : 1;
+          uint32_t w[4][VW];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int tok = 16 * h + t + 4 * x;
+            load_words<VB>(vs + ((tok * C::R + gr * (C::G / 2) + g * VB) ^ row_swizzle<D>(tok)), w[x]);
+          }
+#pragma unroll
+          for (int i = 0; i < VW; ++i)
+#pragma unroll
+            for (int y = 0; y < (VB > 2 ? 2 : 1); ++y) {
+              // bytes 2y, 2y + 1 of keys (t, t + 4) and (t + 8, t + 12)
+              uint32_t e0 = prmt(w[0][i], w[1][i], y ? 0x7632u : 0x5410u);
+              uint32_t e1 = prmt(w[2][i], w[3][i], y ? 0x7632u : 0x5410u);
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const int mt = 4 * i + 2 * y + z;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16(o[nt][gr][mt], e0 & CODE_LO, e0 & CODE_HI, e1 & CODE_LO, e1 & CODE_HI, pf[nt][gr][0],
+                          pf[nt][gr][1]);
+                e0 >>= 8;
+                e1 >>= 8;
+              }
+            }
+        }
+      }
+    }
+
+    // ---- join the warps: accumulators in plain units through shared memory ----
+    cp_async_wait<0>();
+    __syncthreads();                      // every warp is done with its ring
+    float* const js = reinterpret_cast<float*>(smem);
+    constexpr int JS = D + 4;             // floats of a row: D values, maximum, sum, padding
+    const float back = pow2f(24) / vf;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], x);
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr)
+            lowacc[nt][gr][j] += __shfl_xor_sync(0xffffffffu, lowacc[nt][gr][j], x);
+        }
+        float* row = js + (warp * C::ROWS + 8 * nt + 2 * t + j) * JS;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+          for (int i = 0; i < C::MT; ++i) {
+            // tile i of a group: dims 2i and 2i + 1 of this lane row's G / 8
+            const int d = gr * C::G + g * (C::G / 8) + 2 * i;
+            *reinterpret_cast<float2*>(row + d) =
+                make_float2(fmaf(o[nt][gr][i][j], back, lowacc[nt][gr][j]),
+                            fmaf(o[nt][gr][i][2 + j], back * 0.0625f, lowacc[nt][gr][j]));
+          }
+        if (g == 0) {
+          row[D] = m[nt][j];
+          row[D + 1] = l[nt][j];
+        }
+      }
+    __syncthreads();
+    constexpr int LANES = D / 4;          // threads of a row, 4 dims each
+    for (int r = tid / LANES; r < rows; r += AW * 32 / LANES) {
+      const int d = (tid % LANES) * 4;
+      float mt = M_NONE;
+#pragma unroll
+      for (int w = 0; w < AW; ++w) mt = fmaxf(mt, js[(w * C::ROWS + r) * JS + D]);
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < AW; ++w) {
+        const float* row = js + (w * C::ROWS + r) * JS;
+        const float f = ex2(row[D] - mt);
+        const float4 x = *reinterpret_cast<const float4*>(row + d);
+        v.x = fmaf(f, x.x, v.x);
+        v.y = fmaf(f, x.y, v.y);
+        v.z = fmaf(f, x.z, v.z);
+        v.w = fmaf(f, x.w, v.w);
+        sum = fmaf(f, row[D + 1], sum);
+      }
+      if (whole) {
+        const int tok = (row0 + r) / a.rep, hr = row0 + r - tok * a.rep;
+        const int64_t orow = (s.first + tok) * (int64_t)(a.heads * a.rep) + head * a.rep + hr;
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        uint2 h;
+        h.x = pack_h2(v.x * inv, v.y * inv);
+        h.y = pack_h2(v.z * inv, v.w * inv);
+        *reinterpret_cast<uint2*>(a.out + orow * D + d) = h;
+        if (a.lse && d == 0) a.lse[orow] = sum > 0.0f ? (mt + log2f(sum)) * LN2 : -INFINITY;
+      } else {
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (at != at0 ? 1 : 0);
+        float* part = a.parts + (slot * C::ROWS + r) * JS;
+        *reinterpret_cast<float4*>(part + d) = v;
+        if (d == 0) {
+          part[D] = mt;
+          part[D + 1] = sum;
+        }
+      }
+    }
+    if (SPLIT && !whole && first_tile == 0 && tid == 0) {
+      // the unit goes on in the blocks whose ranges cover its last tile
+      const int64_t each = total / gridDim.x, extra = total % gridDim.x;
+      const int64_t last = u0 + s.tiles - 1;
+      const int64_t big = (each + 1) * extra;
+      const int64_t owner = last < big ? last / (each + 1) : extra + (last - big) / each;
+      Meta mm;
+      mm.parts = (int32_t)(owner - blockIdx.x + 1) | (at != at0 ? 1 << 30 : 0);
+      mm.b = (int32_t)b;
+      mm.head = head;
+      mm.qt = qt;
+      a.meta[blockIdx.x] = mm;
+    }
+    at = u0 + last_tile;
+    __syncthreads();                      // the ring is written again
+  }
+}
+
+// Joins the units that fell into several blocks' ranges: block x joins the one
+// that begins (and does not end) in block x's range.
+template <int D, int NT>
+__global__ void __launch_bounds__(128) attn_kv4_join_kernel(const AttnParams a) {
+  constexpr int ROWS = 8 * NT, JS = D + 4, LANES = D / 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Meta mm = a.meta[blockIdx.x];
+  const int n = mm.parts & 0x3fffffff;
+  if (n == 0) return;
+  const int64_t x0 = blockIdx.x;
+  const int64_t slot0 = 2 * x0 + (mm.parts >> 30 & 1);
+  const Seq s = load_seq(a, mm.b, ROWS);
+  const int row0 = mm.qt * ROWS, rows = min(ROWS, s.n * a.rep - row0);
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    auto part = [&](int i) { return a.parts + ((i == 0 ? slot0 : 2 * (x0 + i)) * ROWS + r) * JS; };
+    __shared__ float red[4], sums[128 / LANES];
+    __shared__ float4 acc[128];
+    float mt = M_NONE;
+    for (int i = threadIdx.x; i < n; i += 128) mt = fmaxf(mt, part(i)[D]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mt;
+    __syncthreads();
+    mt = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const int d = (threadIdx.x % LANES) * 4, sub = threadIdx.x / LANES;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int i = sub; i < n; i += 128 / LANES) {
+      const float* p = part(i);
+      const float f = ex2(p[D] - mt);
+      const float4 x = *reinterpret_cast<const float4*>(p + d);
+      v.x = fmaf(f, x.x, v.x);
+      v.y = fmaf(f, x.y, v.y);
+      v.z = fmaf(f, x.z, v.z);
+      v.w = fmaf(f, x.w, v.w);
+      sum = fmaf(f, p[D + 1], sum);
+    }
+    acc[threadIdx.x] = v;
+    if (d == 0) sums[sub] = sum;
+    __syncthreads();
+    if (sub == 0) {
+      sum = sums[0];
+      for (int i = 1; i < 128 / LANES; ++i) {
+        const float4 x = acc[threadIdx.x + i * LANES];
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
+        sum += sums[i];
+      }
+      const int tok = (row0 + r) / a.rep, hr = row0 + r - tok * a.rep;
+      const int64_t orow = (s.first + tok) * (int64_t)(a.heads * a.rep) + mm.head * a.rep + hr;
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      uint2 h;
+      h.x = pack_h2(v.x * inv, v.y * inv);
+      h.y = pack_h2(v.z * inv, v.w * inv);
+      *reinterpret_cast<uint2*>(a.out + orow * D + d) = h;
+      if (a.lse && d == 0) a.lse[orow] = sum > 0.0f ? (mt + log2f(sum)) * LN2 : -INFINITY;
     }
     __syncthreads();
   }
-  for (int i = 0; i < 2; ++i) {
-    const int d = tid + i * AT;
-    if (d < D)
-      reinterpret_cast<__half*>(a.out)[(t * a.q_heads + h) * D + d] = __float2half_rn(l > 0.0f ? acc[i] / l : 0.0f);
+}
+
+// 8 query rows a block where they all fit, else 16.
+inline int row_tiles(int64_t rep, int64_t max_q) { return rep * max_q <= 8 ? 1 : 2; }
+
+// Whether the tiles of all units are dealt out to a grid of resident blocks
+// (and joined), or one block takes each unit.
+inline bool split(int64_t max_len) { return max_len > DIRECT_LEN; }
+
+inline int split_grid(int64_t D, int nt) { return sm_count() * (nt == 1 ? (D == 256 ? 2 : 4) : (D == 256 ? 1 : 2)); }
+
+template <int D, int NG, int NT>
+cudaError_t launch(const AttnParams& p, const AttnKv4Args& a, cudaStream_t stream) {
+  using C = Cfg<D, NG, NT>;
+  if (!split(a.max_len)) {
+    const int64_t units = a.B * p.qtiles * p.heads;
+    if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
+    auto kern = attn_kv4_kernel<D, NG, NT, false>;
+    cudaError_t e = set_smem_once(kern, C::SMEM);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)units, AW * 32, C::SMEM, stream>>>(p);
+    return cudaGetLastError();
   }
-  if (a.lse && tid == 0) a.lse[t * a.q_heads + h] = l > 0.0f ? m + logf(l) : -INFINITY;
+  auto kern = attn_kv4_kernel<D, NG, NT, true>;
+  cudaError_t e = set_smem_once(kern, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int grid = split_grid(D, NT);
+  kern<<<grid, AW * 32, C::SMEM, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, C::ROWS);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_kv4_join_kernel<D, NT>, p);
+}
+
+template <int D, int NG>
+cudaError_t launch_nt(const AttnParams& p, const AttnKv4Args& a, cudaStream_t stream) {
+  return row_tiles(p.rep, a.max_q) == 1 ? launch<D, NG, 1>(p, a, stream) : launch<D, NG, 2>(p, a, stream);
 }
 
 }  // namespace
 
-size_t attn_kv4_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t attn_kv4_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_len) {
+  if (!split(max_len)) return 0;
+  const int nt = row_tiles(q_heads / kv_heads, max_q);
+  const size_t grid = (size_t)split_grid(D, nt);
+  return grid * sizeof(Meta) + 2 * grid * 8 * nt * (D + 4) * sizeof(float);
+}
 
 cudaError_t launch_attn_kv4(const AttnKv4Args& a, cudaStream_t stream) {
-  int* status = nullptr;
-  cudaError_t e = device_status_ptr(&status);
+  AttnParams p{};
+  cudaError_t e = device_status_ptr(&p.status);
   if (e != cudaSuccess) return e;
-  attn_kv4_kernel<<<dim3((unsigned)a.T, (unsigned)a.q_heads), AT, 0, stream>>>(a, status);
-  return cudaGetLastError();
+  p.q = reinterpret_cast<const __half*>(a.q);
+  p.ld_q = a.ld_q;
+  p.T = a.T;
+  p.codes = a.pool.codes;
+  p.params = reinterpret_cast<const uint8_t*>(a.pool.params);
+  if (a.max_len == 0) {   // nothing is read, but the (empty) copies name an address
+    p.codes = reinterpret_cast<const uint8_t*>(a.q);
+    p.params = p.codes;
+  }
+  p.num_pages = a.pool.num_pages;
+  p.page_log2 = __builtin_ctz((unsigned)a.pool.page_size);
+  p.heads = a.pool.heads;
+  p.rep = a.q_heads / a.pool.heads;
+  p.table = a.table;
+  p.ld_table = a.ld_table;
+  p.lens = a.lens;
+  p.cu_q = a.cu_q;
+  p.B = a.B;
+  p.max_q = a.max_q;
+  p.max_len = a.max_len;
+  p.window = a.window;
+  const int rows = 8 * row_tiles(p.rep, a.max_q);
+  p.qtiles = (int)((a.max_q * p.rep + rows - 1) / rows);
+  p.scale = a.scale;
+  p.out = reinterpret_cast<__half*>(a.out);
+  p.lse = a.lse;
+  if (split(a.max_len)) {
+    const size_t grid = (size_t)split_grid(a.pool.D, rows / 8);
+    p.meta = static_cast<Meta*>(a.workspace);
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + grid * sizeof(Meta));
+  }
+  const int D = a.pool.D, ng = D / a.pool.group;
+  if (D == 64) return ng == 1 ? launch_nt<64, 1>(p, a, stream) : launch_nt<64, 2>(p, a, stream);
+  if (D == 128) {
+    if (ng == 1) return launch_nt<128, 1>(p, a, stream);
+    return ng == 2 ? launch_nt<128, 2>(p, a, stream) : launch_nt<128, 4>(p, a, stream);
+  }
+  return ng == 2 ? launch_nt<256, 2>(p, a, stream) : launch_nt<256, 4>(p, a, stream);
 }
 
 }  // namespace bq

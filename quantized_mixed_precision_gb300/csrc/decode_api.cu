@@ -10,6 +10,7 @@ using namespace bq;
 
 constexpr int64_t MAX_ROWS = 1LL << 24;
 constexpr int64_t MAX_HEADS = 65536;
+constexpr int64_t MAX_LEN = 1LL << 30;   // keys of a sequence
 
 inline bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 inline bool aligned16(const void* p) { return aligned(p, 16); }
@@ -101,7 +102,7 @@ bq_status bq_qk_norm_rope_kv4(const uint16_t* q, int64_t ld_q, const uint16_t* k
 size_t bq_attn_kv4_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q,
                              int64_t max_len) {
   if (B < 1 || kv_heads < 1 || q_heads < 1 || D < 1 || max_q < 1 || max_len < 0 || q_heads % kv_heads != 0) return 0;
-  if (B > MAX_ROWS || q_heads > MAX_HEADS || D > 256 || max_q > MAX_ROWS || max_len >= (1LL << 31)) return 0;
+  if (B > MAX_ROWS || q_heads > MAX_HEADS || D > 256 || max_q > MAX_ROWS || max_len > MAX_LEN) return 0;
   return attn_kv4_workspace(B, q_heads, kv_heads, D, max_q, max_len);
 }
 
@@ -116,8 +117,9 @@ bq_status bq_attn_kv4(const uint16_t* q, int64_t ld_q, int64_t T, int64_t q_head
   if (q_heads % kv_heads != 0 || !(scale == scale)) return BQ_ERR_INVALID_ARG;
   if (T == 0 || B == 0) return BQ_OK;
   if (max_q < 1 || (!cu_q && T != B)) return BQ_ERR_INVALID_ARG;
-  if (!q || !out || !seq_lens || (max_len > 0 && (!codes || !params || !block_table))) return BQ_ERR_INVALID_ARG;
-  if (q_heads > MAX_HEADS || T > MAX_ROWS || B > MAX_ROWS || max_q > MAX_ROWS || max_len >= (1LL << 31))
+  if (!q || !out || !seq_lens || (max_len > 0 && (!codes || !params || !block_table || num_pages < 1)))
+    return BQ_ERR_INVALID_ARG;
+  if (q_heads > MAX_HEADS || T > MAX_ROWS || B > MAX_ROWS || max_q > MAX_ROWS || max_len > MAX_LEN)
     return BQ_ERR_UNSUPPORTED;
   if (!valid_pool(D, group, page_size, num_pages)) return BQ_ERR_UNSUPPORTED;
   if (ld_q < q_heads * D || max_len > ld_table * page_size) return BQ_ERR_INVALID_ARG;

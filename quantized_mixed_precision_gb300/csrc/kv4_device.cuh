@@ -1,0 +1,74 @@
+// Device helpers of the 4-bit cache kernels: mma.sync, movmatrix, the base-2
+// exponential, and the meaning of 4-bit codes as fp16 subnormals.
+//
+// A masked word w & 0x000f000f holds two codes u in the low bits of two fp16
+// fields, i.e. the fp16 subnormals u * 2**-24, exactly; w & 0x00f000f0 holds
+// u * 2**-20.  Tensor cores take subnormals as they are, so one LOP3 turns two
+// codes into an exact MMA operand, with no arithmetic; the factor 2**24 (or
+// 2**20) returns in the fp32 scale that follows the sum.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "bq_device.cuh"
+
+namespace bq {
+
+constexpr uint32_t CODE_LO = 0x000f000fu;   // codes worth u * 2**-24
+constexpr uint32_t CODE_HI = 0x00f000f0u;   // codes worth u * 2**-20
+
+// D (16 x 8, fp32) += A (16 x 16) * B (16 x 8), fp16.  With g = lane / 4 and
+// t = lane % 4: a0, a1 hold rows g, g + 8 at k = 2t, 2t + 1, a2, a3 the same
+// rows at k + 8; b0, b1 hold k = 2t, 2t + 1 (+ 8) of column g; d holds
+// columns 2t, 2t + 1 of rows g and g + 8.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values, one row pair per register.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// 2**x (2 ulp; exact 0 at -inf)
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 unpack_h2(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// 2**e as fp32, for e in [-126, 127]
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+// floor(log2(|x|)) of a positive normal fp32 number
+__device__ __forceinline__ int ilog2f(float x) { return ((__float_as_int(x) >> 23) & 255) - 127; }
+
+__device__ __forceinline__ void cp_async_16_pred(uint32_t smem_dst, const void* gmem_src, bool take) {
+  const int bytes = take ? 16 : 0;   // 0: the destination is filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gmem_src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+}  // namespace bq
