@@ -8,11 +8,11 @@
 // need one LOP3 per two codes and no arithmetic (kv4_device.cuh).
 //
 // The keys are the rows of the first product's A operand and the dims the
-// rows of the second one's, so 8 query rows (the heads that share a kv head,
-// times the query tokens) are its 8 columns and none of an MMA is idle at
-// q_heads / kv_heads = 8.  Scores leave the first MMA with a key per lane
-// row, where its step and low are applied, and movmatrix turns the weights
-// into the second MMA's B operand.
+// rows of the second one's (ldmatrix transposes their bytes), so 8 query rows
+// (the heads that share a kv head, times the query tokens) are its 8 columns
+// and none of an MMA is idle at q_heads / kv_heads = 8.  Scores leave the
+// first MMA with a key per lane row, where its step and low are applied, and
+// movmatrix turns the weights into the second MMA's B operand.
 //
 // Work is split over warps by tiles of 32 keys.  A unit is one (sequence,
 // kv head, block of query rows); the blocks of the grid take equal contiguous
@@ -120,6 +120,7 @@ struct Cfg {
   static constexpr int G = D / NG;
   static constexpr int KW = G / 32;                   // key words of a lane in a group
   static constexpr int MT = G / 16;                   // 16-dim tiles of a group
+  static constexpr int PER = R / 16;                  // 16-byte pieces of a code row
   static constexpr int STAGES = D == 256 ? 2 : 3;
   static constexpr int CODE_B = TILE * R;             // bytes of a tile's keys (or values)
   static constexpr int PAR_B = TILE * 4 * NG;
@@ -130,15 +131,20 @@ struct Cfg {
   static constexpr int BLOCKS = NT == 1 ? (D == 256 ? 2 : 4) : (D == 256 ? 1 : 2);   // per SM
 };
 
-// XOR of the address bits of token `tok`'s code row (row bytes D / 2), so that
-// the key loads (8 tokens of a lane row order, 16 / NG bytes each) and the
-// value loads (4 tokens, 8 lanes of 8 / NG bytes) both touch every bank once.
+// XOR of the address bits of token `tok`'s row of key codes, so that the key
+// loads (tokens 2g or 2g + 1, 16 / NG bytes of each quad lane) touch every bank
+// once, and of its row of value codes for ldmatrix (8 consecutive tokens, 16
+// bytes each).  Rows are D / 2 bytes apart.
 template <int D>
-__device__ __forceinline__ int row_swizzle(int tok) {
-  const int b0 = tok & 1, b1 = (tok >> 1) & 1, b2 = (tok >> 2) & 1;
-  if (D == 64) return (b2 << 6) | (b2 << 5) | (b1 << 4);
-  if (D == 128) return (b2 << 6) | ((b1 ^ b2) << 5) | (b1 << 4);
-  return ((b0 ^ b2) << 6) | ((b1 ^ b2) << 5) | (b1 << 4);
+__device__ __forceinline__ constexpr int key_swizzle(int tok) {
+  const int b1 = (tok >> 1) & 1, b2 = (tok >> 2) & 1, b3 = (tok >> 3) & 1;
+  return (D == 64 ? 0 : b1 << 6) | (b2 << 5) | (b3 << 4);
+}
+template <int D>
+__device__ __forceinline__ constexpr int value_swizzle(int tok) {
+  if (D == 64) return ((tok >> 2) & 1) << 4;
+  if (D == 128) return ((tok >> 1) & 3) << 4;
+  return (tok & 7) << 4;
 }
 
 template <int BYTES>
@@ -149,10 +155,25 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   } else if constexpr (BYTES == 8) {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
     w[0] = v.x; w[1] = v.y;
-  } else if constexpr (BYTES == 4) {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else {
-    w[0] = *reinterpret_cast<const uint16_t*>(p);
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+// The params of two consecutive tokens
+template <int NG>
+__device__ __forceinline__ void load_pair(const uint8_t* p, uint32_t (&w)[2][NG]) {
+  if constexpr (NG == 4) {
+    load_words<16>(p, w[0]);
+    load_words<16>(p + 16, w[1]);
+  } else {
+    uint32_t v[2 * NG];
+    load_words<8 * NG>(p, v);
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      w[0][i] = v[i];
+      w[1][i] = v[NG + i];
+    }
   }
 }
 
@@ -225,14 +246,23 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
   }
   const int64_t at0 = at;
 
-  // lane row g of an MMA is key (g >> 1) + 4 (g & 1) of 16 (row g + 8: 8 more), so
-  // that the k columns 2t, 2t + 1 (+ 8) of the second MMA are keys t, t + 4 (+ 8)
-  const int ktok = (g >> 1) + 4 * (g & 1);
-  uint8_t* const ring = smem + warp * C::STAGES * C::STAGE_B;
-  const uint32_t ring_u = smem_u32(ring);
+  // Rows g and g + 8 of a first MMA are keys 2g and 2g + 1 of its 16, so that the
+  // k columns 2t, 2t + 1 and 2t + 8, 2t + 9 of the second one are keys 4t, 4t + 2
+  // and 4t + 1, 4t + 3: the bytes 0, 2 and 1, 3 that ldmatrix hands out.
+  const uint32_t ring = smem_u32(smem) + warp * C::STAGES * C::STAGE_B;
   const int P = 1 << a.page_log2;
-  const int64_t head_b = (int64_t)P * C::R;            // bytes of one head's codes in a page
   constexpr int PR = 4 * NG;                           // bytes of a token's params
+  const uint32_t page_codes = 2u * a.heads * P * C::R, page_params = 2u * a.heads * P * PR;
+  const uint32_t v_codes = (uint32_t)a.heads * P * C::R;   // from a key row to its value row
+  // this lane's share of a copy of 16 keys: piece `lane` (+ 32 i) of their codes, and a piece of their params
+  const int cp_tok = lane / C::PER;
+  const uint32_t cp_lin = cp_tok * C::R + (lane % C::PER) * 16;
+  const int pp = lane & 15;                            // params piece; keys by the low lanes, values by the high ones
+  const uint32_t pp_dst = 2 * C::CODE_B + (lane >= 16 ? C::PAR_B : 0) + pp * 16;
+  const uint32_t pp_src = (lane >= 16 ? (uint32_t)a.heads * P * PR : 0u) + pp * 16;
+  // this lane's loads: key words of tokens 2g and 2g + 1 (group 0), rows of the values' matrices
+  const uint32_t k_at0 = ((2 * g) * C::R + t * (C::G / 8)) ^ key_swizzle<D>(2 * g);
+  const uint32_t v_at = C::CODE_B + (((lane & 15) * C::R + (lane >> 4) * 16) ^ value_swizzle<D>(lane & 15));
 
   while (at < stop) {
     while (at >= base + seq_cost(a, s)) {              // the next sequence with work
@@ -253,6 +283,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
     const int end = min(s.len, s.len - s.n + (row0 + rows - 1) / a.rep + 1);
     const int all_end = s.len - s.n + row0 / a.rep + 1;                 // every row sees below this
     const int all_begin = a.window > 0 ? max((int64_t)0, (int64_t)end - a.window) : 0;   // ... and from here on
+    const int first_seen = a.window > 0 ? (int)max((int64_t)0, (int64_t)all_end - a.window) : 0;
     const int key0 = s.begin + first_tile * TILE;
 
     // pages of this warp's next 16 tiles: lane holds the page of 16 keys
@@ -272,6 +303,10 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
     int pages = load_page(0), pages_next = load_page(16);
 
     // ---- copy tile k of this warp into its ring ----
+    // (keys from `end` on are not copied: what the ring holds there is masked)
+    const uint8_t* const unit_codes = a.codes + (int64_t)head * P * C::R + lane * 16;
+    const uint8_t* const unit_params = a.params + (int64_t)head * P * PR + pp_src;
+    uint32_t put = ring;                               // stage that the next copy fills
     auto issue = [&](int k) {
       if (k < mytiles) {
         if (k > 0 && (k & 15) == 0) {
@@ -279,35 +314,26 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
           pages_next = load_page(k + 16);
         }
         const int key = key0 + (warp + AW * k) * TILE;
-        const uint32_t st = ring_u + (k % C::STAGES) * C::STAGE_B;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int64_t page = __shfl_sync(0xffffffffu, pages, 2 * (k & 15) + h);
-          const bool take = key + 16 * h < end;
-          const int off = (key + 16 * h) & (P - 1);
-          const int64_t row = (page * 2 * a.heads + head) * P + off;     // code row of the 16 keys
-          const uint8_t* kc = a.codes + row * C::R;
-          const uint8_t* vc = kc + a.heads * head_b;
-          constexpr int PER = C::R / 16;                                // 16-byte pieces of a row
+          const uint32_t page = __shfl_sync(0xffffffffu, pages, 2 * (k & 15) + h);
+          if (key + 16 * h < end) {
+            const uint32_t off = (key + 16 * h) & (P - 1);
+            const uint8_t* kc = unit_codes + (uint64_t)page * page_codes + off * C::R;
+            const uint8_t* vc = kc + v_codes;
 #pragma unroll
-          for (int i = 0; i < PER / 2; ++i) {
-            const int c = lane + 32 * i;
-            const int tok = 16 * h + c / PER;
-            const uint32_t dst = (uint32_t)((tok * C::R + (c % PER) * 16) ^ row_swizzle<D>(tok));
-            cp_async_16_pred(st + dst, take ? kc + c * 16 : a.codes, take);
-            cp_async_16_pred(st + C::CODE_B + dst, take ? vc + c * 16 : a.codes, take);
-          }
-          // params: 16 tokens of PR bytes, keys by the low lanes, values by the high ones
-          constexpr int PC = PR;                                        // 16-byte pieces: 16 PR / 16
-          const int c = lane & 15;
-          if (c < PC) {
-            const uint8_t* src = a.params + (row + (lane >= 16 ? (int64_t)a.heads * P : 0)) * PR + c * 16;
-            cp_async_16_pred(st + 2 * C::CODE_B + (lane >= 16 ? C::PAR_B : 0) + h * 16 * PR + c * 16,
-                             take ? src : a.params, take);
+            for (int i = 0; i < C::PER / 2; ++i) {
+              constexpr int STEP = 32 / C::PER;        // tokens of one copy of the warp
+              const uint32_t lin = cp_lin + (16 * h + i * STEP) * C::R;
+              cp_async_16_u(put + (lin ^ key_swizzle<D>(cp_tok + i * STEP)), kc + i * 512);
+              cp_async_16_u(put + C::CODE_B + (lin ^ value_swizzle<D>(cp_tok + i * STEP)), vc + i * 512);
+            }
+            if (pp < PR) cp_async_16_u(put + pp_dst + h * 16 * PR, unit_params + (uint64_t)page * page_params + off * PR);
           }
         }
       }
       cp_async_commit();
+      put = put == ring + (C::STAGES - 1) * C::STAGE_B ? ring : put + C::STAGE_B;
     };
 #pragma unroll
     for (int k = 0; k < C::STAGES - 1; ++k) issue(k);
@@ -380,7 +406,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        m[nt][j] = M_NONE;
+        m[nt][j] = 0.0f;
         l[nt][j] = 0.0f;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
@@ -390,17 +416,22 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
         }
       }
 
+    // Columns that have seen a key have a running maximum m; the others hold 0
+    // there, and while there are any (`fresh`) every tile renews the maxima.
+    bool fresh = true;
+    uint32_t seen = 0;
+    uint32_t st = ring;
 #pragma unroll 1
     for (int k = 0; k < mytiles; ++k) {
       cp_async_wait<C::STAGES - 2>();
       __syncwarp();
       issue(k + C::STAGES - 1);
-      const uint8_t* st = ring + (k % C::STAGES) * C::STAGE_B;
+      const uint8_t* sp = smem + (st - smem_u32(smem));
       const int key = key0 + (warp + AW * k) * TILE;
 
-      // ---- scores (base-2 logits) ----
+      // ---- scores: base-2 logits less the running maximum ----
       float sv[2][NT][4];
-      uint32_t vp[2][2][NG];              // (step, low) of the values, keys ktok and ktok + 8 of each half
+      uint32_t vp[2][2][NG];              // (step, low) of the values, keys 2g and 2g + 1 of each half
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float acc[NT][NG][4];
@@ -410,13 +441,16 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
           for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[nt][gr][i] = 0.0f;
-        const int t0 = 16 * h + ktok, t1 = t0 + 8;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
           uint32_t w0[C::KW], w1[C::KW];
-          const int off = gr * (C::G / 2) + t * (C::G / 8);
-          load_words<C::G / 8>(st + ((t0 * C::R + off) ^ row_swizzle<D>(t0)), w0);
-          load_words<C::G / 8>(st + ((t1 * C::R + off) ^ row_swizzle<D>(t1)), w1);
+          const uint8_t* kw = sp + (k_at0 ^ (gr * (C::G / 2))) + 16 * h * C::R;
+          load_words<C::G / 8>(kw, w0);
+          // token 2g + 1: the next row, in the same 128-byte line (or the next line) with the same swizzle
+          load_words<C::G / 8>(C::R == 64 ? sp + (k_at0 ^ (gr * (C::G / 2)) ^ 64) + 16 * h * C::R
+                                          : (C::R == 32 ? sp + (k_at0 ^ (gr * (C::G / 2)) ^ 32) + 16 * h * C::R
+                                                        : kw + C::R),
+                               w1);
 #pragma unroll
           for (int i = 0; i < C::KW; ++i) {
             const uint32_t x0 = w0[i] >> 8, x1 = w1[i] >> 8;
@@ -429,35 +463,34 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
             }
           }
         }
-        const uint8_t* pk = st + 2 * C::CODE_B;
+        uint32_t kp[2][NG];
+        const uint8_t* pk = sp + 2 * C::CODE_B + (16 * h + 2 * g) * PR;
+        load_pair<NG>(pk, kp);
+        load_pair<NG>(pk + C::PAR_B, vp[h]);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          uint32_t kp[NG];
-          load_words<PR>(pk + (r ? t1 : t0) * PR, kp);
-          load_words<PR>(pk + C::PAR_B + (r ? t1 : t0) * PR, vp[h][r]);
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float x = 0.0f, y = 0.0f;
+              float x = 0.0f, y = -m[nt][j];
 #pragma unroll
               for (int gr = 0; gr < NG; ++gr) {
-                const float2 p = unpack_h2(kp[gr]);
-                x = fmaf(p.x, acc[nt][gr][2 * r + j], x);
+                const float2 p = unpack_h2(kp[r][gr]);
+                x = gr == 0 ? p.x * acc[nt][gr][2 * r + j] : fmaf(p.x, acc[nt][gr][2 * r + j], x);
                 y = fmaf(p.y, qs[nt][gr][j], y);
               }
               sv[h][nt][2 * r + j] = fmaf(x, cf[nt][j], y);
             }
-        }
       }
       // keys that some row does not see, and what lies past the last one
-      if (key < all_begin || key + TILE > all_end || key + TILE > end) {
+      if (key < all_begin || key + TILE > all_end) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const int tok = key + 16 * h + ktok + 8 * r;
-            if (tok >= end || tok < s.len - s.n + row0 / a.rep + 1 - (a.window > 0 ? a.window : (int64_t)1 << 40)) {
+            const int tok = key + 16 * h + 2 * g + r;
+            if (tok >= end || tok < first_seen) {
 #pragma unroll
               for (int gr = 0; gr < NG; ++gr) vp[h][r][gr] = 0;
             }
@@ -465,19 +498,18 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                if (tok > hi[nt][j] || tok < lo[nt][j] || tok >= end) sv[h][nt][2 * r + j] = -INFINITY;
+                if (tok > hi[nt][j] || tok < lo[nt][j]) sv[h][nt][2 * r + j] = -INFINITY;
           }
       }
 
       // ---- running maximum, renewed only when a score passes it by 2**8 ----
-      float top[NT][2], step_top = 0.0f;
-      bool over = false;
+      float top[NT][2], step_top = 0.0f, most = -INFINITY;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           top[nt][j] = fmaxf(fmaxf(sv[0][nt][j], sv[0][nt][2 + j]), fmaxf(sv[1][nt][j], sv[1][nt][2 + j]));
-          over |= top[nt][j] > m[nt][j] + 8.0f;
+          most = fmaxf(most, top[nt][j]);
         }
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -485,8 +517,8 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) step_top = fmaxf(step_top, fabsf(unpack_h2(vp[h][r][gr]).x));
-      over |= step_top * vf > 240.0f;     // weight < 2**8, so the product stays below fp16's 65504
-      if (__any_sync(0xffffffffu, over)) {
+      // (weight < 2**8, so weight * step * vf stays below fp16's 65504 while step * vf <= 240)
+      if (__any_sync(0xffffffffu, fresh || most > 8.0f || step_top * vf > 240.0f)) {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) step_top = fmaxf(step_top, __shfl_xor_sync(0xffffffffu, step_top, x));
         float fv = 1.0f;
@@ -495,6 +527,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
           fv = nv / vf;
           vf = nv;
         }
+        bool all = true;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -502,9 +535,18 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1)
               top[nt][j] = fmaxf(top[nt][j], __shfl_xor_sync(0xffffffffu, top[nt][j], x));
-            const float mn = fmaxf(m[nt][j], top[nt][j]);
-            const float f = ex2(m[nt][j] - mn);
-            m[nt][j] = mn;
+            const uint32_t bit = 1u << (2 * nt + j);
+            // a first maximum may lie below 0; later ones only rise
+            float up = seen & bit ? fmaxf(top[nt][j], 0.0f) : (top[nt][j] == -INFINITY ? 0.0f : top[nt][j]);
+            if (top[nt][j] != -INFINITY) seen |= bit;
+            all = all && (seen & bit);
+            m[nt][j] += up;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              sv[h][nt][j] -= up;
+              sv[h][nt][2 + j] -= up;
+            }
+            const float f = ex2(fminf(-up, 0.0f));   // (nothing has been summed where up < 0)
             l[nt][j] *= f;
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
@@ -516,6 +558,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
               }
             }
           }
+        fresh = !__all_sync(0xffffffffu, all);
       }
 
       // ---- weights, their sums, and the second product ----
@@ -523,53 +566,45 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
       for (int h = 0; h < 2; ++h) {
         uint32_t pf[NT][NG][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int r = 0; r < 2; ++r) {
+          float vs[NG], vl[NG];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float p0 = ex2(sv[h][nt][2 * r] - m[nt][0]), p1 = ex2(sv[h][nt][2 * r + 1] - m[nt][1]);
+          for (int gr = 0; gr < NG; ++gr) {
+            const float2 v = unpack_h2(vp[h][r][gr]);
+            vs[gr] = v.x * vf;
+            vl[gr] = v.y;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float p0 = ex2(sv[h][nt][2 * r]), p1 = ex2(sv[h][nt][2 * r + 1]);
             l[nt][0] += p0;
             l[nt][1] += p1;
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-              const float2 v = unpack_h2(vp[h][r][gr]);
-              lowacc[nt][gr][0] = fmaf(p0, v.y, lowacc[nt][gr][0]);
-              lowacc[nt][gr][1] = fmaf(p1, v.y, lowacc[nt][gr][1]);
-              const float stp = v.x * vf;
+              lowacc[nt][gr][0] = fmaf(p0, vl[gr], lowacc[nt][gr][0]);
+              lowacc[nt][gr][1] = fmaf(p1, vl[gr], lowacc[nt][gr][1]);
               // the only rounding to 16 bits: weight times step, 2**-11 relative
-              pf[nt][gr][r] = movmatrix_trans(pack_h2(p0 * stp, p1 * stp));
+              pf[nt][gr][r] = movmatrix_trans(pack_h2(p0 * vs[gr], p1 * vs[gr]));
             }
           }
-        const uint8_t* vs = st + C::CODE_B;
+        }
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          constexpr int VB = C::G / 16;                      // bytes of a lane in a group: 8, 4 or 2
-          constexpr int VW = VB > 4 ? VB / 4 : 1;
-          uint32_t w[4][VW];
+        for (int c = 0; c < C::PER; c += 2) {
+          // 16-byte pieces c and c + 1 (32 dims each) of 16 tokens
+          uint32_t w[4];
+          ldmatrix_b8_trans_x2(st + (v_at ^ (c * 16)) + 16 * h * C::R, w);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int tok = 16 * h + t + 4 * x;
-            load_words<VB>(vs + ((tok * C::R + gr * (C::G / 2) + g * VB) ^ row_swizzle<D>(tok)), w[x]);
+            const int gr = (c + x / 2) * 32 / C::G, i = ((c + x / 2) * 32 % C::G) / 16 + (x & 1);
+            const uint32_t e = w[x] >> 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(o[nt][gr][i], w[x] & CODE_LO, w[x] & CODE_HI, e & CODE_LO, e & CODE_HI, pf[nt][gr][0],
+                      pf[nt][gr][1]);
           }
-#pragma unroll
-          for (int i = 0; i < VW; ++i)
-#pragma unroll
-            for (int y = 0; y < (VB > 2 ? 2 : 1); ++y) {
-              // bytes 2y, 2y + 1 of keys (t, t + 4) and (t + 8, t + 12)
-              uint32_t e0 = prmt(w[0][i], w[1][i], y ? 0x7632u : 0x5410u);
-              uint32_t e1 = prmt(w[2][i], w[3][i], y ? 0x7632u : 0x5410u);
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const int mt = 4 * i + 2 * y + z;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma_f16(o[nt][gr][mt], e0 & CODE_LO, e0 & CODE_HI, e1 & CODE_LO, e1 & CODE_HI, pf[nt][gr][0],
-                          pf[nt][gr][1]);
-                e0 >>= 8;
-                e1 >>= 8;
-              }
-            }
         }
       }
+      st = st == ring + (C::STAGES - 1) * C::STAGE_B ? ring : st + C::STAGE_B;
     }
 
     // ---- join the warps: accumulators in plain units through shared memory ----
@@ -594,14 +629,14 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
         for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
           for (int i = 0; i < C::MT; ++i) {
-            // tile i of a group: dims 2i and 2i + 1 of this lane row's G / 8
-            const int d = gr * C::G + g * (C::G / 8) + 2 * i;
+            // tile i of a group: byte g of its i-th 8, dims 2g and 2g + 1
+            const int d = gr * C::G + 16 * i + 2 * g;
             *reinterpret_cast<float2*>(row + d) =
                 make_float2(fmaf(o[nt][gr][i][j], back, lowacc[nt][gr][j]),
                             fmaf(o[nt][gr][i][2 + j], back * 0.0625f, lowacc[nt][gr][j]));
           }
         if (g == 0) {
-          row[D] = m[nt][j];
+          row[D] = l[nt][j] > 0.0f ? m[nt][j] : M_NONE;
           row[D + 1] = l[nt][j];
         }
       }

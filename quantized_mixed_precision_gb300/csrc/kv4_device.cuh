@@ -59,9 +59,19 @@ __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) 
 // floor(log2(|x|)) of a positive normal fp32 number
 __device__ __forceinline__ int ilog2f(float x) { return ((__float_as_int(x) >> 23) & 255) - 127; }
 
-__device__ __forceinline__ void cp_async_16_pred(uint32_t smem_dst, const void* gmem_src, bool take) {
-  const int bytes = take ? 16 : 0;   // 0: the destination is filled with zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gmem_src), "r"(bytes) : "memory");
+// Two 16 x 16 byte matrices, transposed: lanes 0..15 give the rows of the
+// first, lanes 16..31 those of the second (16 bytes each); r[2 i] and r[2 i + 1]
+// hold rows 4t .. 4t + 3 of columns g and g + 8 of matrix i.
+__device__ __forceinline__ void ldmatrix_b8_trans_x2(uint32_t saddr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+
+// 16-byte asynchronous copy to a shared-memory address
+__device__ __forceinline__ void cp_async_16_u(uint32_t smem_dst, const void* gmem_src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gmem_src) : "memory");
 }
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
