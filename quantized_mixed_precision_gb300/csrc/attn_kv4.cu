@@ -113,6 +113,8 @@ __device__ __forceinline__ int64_t seq_cost(const AttnParams& a, const Seq& s) {
   return (int64_t)s.tiles * s.qtiles * a.heads;
 }
 
+constexpr int blocks_per_sm(int D, int nt) { return nt == 1 ? (D == 256 ? 2 : 3) : (D == 256 ? 1 : 2); }
+
 template <int D, int NG, int NT>
 struct Cfg {
   static constexpr int ROWS = 8 * NT;
@@ -121,14 +123,16 @@ struct Cfg {
   static constexpr int KW = G / 32;                   // key words of a lane in a group
   static constexpr int MT = G / 16;                   // 16-dim tiles of a group
   static constexpr int PER = R / 16;                  // 16-byte pieces of a code row
-  static constexpr int STAGES = D == 256 ? 2 : 3;
+  static constexpr int STAGES = 2;   // 3 or 4 stages a warp read 1-2 % slower
   static constexpr int CODE_B = TILE * R;             // bytes of a tile's keys (or values)
   static constexpr int PAR_B = TILE * 4 * NG;
   static constexpr int STAGE_B = 2 * CODE_B + 2 * PAR_B;
   static constexpr int RING_B = AW * STAGES * STAGE_B;
   static constexpr int JOIN_B = AW * ROWS * (D + 4) * 4;
   static constexpr int SMEM = RING_B > JOIN_B ? RING_B : JOIN_B;
-  static constexpr int BLOCKS = NT == 1 ? (D == 256 ? 2 : 4) : (D == 256 ? 1 : 2);   // per SM
+  // Blocks per SM: what the registers allow without spills.  With D = 128, 3 blocks (168 registers a thread)
+  // take 133 us for 739 MB of cache, 4 blocks (128 registers) 147 us, 2 blocks 138 us.
+  static constexpr int BLOCKS = blocks_per_sm(D, NT);
 };
 
 // XOR of the address bits of token `tok`'s row of key codes, so that the key
@@ -768,7 +772,7 @@ inline int row_tiles(int64_t rep, int64_t max_q) { return rep * max_q <= 8 ? 1 :
 // (and joined), or one block takes each unit.
 inline bool split(int64_t max_len) { return max_len > DIRECT_LEN; }
 
-inline int split_grid(int64_t D, int nt) { return sm_count() * (nt == 1 ? (D == 256 ? 2 : 4) : (D == 256 ? 1 : 2)); }
+inline int split_grid(int64_t D, int nt) { return sm_count() * blocks_per_sm((int)D, nt); }
 
 template <int D, int NG, int NT>
 cudaError_t launch(const AttnParams& p, const AttnKv4Args& a, cudaStream_t stream) {
