@@ -1,4 +1,5 @@
-"""Builds libbq.so in-tree from csrc/*.cu for sm_103a (nvcc, no cmake).
+"""Builds libbq.so in-tree from csrc/*.cu for sm_103a (nvcc, no cmake), and the
+native form of the decoder-layer binding from csrc/decode_binding.cpp (g++).
 
 Translation units compile in parallel; the CUDA runtime is linked statically
 so the library loads on a machine without a GPU (for symbol checks) as well
@@ -19,6 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbq.so")
+BINDING = os.path.join(PKG, "_decode_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -41,14 +43,36 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    """Compiles against this interpreter's Python and torch headers and links with its torch libraries."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    home = os.path.dirname(nvcc()).removesuffix("bin")
+    include = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(home, "include"),
+               *cpp_extension.include_paths()]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[x for d in include for x in ("-isystem", d)], os.path.join(CSRC, "decode_binding.cpp"), "-o", tmp,
+           "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for decode_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     extra = list(extra or [])
     if verbose:
         extra += ["-Xptxas", "-v"]
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        binding.result()
     tmp = LIB + ".tmp"
     r = subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:

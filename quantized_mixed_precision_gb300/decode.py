@@ -40,6 +40,10 @@ class _Bound:
         self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.gemm, self.write, self.attn = lib.bq_gemm_f16xi4_group, lib.bq_qk_norm_rope_kv4, lib.bq_attn_kv4
         self.workspace = lib.bq_attn_kv4_workspace
+        # the native form of this module; it returns None for calls that it leaves to the code here
+        from . import _decode_binding as native
+        native.bind(*(ctypes.cast(f, _vp).value for f in (self.gemm, self.write, self.attn, self.workspace)))
+        self.native = native
 
 
 _bound = None
@@ -103,6 +107,11 @@ def bq_gemm_f16xi4_group(X, Wp, scale, group, zero_point=None, layout="interleav
     """fp16 X (M, K) times 4-bit weights Wp (N, K // 2 bytes) with fp16 scales (N, K // group) and, for unsigned
     codes, fp16 zero points of the same shape -> fp16 (M, N).  X may have a row stride."""
     import torch
+    if out is None and stream is None:
+        r = (_bound or _load()).native.gemm(X, Wp, scale, group, zero_point, _CODES.get(layout, layout),
+                                            _CODES.get(activation, activation))
+        if r is not None:
+            return r if type(r) is not int else _bound.bq._check(r, "bq_gemm_f16xi4_group")
     _need(X, torch.float16, "X", 2)
     _need(Wp, torch.uint8, "Wp", 2)
     b = _bound or _load()
@@ -179,6 +188,11 @@ def bq_qk_norm_rope_kv4(q, k, v, codes, params, slots, positions=None, cos=None,
     ``slots``.  Returns (q_out, k_values, v_values); the last two are None unless ``values``: they are what the cache
     then holds.  q, k and v may be views of one QKV matrix.  cos and sin are fp32 (positions, rot // 2)."""
     import torch
+    if out is None and stream is None:
+        r = (_bound or _load()).native.write(q, k, v, codes, params, slots, positions, cos, sin, q_weight, k_weight, eps,
+                                             pairs, values)
+        if r is not None:
+            return r if type(r) is not int else _bound.bq._check(r, "bq_qk_norm_rope_kv4")
     _need(q, torch.float16, "q", 3)
     b = _bound or _load()
     f16 = b.f16
@@ -242,6 +256,11 @@ def bq_attn_kv4(q, codes, params, block_table, seq_lens, cu_q=None, max_q=1, max
     last of its seq_lens[b] tokens in the cache.  ``max_len`` bounds the lengths (None: the width of the table);
     ``scale`` defaults to D ** -0.5; ``workspace`` (uint8) is allocated for the call when it is not given."""
     import torch
+    if out is None and stream is None:
+        r = (_bound or _load()).native.attn(q, codes, params, block_table, seq_lens, cu_q, max_q, max_len, scale, window,
+                                            lse, workspace)
+        if r is not None:
+            return r if type(r) is not int else _bound.bq._check(r, "bq_attn_kv4")
     _need(q, torch.float16, "q", 3)
     b = _bound or _load()
     f16, i32 = b.f16, b.i32
