@@ -74,6 +74,12 @@ __device__ __forceinline__ void cp_async_16_u(uint32_t smem_dst, const void* gme
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gmem_src) : "memory");
 }
 
+// The same through L1, for data that many blocks read: with copies past L1 the 8 KB row of X of a GEMV, read by all 688
+// blocks, cost 8 us.
+__device__ __forceinline__ void cp_async_16_l1(uint32_t smem_dst, const void* gmem_src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gmem_src) : "memory");
+}
+
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 template <int N>
