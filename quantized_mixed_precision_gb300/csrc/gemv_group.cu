@@ -49,6 +49,9 @@ struct StagePlan {
 // quad lane of rows 0..7 (a multiple of 128 bytes apart) then touch every bank once.
 __device__ __forceinline__ int row_swizzle(int r) { return (r & 1) << 6 | (r & 2) << 4 | (r & 4) << 2; }
 
+// The same for rows of 64 bytes (two of them share 128 bytes).
+__device__ __forceinline__ int weight_swizzle(int r) { return (r & 2) << 4 | (r & 4) << 2; }
+
 // Codes of a word as MMA operands; signed codes become u = c + 8 by flipping their top bit, in the same LOP3.  The
 // masks come in registers that the compiler cannot see through: with constants it put one of the two into a register
 // again for every LOP3.
@@ -284,22 +287,335 @@ cudaError_t launch_gemv(const GroupGemmArgs& a, cudaStream_t stream) {
                             reinterpret_cast<__half*>(a.y), plan);
 }
 
+// ---------------------------------------------------------------------------
+// More rows of X: blocks of 128 columns j and up to 64 rows i, K split over a
+// cluster.  A warp owns 32 columns and up to 32 rows; the warps of a block share
+// X, a slab of 128 k at a time, and two warps with the same columns their
+// weights.  The codes are converted to exact signed fp16 (a conversion serves all
+// rows of a warp, so its subtraction is cheap here and one accumulator a group is
+// enough).  What a slab needs besides (the order of X for plain codes, its sums
+// over groups for zero points, which add (8 - z) s sum) is made while the slab
+// before it is multiplied, so that a slab costs one barrier.
+// ---------------------------------------------------------------------------
+constexpr int GB_SLAB = 128;                 // k of a slab
+constexpr int GB_COLS = 128;                 // columns j of a block
+constexpr int GB_XS = 4;                     // slabs of X in the ring
+constexpr int GB_WS = 4;                     // slabs of weights in the ring
+
+// Blocks an SM: NT row tiles of 8 a warp, RG warps along the rows
+constexpr int block_slots(int nt, int rg) { return rg == 2 ? 2 : (nt == 4 ? 3 : 4); }
+
+template <int NT, int RG, int G>
+struct BlockCfg {
+  static constexpr int THREADS = 128 * RG;
+  static constexpr int ROWS = 8 * NT * RG;
+  static constexpr int X_B = ROWS * GB_SLAB * 2;
+  static constexpr int W_B = GB_COLS * GB_SLAB / 2;
+  static constexpr int SG = GB_SLAB / G;
+  static constexpr int SUMS = ROWS * SG;                             // sums of X over a slab's groups
+  static constexpr int STEPS = GB_COLS * SG;                         // (step, zero) of a slab
+  static constexpr int RING = GB_XS * X_B + GB_WS * W_B + 2 * SUMS * 4 + 2 * STEPS * 4;
+  static constexpr int ACC = ROWS * (GB_COLS + 4) * 4;               // partial results, for the cluster
+  static constexpr int SMEM = RING > ACC ? RING : ACC;
+};
+
+// Exact signed fp16 pairs of a word's codes, in the order of its masks: signed codes c, or unsigned ones less 8.
+template <bool ZP>
+__device__ __forceinline__ void signed_codes(uint32_t w, uint32_t (&h)[4]) {
+  const uint32_t y = w >> 8;
+  if constexpr (ZP) {
+    h[0] = hsub2_u32((w & CODE_LO) | H2_MAGIC, H2_1032);
+    h[1] = hfma2_u32((w & CODE_HI) | H2_MAGIC, H2_INV16, H2_NEG72);
+    h[2] = hsub2_u32((y & CODE_LO) | H2_MAGIC, H2_1032);
+    h[3] = hfma2_u32((y & CODE_HI) | H2_MAGIC, H2_INV16, H2_NEG72);
+  } else {
+    cvt_i4x8_f16(w, h);
+  }
+}
+
+template <int NT, int RG, int G, bool ZP>
+__global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
+    gemm_group_kernel(const __half* __restrict__ x, int64_t ld_x, const uint8_t* __restrict__ w, bool inter, int M, int N,
+                      int K, const uint16_t* __restrict__ scale, const uint16_t* __restrict__ zero, int actfn,
+                      __half* __restrict__ y, int parts) {
+  using C = BlockCfg<NT, RG, G>;
+  constexpr int WORDS = G / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int wcol = warp & 3, wrow = warp >> 2;              // this warp's columns and rows
+  const int part = blockIdx.x % parts, unit = blockIdx.x / parts;   // a cluster is the parts of a unit
+  const int m0 = blockIdx.y * C::ROWS, rows = min(C::ROWS, M - m0);
+  const int slabs = (K + GB_SLAB - 1) / GB_SLAB, ngroups = K / G;
+  const int s0 = (int)((int64_t)slabs * part / parts), s1 = (int)((int64_t)slabs * (part + 1) / parts);
+  uint8_t* const xr = smem;
+  uint8_t* const wr = smem + GB_XS * C::X_B;
+  float* const sums = reinterpret_cast<float*>(wr + GB_WS * C::W_B);
+  uint32_t* const steps = reinterpret_cast<uint32_t*>(sums + 2 * C::SUMS);
+  const int row_b = K / 2;
+
+  // copies: 16 pieces of 8 k a row of X (piece of word i, quad lane t at 4 i + t of its group, halves of 128 bytes
+  // swapped in odd rows); 4 pieces of a weight row
+  constexpr int XR = C::THREADS / 16, WR = C::THREADS / 4;  // rows of one copy of the block
+  const int xc = tid & 15, x_row = tid >> 4;
+  const __half* const xsrc = x + (int64_t)(m0 + x_row) * ld_x + xc * 8;
+  const uint32_t x_to = smem_u32(xr) + x_row * 256 +
+                        (((xc / (G / 8) * (G / 8) + xc % (G / 32) * 4 + xc % (G / 8) / (G / 32)) ^ ((x_row & 1) << 2)) << 4);
+  const int w_row = tid >> 2;
+  const uint32_t w_to = smem_u32(wr) + ((w_row * 64 + (tid & 3) * 16) ^ weight_swizzle(w_row));
+  const uint8_t* wsrc[GB_COLS / WR];
+#pragma unroll
+  for (int i = 0; i < GB_COLS / WR; ++i)
+    wsrc[i] = w + (size_t)min(unit * GB_COLS + w_row + WR * i, N - 1) * row_b + (tid & 3) * 16;
+  auto issue = [&](int s) {
+    if (s < s1) {
+      if (s * GB_SLAB + xc * 8 < K)
+#pragma unroll
+        for (int r = 0; r < C::ROWS; r += XR)
+          if (r + x_row < rows)
+            cp_async_16_l1(x_to + ((s - s0) & (GB_XS - 1)) * C::X_B + r * 256, xsrc + (int64_t)r * ld_x + s * GB_SLAB);
+      if (s * (GB_SLAB / 2) + (tid & 3) * 16 < row_b)
+#pragma unroll
+        for (int i = 0; i < GB_COLS / WR; ++i)
+          cp_async_16_u(w_to + ((s - s0) & (GB_WS - 1)) * C::W_B + i * WR * 64, wsrc[i] + s * (GB_SLAB / 2));
+    }
+    cp_async_commit();
+  };
+  // What slab s needs besides its copies
+  auto ready = [&](int s) {
+    if (s >= s1) return;
+    uint8_t* const xs = xr + ((s - s0) & (GB_XS - 1)) * C::X_B;
+    if (ZP || !inter) {
+      float* const to = sums + ((s - s0) & 1) * C::SUMS;
+#pragma unroll
+      for (int r = x_row; r < C::ROWS; r += XR) {           // (whole warps: rows past the last are not used)
+        uint4* const at = reinterpret_cast<uint4*>(xs + r * 256 + ((xc ^ ((r & 1) << 2)) << 4));
+        const uint4 p = *at;
+        if (ZP) {
+          // a group's pieces are those of G / 8 neighbouring lanes, in whatever order
+          const float2 a = unpack_h2(p.x), b = unpack_h2(p.y), c = unpack_h2(p.z), d = unpack_h2(p.w);
+          float v = ((a.x + a.y) + (b.x + b.y)) + ((c.x + c.y) + (d.x + d.y));
+#pragma unroll
+          for (int o = 1; o < G / 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o, 16);
+          if (xc % (G / 8) == 0) to[r * C::SG + xc / (G / 8)] = v;
+        }
+        if (!inter)
+          *at = make_uint4(prmt(p.x, p.z, 0x5410u), prmt(p.x, p.z, 0x7632u), prmt(p.y, p.w, 0x5410u),
+                           prmt(p.y, p.w, 0x7632u));
+      }
+    }
+  };
+  issue(s0);
+  issue(s0 + 1);
+  issue(s0 + 2);
+
+  float acc[2][NT][4];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[r][nt][i] = 0.0f;
+  // (step, zero) of a column for the groups of a slab: loaded two slabs before they are used (a load takes longer than
+  // a slab), and passed on through shared memory
+  const size_t s_at = (size_t)min(unit * GB_COLS + (tid & 127), N - 1) * ngroups;
+  constexpr int PER = (C::SG + RG - 1) / RG;                // groups of a thread: with two warps along the rows, half
+  const int j0 = PER * (tid >> 7);
+  auto load_steps = [&](int s, uint32_t (&v)[PER]) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int group = s * C::SG + j0 + j;
+      v[j] = 0;
+      if (s < s1 && j0 + j < C::SG && group < ngroups)
+        v[j] = ZP ? __ldg(scale + s_at + group) | (uint32_t)__ldg(zero + s_at + group) << 16 : __ldg(scale + s_at + group);
+    }
+  };
+  auto store_steps = [&](int s, const uint32_t (&v)[PER]) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (j0 + j < C::SG) steps[((s - s0) & 1) * C::STEPS + (j0 + j) * GB_COLS + (tid & 127)] = v[j];
+  };
+  uint32_t st0[PER], st1[PER];
+  load_steps(s0, st0);
+  load_steps(s0 + 1, st1);
+  cp_async_wait<2>();
+  __syncthreads();
+  ready(s0);
+  store_steps(s0, st0);
+
+  // (two sets of registers take turns: a copy between them would wait for the load)
+  auto slab = [&](int s, const uint32_t (&have)[PER], uint32_t (&next)[PER]) {
+    load_steps(s + 2, next);
+    cp_async_wait<1>();                      // slab s + 1 has come
+    __syncthreads();                         // ... for everybody, slab s is ready, and slab s - 1 has been read
+    issue(s + 3);
+    ready(s + 1);
+    store_steps(s + 1, have);
+    const uint32_t* const sp = steps + ((s - s0) & 1) * C::STEPS + wcol * 32 + g;
+    const uint8_t* const xs = xr + ((s - s0) & (GB_XS - 1)) * C::X_B + wrow * NT * 8 * 256;
+    const float* const sum = sums + ((s - s0) & 1) * C::SUMS + wrow * NT * 8 * C::SG;
+    const uint8_t* const ws = wr + ((s - s0) & (GB_WS - 1)) * C::W_B + wcol * 32 * 64;
+#pragma unroll
+    for (int j = 0; j < C::SG; ++j) {
+      if (s * C::SG + j >= ngroups) break;           // uniform
+      float c[2][NT][4];
+      uint32_t wd[4][WORDS];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* p = ws + (((g * 64) + j * (G / 2) + t * (G / 8)) ^ weight_swizzle(g)) + i * 512;
+        if constexpr (WORDS == 4) *reinterpret_cast<uint4*>(wd[i]) = *reinterpret_cast<const uint4*>(p);
+        else if constexpr (WORDS == 2) *reinterpret_cast<uint2*>(wd[i]) = *reinterpret_cast<const uint2*>(p);
+        else wd[i][0] = *reinterpret_cast<const uint32_t*>(p);
+      }
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) {
+        uint32_t h[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) signed_codes<ZP>(wd[r][i], h[r]);
+        // blocks of four tiles: all first halves of the word before the second, so that no MMA waits for the last
+        constexpr int NB = NT < 4 ? NT : 4;
+#pragma unroll
+        for (int nb = 0; nb < NT; nb += NB) {
+          uint4 v[NB];
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+            v[n] = *reinterpret_cast<const uint4*>(xs + (8 * (nb + n) + g) * 256 +
+                                                   (((j * (G / 8) + i * 4 + t) ^ ((g & 1) << 2)) << 4));
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float(&d)[4] = c[r][nb + n];
+              if (i == 0) mma_f16_zero(d, h[2 * r][0], h[2 * r + 1][0], h[2 * r][1], h[2 * r + 1][1], v[n].x, v[n].y);
+              else mma_f16(d, h[2 * r][0], h[2 * r + 1][0], h[2 * r][1], h[2 * r + 1][1], v[n].x, v[n].y);
+            }
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              mma_f16(c[r][nb + n], h[2 * r][2], h[2 * r + 1][2], h[2 * r][3], h[2 * r + 1][3], v[n].z, v[n].w);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float2 p0 = unpack_h2(sp[j * GB_COLS + 16 * r]), p1 = unpack_h2(sp[j * GB_COLS + 16 * r + 8]);
+        const float a0 = p0.x, a1 = p1.x, b0 = 8.0f - p0.y, b1 = 8.0f - p1.y;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float x0 = 0.0f, x1 = 0.0f;
+          if (ZP) {
+            x0 = sum[(8 * nt + 2 * t) * C::SG + j];
+            x1 = sum[(8 * nt + 2 * t + 1) * C::SG + j];
+          }
+          acc[r][nt][0] = fmaf(a0, ZP ? fmaf(b0, x0, c[r][nt][0]) : c[r][nt][0], acc[r][nt][0]);
+          acc[r][nt][1] = fmaf(a0, ZP ? fmaf(b0, x1, c[r][nt][1]) : c[r][nt][1], acc[r][nt][1]);
+          acc[r][nt][2] = fmaf(a1, ZP ? fmaf(b1, x0, c[r][nt][2]) : c[r][nt][2], acc[r][nt][2]);
+          acc[r][nt][3] = fmaf(a1, ZP ? fmaf(b1, x1, c[r][nt][3]) : c[r][nt][3], acc[r][nt][3]);
+        }
+      }
+    }
+  };
+
+  for (int s = s0; s < s1; s += 2) {
+    slab(s, st1, st0);
+    if (s + 1 < s1) slab(s + 1, st0, st1);
+  }
+
+  // ---- add the cluster's shares of K in rank order, each block a share of the columns ----
+  cp_async_wait<0>();
+  __syncthreads();
+  float* const pa = reinterpret_cast<float*>(smem);         // [row of X][column], padded
+  constexpr int LD = GB_COLS + 4;
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        pa[(8 * (wrow * NT + nt) + 2 * t + (i & 1)) * LD + wcol * 32 + 16 * r + g + 8 * (i >> 1)] = acc[r][nt][i];
+  if (parts > 1) cluster_sync_all(); else __syncthreads();
+  const int c0 = GB_COLS * part / parts, c1 = GB_COLS * (part + 1) / parts, cols = c1 - c0;
+  const uint32_t pa_u = smem_u32(pa);
+  for (int i = tid; i < rows * cols; i += C::THREADS) {
+    const int r = i / cols, cc = c0 + i - r * cols;
+    const int n = unit * GB_COLS + cc;
+    if (n >= N) continue;
+    float v = 0.0f;
+    if (parts == 1) {
+      v = pa[r * LD + cc];
+    } else {
+      for (int p = 0; p < parts; ++p) {
+        float u;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(mapa_shared(pa_u + (r * LD + cc) * 4, p)));
+        v += u;
+      }
+    }
+    y[(size_t)(m0 + r) * N + n] = __float2half_rn(apply_act(v, actfn));
+  }
+  if (parts > 1) cluster_sync_all();                        // nobody leaves while its shares are read
+}
+
+template <int NT, int RG, int G, bool ZP>
+cudaError_t launch_block(const GroupGemmArgs& a, cudaStream_t stream) {
+  using C = BlockCfg<NT, RG, G>;
+  const int64_t units = (a.N + GB_COLS - 1) / GB_COLS, zs = (a.M + C::ROWS - 1) / C::ROWS;
+  // K is split over as many blocks as make the fewest waves of resident blocks for their share of K, with a little
+  // for each part to join; at least four slabs a part
+  const int slabs = (int)((a.K + GB_SLAB - 1) / GB_SLAB);
+  const int64_t slots = (int64_t)sm_count() * block_slots(NT, RG);
+  int parts = 1;
+  double best = 1e30;
+  for (int p = 1; p <= 4 && (p == 1 || slabs >= 4 * p); ++p) {
+    const double cost = (double)((units * zs * p + slots - 1) / slots) / p * (1.0 + 0.02 * p);
+    if (cost < best) {
+      best = cost;
+      parts = p;
+    }
+  }
+  auto kern = gemm_group_kernel<NT, RG, G, ZP>;
+  cudaError_t e = set_smem_once(kern, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(parts * units), (unsigned)zs);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)parts;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, reinterpret_cast<const __half*>(a.x), a.ld_x, a.w,
+                            a.layout == BQ_LAYOUT_INTERLEAVED, (int)a.M, (int)a.N, (int)a.K, a.scale, a.zero_point,
+                            a.actfn, reinterpret_cast<__half*>(a.y), parts);
+}
+
+template <int G, bool ZP>
+cudaError_t launch_rows(const GroupGemmArgs& a, cudaStream_t stream) {
+  if (a.M <= 8) return launch_gemv<G, ZP>(a, stream);
+  if (a.M <= 16) return launch_block<2, 1, G, ZP>(a, stream);
+  if (a.M <= 32) return launch_block<4, 1, G, ZP>(a, stream);
+  return launch_block<4, 2, G, ZP>(a, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_group(const GroupGemmArgs& g, cudaStream_t stream) {
   const bool zp = g.zero_point != nullptr;
-  for (int64_t m = 0; m < g.M; m += 8) {
+  constexpr int64_t MOST = 32768;          // rows of a launch
+  for (int64_t m = 0; m < g.M; m += MOST) {
     GroupGemmArgs a = g;
     a.x = g.x + m * g.ld_x;
     a.y = g.y + m * g.N;
-    a.M = g.M - m < 8 ? g.M - m : 8;
+    a.M = g.M - m < MOST ? g.M - m : MOST;
     cudaError_t e;
     if (g.group == 128)
-      e = zp ? launch_gemv<128, true>(a, stream) : launch_gemv<128, false>(a, stream);
+      e = zp ? launch_rows<128, true>(a, stream) : launch_rows<128, false>(a, stream);
     else if (g.group == 64)
-      e = zp ? launch_gemv<64, true>(a, stream) : launch_gemv<64, false>(a, stream);
+      e = zp ? launch_rows<64, true>(a, stream) : launch_rows<64, false>(a, stream);
     else
-      e = zp ? launch_gemv<32, true>(a, stream) : launch_gemv<32, false>(a, stream);
+      e = zp ? launch_rows<32, true>(a, stream) : launch_rows<32, false>(a, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
