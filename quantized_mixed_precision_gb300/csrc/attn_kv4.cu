@@ -113,7 +113,9 @@ __device__ __forceinline__ int64_t seq_cost(const AttnParams& a, const Seq& s) {
   return (int64_t)s.tiles * s.qtiles * a.heads;
 }
 
-constexpr int blocks_per_sm(int D, int nt) { return nt == 1 ? (D == 256 ? 2 : 3) : (D == 256 ? 1 : 2); }
+// Blocks per SM, by the registers of the accumulators: what fits without spills.  With D = 128 and 8 query rows, 3 blocks
+// (168 registers a thread) take 133 us for 739 MB of cache, 4 blocks (128 registers) 147 us, 2 blocks 138 us.
+constexpr int blocks_per_sm(int D, int nt) { return D < 256 && D * nt <= 256 ? 3 : 2; }
 
 template <int D, int NG, int NT>
 struct Cfg {
@@ -129,9 +131,13 @@ struct Cfg {
   static constexpr int STAGE_B = 2 * CODE_B + 2 * PAR_B;
   static constexpr int RING_B = AW * STAGES * STAGE_B;
   static constexpr int JOIN_B = AW * ROWS * (D + 4) * 4;
-  static constexpr int SMEM = RING_B > JOIN_B ? RING_B : JOIN_B;
-  // Blocks per SM: what the registers allow without spills.  With D = 128, 3 blocks (168 registers a thread)
-  // take 133 us for 739 MB of cache, 4 blocks (128 registers) 147 us, 2 blocks 138 us.
+  static constexpr int WORK_B = RING_B > JOIN_B ? RING_B : JOIN_B;
+  // With more than 128 accumulators a lane's queries and constants live in shared memory, and with 512 a tile is
+  // worked on 16 keys at a time, for the registers' sake.
+  static constexpr bool WIDE = D * NT >= 256;
+  static constexpr int HB = D * NT >= 512 ? 1 : 2;
+  static constexpr int QF_B = NT * NG * KW * 512;
+  static constexpr int SMEM = WORK_B + (WIDE ? QF_B + ROWS * 4 * (NG + 3) : 0);
   static constexpr int BLOCKS = blocks_per_sm(D, NT);
 };
 
@@ -343,110 +349,169 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
     for (int k = 0; k < C::STAGES - 1; ++k) issue(k);
 
     // ---- query fragments: column g of n-tile nt is row row0 + 8 nt + g ----
-    uint32_t qf[NT][NG][C::KW][4];
-    float cf[NT][2], qs[NT][NG][2];       // for columns 2t, 2t + 1
-    int hi[NT][2], lo[NT][2];             // last and first key those rows see
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = 8 * nt + g;
-      const int tok = (row0 + min(r, rows - 1)) / a.rep;
-      const int hr = (row0 + min(r, rows - 1)) - tok * a.rep;
+    struct Query {
+      uint4 f[NG][C::KW];          // (low codes' pair, pair; high codes' pair, pair) of a key word
+      float c, sum[NG];            // factor of the products, scaled sums over the groups
+    };
+    auto load_query = [&](int nt) -> Query {
+      Query q;
+      const int r = row0 + min(8 * nt + g, rows - 1);
+      const int tok = r / a.rep, hr = r - tok * a.rep;
       const __half* qp = a.q + (s.first + tok) * a.ld_q + (int64_t)(head * a.rep + hr) * D;
-      uint4 raw[NG][C::KW];
-      float top = 0.0f, part[NG];
+      float top = 0.0f;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        part[gr] = 0.0f;
+        q.sum[gr] = 0.0f;
 #pragma unroll
         for (int i = 0; i < C::KW; ++i) {
-          raw[gr][i] = *reinterpret_cast<const uint4*>(qp + gr * C::G + t * (C::G / 4) + 8 * i);
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[gr][i]);
+          q.f[gr][i] = *reinterpret_cast<const uint4*>(qp + gr * C::G + t * (C::G / 4) + 8 * i);
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&q.f[gr][i]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 f = unpack_h2(w[e]);
             top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-            part[gr] += f.x + f.y;
+            q.sum[gr] += f.x + f.y;
           }
         }
       }
+      const float sc = a.scale * LOG2E;
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 1; o < 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) part[gr] += __shfl_xor_sync(0xffffffffu, part[gr], o);
+      for (int gr = 0; gr < NG; ++gr) {
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) q.sum[gr] += __shfl_xor_sync(0xffffffffu, q.sum[gr], o);
+        q.sum[gr] *= sc;
       }
       // the row times a power of two that brings its largest value to [2**10, 2**11): exact, and the
       // columns that meet low codes can carry the factor 16 that low and high codes differ by
       const int e = top > 0.0f ? 10 - ilog2f(top) : 0;
-      const float f1 = pow2f(e);
+      const float f1 = pow2f(e), f16 = f1 * 16.0f;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
         for (int i = 0; i < C::KW; ++i) {
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[gr][i]);
-          float2 d01 = unpack_h2(w[0]), d23 = unpack_h2(w[1]), d45 = unpack_h2(w[2]), d67 = unpack_h2(w[3]);
-          qf[nt][gr][i][0] = pack_h2(d01.x * f1 * 16.0f, d45.x * f1 * 16.0f);
-          qf[nt][gr][i][1] = pack_h2(d23.x * f1 * 16.0f, d67.x * f1 * 16.0f);
-          qf[nt][gr][i][2] = pack_h2(d01.y * f1, d45.y * f1);
-          qf[nt][gr][i][3] = pack_h2(d23.y * f1, d67.y * f1);
+          const uint4 v = q.f[gr][i];
+          const float2 d01 = unpack_h2(v.x), d23 = unpack_h2(v.y), d45 = unpack_h2(v.z), d67 = unpack_h2(v.w);
+          q.f[gr][i] = make_uint4(pack_h2(d01.x * f16, d45.x * f16), pack_h2(d23.x * f16, d67.x * f16),
+                                  pack_h2(d01.y * f1, d45.y * f1), pack_h2(d23.y * f1, d67.y * f1));
         }
-      const float sc = a.scale * LOG2E;
-      const float c1 = sc * pow2f(20 - e);
+      q.c = sc * pow2f(20 - e);
+      return q;
+    };
+    // last and first key that row r (of the unit's n-tiles) sees
+    auto last_key = [&](int r) { return s.len - s.n + (row0 + min(r, rows - 1)) / a.rep; };
+    auto first_key = [&](int hi) { return a.window > 0 ? (int)max((int64_t)0, (int64_t)hi + 1 - a.window) : 0; };
+    constexpr int NR = C::WIDE ? 1 : NT;
+    uint4 qr[NR][NG][C::KW];              // the same in registers ...
+    P2 cfr[NR], qsr[NR][NG];              // ... with the constants of columns 2t, 2t + 1
+    int2 hir[NR];
+    uint4* const qsm = reinterpret_cast<uint4*>(smem + C::WORK_B);   // or in shared memory: [nt][group][word][lane],
+    float* const csm = reinterpret_cast<float*>(smem + C::WORK_B + C::QF_B);   // [factor, sums, last, first][row]
+    if constexpr (C::WIDE) {
+      for (int nt = warp; nt < NT; nt += AW) {
+        const Query q = load_query(nt);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int src = (2 * t + j) * 4;
-        cf[nt][j] = __shfl_sync(0xffffffffu, c1, src);
+        for (int gr = 0; gr < NG; ++gr) {
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) qs[nt][gr][j] = __shfl_sync(0xffffffffu, part[gr], src) * sc;
-        const int rr = row0 + min(8 * nt + 2 * t + j, rows - 1);
-        hi[nt][j] = s.len - s.n + rr / a.rep;
-        lo[nt][j] = a.window > 0 ? (int)max((int64_t)0, (int64_t)hi[nt][j] + 1 - a.window) : 0;
+          for (int i = 0; i < C::KW; ++i) qsm[((nt * NG + gr) * C::KW + i) * 32 + lane] = q.f[gr][i];
+          if (t == 0) csm[(1 + gr) * C::ROWS + 8 * nt + g] = q.sum[gr];
+        }
+        if (t == 0) {
+          const int hi = last_key(8 * nt + g);
+          csm[8 * nt + g] = q.c;
+          csm[(1 + NG) * C::ROWS + 8 * nt + g] = __int_as_float(hi);
+          csm[(2 + NG) * C::ROWS + 8 * nt + g] = __int_as_float(first_key(hi));
+        }
+      }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const Query q = load_query(nt);
+        const int src = 8 * t;             // lane of row 2t
+        cfr[nt] = p2(__shfl_sync(0xffffffffu, q.c, src), __shfl_sync(0xffffffffu, q.c, src + 4));
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          qsr[nt][gr] = p2(__shfl_sync(0xffffffffu, q.sum[gr], src), __shfl_sync(0xffffffffu, q.sum[gr], src + 4));
+#pragma unroll
+          for (int i = 0; i < C::KW; ++i) qr[nt][gr][i] = q.f[gr][i];
+        }
+        hir[nt] = make_int2(last_key(8 * nt + 2 * t), last_key(8 * nt + 2 * t + 1));
+      }
+    }
+    auto query = [&](int nt, int gr, int i) -> uint4 {
+      if constexpr (C::WIDE) return qsm[((nt * NG + gr) * C::KW + i) * 32 + lane];
+      else return qr[nt][gr][i];
+    };
+    auto factor = [&](int nt) -> P2 {
+      if constexpr (C::WIDE) return *reinterpret_cast<const P2*>(csm + 8 * nt + 2 * t);
+      else return cfr[nt];
+    };
+    auto query_sum = [&](int nt, int gr) -> P2 {
+      if constexpr (C::WIDE) return *reinterpret_cast<const P2*>(csm + (1 + gr) * C::ROWS + 8 * nt + 2 * t);
+      else return qsr[nt][gr];
+    };
+    auto lasts = [&](int nt) -> int2 {
+      if constexpr (C::WIDE) return *reinterpret_cast<const int2*>(csm + (1 + NG) * C::ROWS + 8 * nt + 2 * t);
+      else return hir[nt];
+    };
+    auto firsts = [&](int nt) -> int2 {
+      if constexpr (C::WIDE) return *reinterpret_cast<const int2*>(csm + (2 + NG) * C::ROWS + 8 * nt + 2 * t);
+      else return make_int2(first_key(hir[nt].x), first_key(hir[nt].y));
+    };
+
+    float o[NT][NG][C::MT][4];
+    P2 lowacc[NT][NG], m[NT], l[NT];      // columns 2t, 2t + 1
+    float vf = pow2f(30);                 // power of two that the values' steps carry into fp16
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt] = l[nt] = p2(0.0f, 0.0f);
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        lowacc[nt][gr] = p2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[nt][gr][i][j] = 0.0f;
       }
     }
 
-    float o[NT][NG][C::MT][4], lowacc[NT][NG][2], m[NT][2], l[NT][2];
-    float vf = pow2f(30);                 // power of two that the values' steps carry into fp16
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        m[nt][j] = 0.0f;
-        l[nt][j] = 0.0f;
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          lowacc[nt][gr][j] = 0.0f;
-#pragma unroll
-          for (int i = 0; i < C::MT; ++i) o[nt][gr][i][2 * j] = o[nt][gr][i][2 * j + 1] = 0.0f;
-        }
-      }
-
     // Columns that have seen a key have a running maximum m; the others hold 0
-    // there, and while there are any (`fresh`) every tile renews the maxima.
+    // there, and while there are any (`fresh`) every step renews the maxima.
     bool fresh = true;
     uint32_t seen = 0;
     uint32_t st = ring;
+    constexpr int HB = C::HB;             // halves (16 keys) of a step
 #pragma unroll 1
     for (int k = 0; k < mytiles; ++k) {
       cp_async_wait<C::STAGES - 2>();
       __syncwarp();
       issue(k + C::STAGES - 1);
-      const uint8_t* sp = smem + (st - smem_u32(smem));
-      const int key = key0 + (warp + AW * k) * TILE;
+#pragma unroll 1
+      for (int h0 = 0; h0 < 2; h0 += HB) {
+      const uint32_t sth = st + 16 * h0 * C::R;
+      const uint8_t* sp = smem + (sth - smem_u32(smem));
+      const uint8_t* pp16 = smem + (st - smem_u32(smem)) + 2 * C::CODE_B + (16 * h0 + 2 * g) * PR;
+      const int key = key0 + (warp + AW * k) * TILE + 16 * h0;
 
       // ---- scores: base-2 logits less the running maximum ----
-      float sv[2][NT][4];
-      uint32_t vp[2][2][NG];              // (step, low) of the values, keys 2g and 2g + 1 of each half
+      P2 sv[HB][NT][2];                   // [half][n-tile][key 2g, 2g + 1]
+      uint32_t vp[HB][2][NG];             // (step, low) of the values, keys 2g and 2g + 1 of each half
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float acc[NT][NG][4];
+      for (int h = 0; h < HB; ++h) {
+        uint32_t kp[2][NG];
+        load_pair<NG>(pp16 + 16 * h * PR, kp);
+        load_pair<NG>(pp16 + 16 * h * PR + C::PAR_B, vp[h]);
+        P2 x[NT][2], y[NT][2];            // products by the steps; what the lows add, less the maximum
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nt][gr][i] = 0.0f;
+        for (int nt = 0; nt < NT; ++nt) {
+          const float2 mm = f2(m[nt]);
+          y[nt][0] = y[nt][1] = p2(-mm.x, -mm.y);
+        }
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
+          float acc[NT][4];
           uint32_t w0[C::KW], w1[C::KW];
           const uint8_t* kw = sp + (k_at0 ^ (gr * (C::G / 2))) + 16 * h * C::R;
           load_words<C::G / 8>(kw, w0);
@@ -458,39 +523,41 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
 #pragma unroll
           for (int i = 0; i < C::KW; ++i) {
             const uint32_t x0 = w0[i] >> 8, x1 = w1[i] >> 8;
+            const uint32_t l0 = w0[i] & CODE_LO, l1 = w1[i] & CODE_LO, l2 = x0 & CODE_LO, l3 = x1 & CODE_LO;
+            const uint32_t h0 = w0[i] & CODE_HI, h1 = w1[i] & CODE_HI, h2 = x0 & CODE_HI, h3 = x1 & CODE_HI;
+            uint4 qv[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_f16(acc[nt][gr], w0[i] & CODE_LO, w1[i] & CODE_LO, x0 & CODE_LO, x1 & CODE_LO, qf[nt][gr][i][0],
-                      qf[nt][gr][i][1]);
-              mma_f16(acc[nt][gr], w0[i] & CODE_HI, w1[i] & CODE_HI, x0 & CODE_HI, x1 & CODE_HI, qf[nt][gr][i][2],
-                      qf[nt][gr][i][3]);
+              qv[nt] = query(nt, gr, i);
+              if (i == 0) mma_f16_zero(acc[nt], l0, l1, l2, l3, qv[nt].x, qv[nt].y);
+              else mma_f16(acc[nt], l0, l1, l2, l3, qv[nt].x, qv[nt].y);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], h0, h1, h2, h3, qv[nt].z, qv[nt].w);
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float2 p = unpack_h2(kp[r][gr]);
+            const P2 step = p2(p.x, p.x), low = p2(p.y, p.y);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const P2 d = p2(acc[nt][2 * r], acc[nt][2 * r + 1]);
+              x[nt][r] = gr == 0 ? mul2(step, d) : fma2(step, d, x[nt][r]);
+              y[nt][r] = fma2(low, query_sum(nt, gr), y[nt][r]);
             }
           }
         }
-        uint32_t kp[2][NG];
-        const uint8_t* pk = sp + 2 * C::CODE_B + (16 * h + 2 * g) * PR;
-        load_pair<NG>(pk, kp);
-        load_pair<NG>(pk + C::PAR_B, vp[h]);
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int nt = 0; nt < NT; ++nt) {
+          const P2 c = factor(nt);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float x = 0.0f, y = -m[nt][j];
-#pragma unroll
-              for (int gr = 0; gr < NG; ++gr) {
-                const float2 p = unpack_h2(kp[r][gr]);
-                x = gr == 0 ? p.x * acc[nt][gr][2 * r + j] : fmaf(p.x, acc[nt][gr][2 * r + j], x);
-                y = fmaf(p.y, qs[nt][gr][j], y);
-              }
-              sv[h][nt][2 * r + j] = fmaf(x, cf[nt][j], y);
-            }
+          for (int r = 0; r < 2; ++r) sv[h][nt][r] = fma2(x[nt][r], c, y[nt][r]);
+        }
       }
       // keys that some row does not see, and what lies past the last one
-      if (key < all_begin || key + TILE > all_end) {
+      if (key < all_begin || key + 16 * HB > all_end) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < HB; ++h)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const int tok = key + 16 * h + 2 * g + r;
@@ -499,24 +566,32 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
               for (int gr = 0; gr < NG; ++gr) vp[h][r][gr] = 0;
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                if (tok > hi[nt][j] || tok < lo[nt][j]) sv[h][nt][2 * r + j] = -INFINITY;
+            for (int nt = 0; nt < NT; ++nt) {
+              const int2 hi = lasts(nt), lo = firsts(nt);
+              float2 v = f2(sv[h][nt][r]);
+              if (tok > hi.x || tok < lo.x) v.x = -INFINITY;
+              if (tok > hi.y || tok < lo.y) v.y = -INFINITY;
+              sv[h][nt][r] = p2(v.x, v.y);
+            }
           }
       }
 
       // ---- running maximum, renewed only when a score passes it by 2**8 ----
-      float top[NT][2], step_top = 0.0f, most = -INFINITY;
+      float2 top[NT];
+      float step_top = 0.0f, most = -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        top[nt] = f2(sv[0][nt][0]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          top[nt][j] = fmaxf(fmaxf(sv[0][nt][j], sv[0][nt][2 + j]), fmaxf(sv[1][nt][j], sv[1][nt][2 + j]));
-          most = fmaxf(most, top[nt][j]);
+        for (int i = 1; i < 2 * HB; ++i) {
+          const float2 v = f2(sv[i / 2][nt][i & 1]);
+          top[nt].x = fmaxf(top[nt].x, v.x);
+          top[nt].y = fmaxf(top[nt].y, v.y);
         }
+        most = fmaxf(most, fmaxf(top[nt].x, top[nt].y));
+      }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < HB; ++h)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -533,62 +608,67 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
         }
         bool all = true;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          float up[2], f[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
+            float v = j ? top[nt].y : top[nt].x;
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1)
-              top[nt][j] = fmaxf(top[nt][j], __shfl_xor_sync(0xffffffffu, top[nt][j], x));
+            for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
             const uint32_t bit = 1u << (2 * nt + j);
             // a first maximum may lie below 0; later ones only rise
-            float up = seen & bit ? fmaxf(top[nt][j], 0.0f) : (top[nt][j] == -INFINITY ? 0.0f : top[nt][j]);
-            if (top[nt][j] != -INFINITY) seen |= bit;
+            up[j] = seen & bit ? fmaxf(v, 0.0f) : (v == -INFINITY ? 0.0f : v);
+            if (v != -INFINITY) seen |= bit;
             all = all && (seen & bit);
-            m[nt][j] += up;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              sv[h][nt][j] -= up;
-              sv[h][nt][2 + j] -= up;
-            }
-            const float f = ex2(fminf(-up, 0.0f));   // (nothing has been summed where up < 0)
-            l[nt][j] *= f;
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              lowacc[nt][gr][j] *= f;
-#pragma unroll
-              for (int i = 0; i < C::MT; ++i) {
-                o[nt][gr][i][j] *= f * fv;
-                o[nt][gr][i][2 + j] *= f * fv;
-              }
-            }
+            f[j] = ex2(fminf(-up[j], 0.0f));       // (nothing has been summed where up < 0)
           }
+          const P2 ff = p2(f[0], f[1]), down = p2(-up[0], -up[1]), of = p2(f[0] * fv, f[1] * fv);
+          m[nt] = add2(m[nt], p2(up[0], up[1]));
+          l[nt] = mul2(l[nt], ff);
+#pragma unroll
+          for (int h = 0; h < HB; ++h)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) sv[h][nt][r] = add2(sv[h][nt][r], down);
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            lowacc[nt][gr] = mul2(lowacc[nt][gr], ff);
+#pragma unroll
+            for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const float2 v = f2(mul2(p2(o[nt][gr][i][e], o[nt][gr][i][e + 1]), of));
+                o[nt][gr][i][e] = v.x;
+                o[nt][gr][i][e + 1] = v.y;
+              }
+          }
+        }
         fresh = !__all_sync(0xffffffffu, all);
       }
 
       // ---- weights, their sums, and the second product ----
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < HB; ++h) {
         uint32_t pf[NT][NG][2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float vs[NG], vl[NG];
+          P2 vs[NG], vl[NG];
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
             const float2 v = unpack_h2(vp[h][r][gr]);
-            vs[gr] = v.x * vf;
-            vl[gr] = v.y;
+            vs[gr] = p2(v.x * vf, v.x * vf);
+            vl[gr] = p2(v.y, v.y);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float p0 = ex2(sv[h][nt][2 * r]), p1 = ex2(sv[h][nt][2 * r + 1]);
-            l[nt][0] += p0;
-            l[nt][1] += p1;
+            const float2 e = f2(sv[h][nt][r]);
+            const P2 w = p2(ex2(e.x), ex2(e.y));
+            l[nt] = add2(l[nt], w);
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-              lowacc[nt][gr][0] = fmaf(p0, vl[gr], lowacc[nt][gr][0]);
-              lowacc[nt][gr][1] = fmaf(p1, vl[gr], lowacc[nt][gr][1]);
+              lowacc[nt][gr] = fma2(w, vl[gr], lowacc[nt][gr]);
               // the only rounding to 16 bits: weight times step, 2**-11 relative
-              pf[nt][gr][r] = movmatrix_trans(pack_h2(p0 * vs[gr], p1 * vs[gr]));
+              const float2 v = f2(mul2(w, vs[gr]));
+              pf[nt][gr][r] = movmatrix_trans(pack_h2(v.x, v.y));
             }
           }
         }
@@ -596,7 +676,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
         for (int c = 0; c < C::PER; c += 2) {
           // 16-byte pieces c and c + 1 (32 dims each) of 16 tokens
           uint32_t w[4];
-          ldmatrix_b8_trans_x2(st + (v_at ^ (c * 16)) + 16 * h * C::R, w);
+          ldmatrix_b8_trans_x2(sth + (v_at ^ (c * 16)) + 16 * h * C::R, w);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int gr = (c + x / 2) * 32 / C::G, i = ((c + x / 2) * 32 % C::G) / 16 + (x & 1);
@@ -608,6 +688,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
           }
         }
       }
+      }
       st = st == ring + (C::STAGES - 1) * C::STAGE_B ? ring : st + C::STAGE_B;
     }
 
@@ -618,15 +699,18 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
     constexpr int JS = D + 4;             // floats of a row: D values, maximum, sum, padding
     const float back = pow2f(24) / vf;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 mm = f2(m[nt]), ll = f2(l[nt]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        float sum = j ? ll.y : ll.x, low[NG];
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) low[gr] = j ? f2(lowacc[nt][gr]).y : f2(lowacc[nt][gr]).x;
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
-          l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], x);
+          sum += __shfl_xor_sync(0xffffffffu, sum, x);
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr)
-            lowacc[nt][gr][j] += __shfl_xor_sync(0xffffffffu, lowacc[nt][gr][j], x);
+          for (int gr = 0; gr < NG; ++gr) low[gr] += __shfl_xor_sync(0xffffffffu, low[gr], x);
         }
         float* row = js + (warp * C::ROWS + 8 * nt + 2 * t + j) * JS;
 #pragma unroll
@@ -635,15 +719,15 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
           for (int i = 0; i < C::MT; ++i) {
             // tile i of a group: byte g of its i-th 8, dims 2g and 2g + 1
             const int d = gr * C::G + 16 * i + 2 * g;
-            *reinterpret_cast<float2*>(row + d) =
-                make_float2(fmaf(o[nt][gr][i][j], back, lowacc[nt][gr][j]),
-                            fmaf(o[nt][gr][i][2 + j], back * 0.0625f, lowacc[nt][gr][j]));
+            *reinterpret_cast<float2*>(row + d) = make_float2(fmaf(o[nt][gr][i][j], back, low[gr]),
+                                                              fmaf(o[nt][gr][i][2 + j], back * 0.0625f, low[gr]));
           }
         if (g == 0) {
-          row[D] = l[nt][j] > 0.0f ? m[nt][j] : M_NONE;
-          row[D + 1] = l[nt][j];
+          row[D] = sum > 0.0f ? (j ? mm.y : mm.x) : M_NONE;
+          row[D + 1] = sum;
         }
       }
+    }
     __syncthreads();
     constexpr int LANES = D / 4;          // threads of a row, 4 dims each
     for (int r = tid / LANES; r < rows; r += AW * 32 / LANES) {
@@ -765,8 +849,12 @@ __global__ void __launch_bounds__(128) attn_kv4_join_kernel(const AttnParams a) 
   }
 }
 
-// 8 query rows a block where they all fit, else 16.
-inline int row_tiles(int64_t rep, int64_t max_q) { return rep * max_q <= 8 ? 1 : 2; }
+// Query rows of a block, in tiles of 8: what the longest query needs, at most 32 (16 with D = 256).  A conversion of the
+// cache's codes serves all of a block's rows.
+inline int row_tiles(int64_t rep, int64_t max_q, int64_t D) {
+  const int64_t rows = rep * max_q;
+  return rows <= 8 ? 1 : (rows <= 16 || D == 256 ? 2 : 4);
+}
 
 // Whether the tiles of all units are dealt out to a grid of resident blocks
 // (and joined), or one block takes each unit.
@@ -807,14 +895,18 @@ cudaError_t launch(const AttnParams& p, const AttnKv4Args& a, cudaStream_t strea
 
 template <int D, int NG>
 cudaError_t launch_nt(const AttnParams& p, const AttnKv4Args& a, cudaStream_t stream) {
-  return row_tiles(p.rep, a.max_q) == 1 ? launch<D, NG, 1>(p, a, stream) : launch<D, NG, 2>(p, a, stream);
+  const int nt = row_tiles(p.rep, a.max_q, D);
+  if (nt == 1) return launch<D, NG, 1>(p, a, stream);
+  if constexpr (D < 256)
+    if (nt == 4) return launch<D, NG, 4>(p, a, stream);
+  return launch<D, NG, 2>(p, a, stream);
 }
 
 }  // namespace
 
 size_t attn_kv4_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_len) {
   if (!split(max_len)) return 0;
-  const int nt = row_tiles(q_heads / kv_heads, max_q);
+  const int nt = row_tiles(q_heads / kv_heads, max_q, D);
   const size_t grid = (size_t)split_grid(D, nt);
   return grid * sizeof(Meta) + 2 * grid * 8 * nt * (D + 4) * sizeof(float);
 }
@@ -844,7 +936,7 @@ cudaError_t launch_attn_kv4(const AttnKv4Args& a, cudaStream_t stream) {
   p.max_q = a.max_q;
   p.max_len = a.max_len;
   p.window = a.window;
-  const int rows = 8 * row_tiles(p.rep, a.max_q);
+  const int rows = 8 * row_tiles(p.rep, a.max_q, a.pool.D);
   p.qtiles = (int)((a.max_q * p.rep + rows - 1) / rows);
   p.scale = a.scale;
   p.out = reinterpret_cast<__half*>(a.out);

@@ -18,15 +18,6 @@ namespace bq {
 
 namespace {
 
-// D = A * B with a zero C.
-__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                             uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
 // ---------------------------------------------------------------------------
 // Up to 8 rows of X: bound by one read of the weights.  A block owns 16 columns
 // and its warps take stages of K in turn, each through a ring of its own, so

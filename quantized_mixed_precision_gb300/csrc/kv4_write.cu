@@ -38,34 +38,6 @@ constexpr int WT = 128;   // threads of a block
 constexpr int WQ = 4;     // items (a head for each D / 8 threads) of queries whose loads are issued together
 constexpr int WKV = 2;    // the same for keys and values
 
-struct P2 {               // two fp32 values in one 64-bit register
-  uint64_t v;
-};
-__device__ __forceinline__ P2 p2(float a, float b) {
-  P2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 f2(P2 p) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p.v));
-  return r;
-}
-__device__ __forceinline__ P2 mul2(P2 a, P2 b) {
-  P2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ P2 add2(P2 a, P2 b) {
-  P2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ P2 fma2(P2 a, P2 b, P2 c) {
-  P2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
 // a * b rounded, for a product that an addition follows: ptxas contracts a packed mul.rn and add.rn into one fma
 // (seen as outputs one place off), which an fma with an addend that it does not know keeps apart.  mz: -0.
 __device__ __forceinline__ P2 product2(P2 a, P2 b, P2 mz) { return fma2(a, b, mz); }
