@@ -36,8 +36,10 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float M_NONE = -1e30f;  // running maximum before any key
 
+// A unit that has to be joined: its first block, whether that holds it in its second slot, and its blocks
 struct Meta {
-  int32_t parts;       // 0: nothing to join here
+  int32_t parts;       // 0: nothing to join
+  int32_t block, slot;
   int32_t b, head, qt;
 };
 
@@ -58,7 +60,8 @@ struct AttnParams {
   __half* out;
   float* lse;
   float* parts;                   // [2 * grid][rows][D + 2]
-  Meta* meta;                     // [grid]
+  Meta* meta;                     // by unit [B][qtiles][heads], or by the block where a unit begins [grid]
+  int by_unit;
   int* status;
 };
 
@@ -132,10 +135,10 @@ struct Cfg {
   static constexpr int RING_B = AW * STAGES * STAGE_B;
   static constexpr int JOIN_B = AW * ROWS * (D + 4) * 4;
   static constexpr int WORK_B = RING_B > JOIN_B ? RING_B : JOIN_B;
-  // With more than 128 accumulators a lane's queries and constants live in shared memory, and with 512 a tile is
-  // worked on 16 keys at a time, for the registers' sake.
+  // With 64 accumulators a lane or more its queries and constants live in shared memory, and with 128 of D = 256 a
+  // tile is worked on 16 keys at a time, for the registers' sake.
   static constexpr bool WIDE = D * NT >= 256;
-  static constexpr int HB = D * NT >= 512 ? 1 : 2;
+  static constexpr int HB = D == 256 && NT == 2 ? 1 : 2;
   static constexpr int QF_B = NT * NG * KW * 512;
   static constexpr int SMEM = WORK_B + (WIDE ? QF_B + ROWS * 4 * (NG + 3) : 0);
   static constexpr int BLOCKS = blocks_per_sm(D, NT);
@@ -192,22 +195,28 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
   using C = Cfg<D, NG, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t scan[AW + 2];
+  __shared__ Seq first_seq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- which tiles are ours ----
   int64_t at, stop, base = 0;       // tiles [at, stop) of all units; base: the first tile of sequence b
   int64_t b = 0;
   Seq s;
-  int64_t total = 0;
+  int64_t each = 0, extra = 0;      // every block has `each` tiles, the first `extra` of them one more
   if constexpr (SPLIT) {
     // total tiles, then the sequence that holds our first tile: each thread
     // sums the costs of a contiguous share of the sequences
     const int64_t per = (a.B + AW * 32 - 1) / (AW * 32);
     const int64_t b0 = min((int64_t)tid * per, a.B), b1 = min(b0 + per, a.B);
     int64_t mine = 0;
-    for (int64_t i = b0; i < b1; ++i) mine += seq_cost(a, load_seq(a, i, C::ROWS));
-    int64_t inc = mine;
+    for (int64_t i = b0; i < b1; ++i) {
+      s = load_seq(a, i, C::ROWS);
+      mine += seq_cost(a, s);
+    }
+    int64_t inc = mine, total = 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
@@ -222,29 +231,34 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
       total += scan[w];
     }
     inc += before;
-    const int64_t each = total / gridDim.x, extra = total % gridDim.x;
+    if (total >> 32) {
+      each = total / gridDim.x;
+      extra = total % gridDim.x;
+    } else {
+      each = (uint32_t)total / gridDim.x;
+      extra = (uint32_t)total % gridDim.x;
+    }
     at = each * blockIdx.x + min((int64_t)blockIdx.x, extra);
     stop = at + each + (blockIdx.x < extra ? 1 : 0);
-    if (tid == 0) {
-      Meta none{};
-      a.meta[blockIdx.x] = none;
-    }
+    if (tid == 0 && !a.by_unit) a.meta[blockIdx.x] = Meta{};
     if (at >= stop) return;
     if (at >= inc - mine && at < inc) {
-      int64_t sum = inc - mine;
-      int64_t i = b0;
-      for (;; ++i) {
-        const int64_t c = seq_cost(a, load_seq(a, i, C::ROWS));
-        if (at < sum + c) break;
-        sum += c;
+      int64_t sum = inc - mine, i = b0;
+      if (per > 1) {
+        for (;; ++i) {
+          s = load_seq(a, i, C::ROWS);
+          if (at < sum + seq_cost(a, s)) break;
+          sum += seq_cost(a, s);
+        }
       }
+      first_seq = s;
       scan[AW] = i;
       scan[AW + 1] = sum;
     }
     __syncthreads();
     b = scan[AW];
     base = scan[AW + 1];
-    s = load_seq(a, b, C::ROWS);
+    s = first_seq;
   } else {
     const int64_t per_b = (int64_t)a.qtiles * a.heads;
     b = blockIdx.x / per_b;
@@ -279,7 +293,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
       base += seq_cost(a, s);
       s = load_seq(a, ++b, C::ROWS);
     }
-    const int unit = (int)((at - base) / s.tiles);
+    const int unit = (at - base) >> 32 ? (int)((at - base) / s.tiles) : (int)((uint32_t)(at - base) / (uint32_t)s.tiles);
     const int64_t u0 = base + (int64_t)unit * s.tiles;
     const int first_tile = (int)(at - u0);
     const int last_tile = (int)min((int64_t)s.tiles, stop - u0);
@@ -345,26 +359,28 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
       cp_async_commit();
       put = put == ring + (C::STAGES - 1) * C::STAGE_B ? ring : put + C::STAGE_B;
     };
-#pragma unroll
-    for (int k = 0; k < C::STAGES - 1; ++k) issue(k);
-
     // ---- query fragments: column g of n-tile nt is row row0 + 8 nt + g ----
     struct Query {
       uint4 f[NG][C::KW];          // (low codes' pair, pair; high codes' pair, pair) of a key word
       float c, sum[NG];            // factor of the products, scaled sums over the groups
     };
-    auto load_query = [&](int nt) -> Query {
-      Query q;
+    auto fetch_query = [&](int nt, Query& q) {
       const int r = row0 + min(8 * nt + g, rows - 1);
       const int tok = r / a.rep, hr = r - tok * a.rep;
       const __half* qp = a.q + (s.first + tok) * a.ld_q + (int64_t)(head * a.rep + hr) * D;
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+        for (int i = 0; i < C::KW; ++i)
+          q.f[gr][i] = *reinterpret_cast<const uint4*>(qp + gr * C::G + t * (C::G / 4) + 8 * i);
+    };
+    auto finish_query = [&](Query& q) {
       float top = 0.0f;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         q.sum[gr] = 0.0f;
 #pragma unroll
         for (int i = 0; i < C::KW; ++i) {
-          q.f[gr][i] = *reinterpret_cast<const uint4*>(qp + gr * C::G + t * (C::G / 4) + 8 * i);
           const uint32_t* w = reinterpret_cast<const uint32_t*>(&q.f[gr][i]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -397,8 +413,13 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
                                   pack_h2(d01.y * f1, d45.y * f1), pack_h2(d23.y * f1, d67.y * f1));
         }
       q.c = sc * pow2f(20 - e);
-      return q;
     };
+    // (the loads of the queries go out before the copies, which wait for their pages)
+    Query q0;
+    if (!C::WIDE || warp < NT) fetch_query(C::WIDE ? warp : 0, q0);
+#pragma unroll
+    for (int k = 0; k < C::STAGES - 1; ++k) issue(k);
+
     // last and first key that row r (of the unit's n-tiles) sees
     auto last_key = [&](int r) { return s.len - s.n + (row0 + min(r, rows - 1)) / a.rep; };
     auto first_key = [&](int hi) { return a.window > 0 ? (int)max((int64_t)0, (int64_t)hi + 1 - a.window) : 0; };
@@ -409,8 +430,11 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
     uint4* const qsm = reinterpret_cast<uint4*>(smem + C::WORK_B);   // or in shared memory: [nt][group][word][lane],
     float* const csm = reinterpret_cast<float*>(smem + C::WORK_B + C::QF_B);   // [factor, sums, last, first][row]
     if constexpr (C::WIDE) {
-      for (int nt = warp; nt < NT; nt += AW) {
-        const Query q = load_query(nt);
+      static_assert(NT <= AW, "a warp prepares one tile of queries");
+      if (warp < NT) {
+        const int nt = warp;
+        finish_query(q0);
+        const Query& q = q0;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
 #pragma unroll
@@ -428,7 +452,9 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
     } else {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const Query q = load_query(nt);
+        if (nt > 0) fetch_query(nt, q0);
+        finish_query(q0);
+        const Query& q = q0;
         const int src = 8 * t;             // lane of row 2t
         cfr[nt] = p2(__shfl_sync(0xffffffffu, q.c, src), __shfl_sync(0xffffffffu, q.c, src + 4));
 #pragma unroll
@@ -767,85 +793,108 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
         }
       }
     }
-    if (SPLIT && !whole && first_tile == 0 && tid == 0) {
-      // the unit goes on in the blocks whose ranges cover its last tile
-      const int64_t each = total / gridDim.x, extra = total % gridDim.x;
-      const int64_t last = u0 + s.tiles - 1;
-      const int64_t big = (each + 1) * extra;
-      const int64_t owner = last < big ? last / (each + 1) : extra + (last - big) / each;
-      Meta mm;
-      mm.parts = (int32_t)(owner - blockIdx.x + 1) | (at != at0 ? 1 << 30 : 0);
-      mm.b = (int32_t)b;
-      mm.head = head;
-      mm.qt = qt;
-      a.meta[blockIdx.x] = mm;
+    if (SPLIT && first_tile == 0 && tid == 0 && (!whole || a.by_unit)) {
+      Meta mm{};
+      if (!whole) {
+        // the unit goes on in the blocks whose ranges cover its last tile
+        const int64_t last = u0 + s.tiles - 1, big = (each + 1) * extra;
+        const int64_t owner = last < big ? last / (each + 1) : extra + (last - big) / each;
+        mm.parts = (int32_t)(owner - blockIdx.x + 1);
+        mm.block = (int32_t)blockIdx.x;
+        mm.slot = at != at0 ? 1 : 0;
+        mm.b = (int32_t)b;
+        mm.head = head;
+        mm.qt = qt;
+      }
+      a.meta[a.by_unit ? (b * a.qtiles + qt) * a.heads + head : (int64_t)blockIdx.x] = mm;
     }
     at = u0 + last_tile;
     __syncthreads();                      // the ring is written again
   }
 }
 
-// Joins the units that fell into several blocks' ranges: block x joins the one
-// that begins (and does not end) in block x's range.
+// Joins a unit that fell into several blocks' ranges.  With gridDim.y = 1 a block takes all rows of a unit at a time, a
+// thread four dims of a row; with one block a row (few units, so many parts each) the threads share the parts.
 template <int D, int NT>
-__global__ void __launch_bounds__(128) attn_kv4_join_kernel(const AttnParams a) {
-  constexpr int ROWS = 8 * NT, JS = D + 4, LANES = D / 4;
+__global__ void __launch_bounds__(256) attn_kv4_join_kernel(const AttnParams a) {
+  constexpr int ROWS = 8 * NT, JS = D + 4, LANES = D / 4, SUBS = 256 / LANES;
+  __shared__ float sums[SUBS], red[8];
+  __shared__ float4 acc[256];
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (a.by_unit) {
+    // units that do not exist (a short sequence of queries) have no meta
+    const int qt = blockIdx.x / a.heads % a.qtiles;
+    if (qt > 0 && qt >= load_seq(a, blockIdx.x / (a.heads * a.qtiles), ROWS).qtiles) return;
+    if (qt == 0 && load_seq(a, blockIdx.x / (a.heads * a.qtiles), ROWS).n == 0) return;
+  }
   const Meta mm = a.meta[blockIdx.x];
-  const int n = mm.parts & 0x3fffffff;
+  const int n = mm.parts;
   if (n == 0) return;
-  const int64_t x0 = blockIdx.x;
-  const int64_t slot0 = 2 * x0 + (mm.parts >> 30 & 1);
   const Seq s = load_seq(a, mm.b, ROWS);
   const int row0 = mm.qt * ROWS, rows = min(ROWS, s.n * a.rep - row0);
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    auto part = [&](int i) { return a.parts + ((i == 0 ? slot0 : 2 * (x0 + i)) * ROWS + r) * JS; };
-    __shared__ float red[4], sums[128 / LANES];
-    __shared__ float4 acc[128];
-    float mt = M_NONE;
-    for (int i = threadIdx.x; i < n; i += 128) mt = fmaxf(mt, part(i)[D]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mt;
-    __syncthreads();
-    mt = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const int d = (threadIdx.x % LANES) * 4, sub = threadIdx.x / LANES;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float sum = 0.0f;
+  const int d = (threadIdx.x % LANES) * 4, sub = threadIdx.x / LANES;
+  auto part = [&](int i, int r) { return a.parts + ((2 * (int64_t)(mm.block + i) + (i == 0 ? mm.slot : 0)) * ROWS + r) * JS; };
+  auto store = [&](int r, float4 v, float sum, float mt) {
+    const int tok = (row0 + r) / a.rep, hr = row0 + r - tok * a.rep;
+    const int64_t orow = (s.first + tok) * (int64_t)(a.heads * a.rep) + mm.head * a.rep + hr;
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    uint2 h;
+    h.x = pack_h2(v.x * inv, v.y * inv);
+    h.y = pack_h2(v.z * inv, v.w * inv);
+    *reinterpret_cast<uint2*>(a.out + orow * D + d) = h;
+    if (a.lse && d == 0) a.lse[orow] = sum > 0.0f ? (mt + log2f(sum)) * LN2 : -INFINITY;
+  };
+  auto add = [&](const float* p, float mt, float4& v, float& sum) {
+    const float f = ex2(p[D] - mt);
+    const float4 x = *reinterpret_cast<const float4*>(p + d);
+    v.x = fmaf(f, x.x, v.x);
+    v.y = fmaf(f, x.y, v.y);
+    v.z = fmaf(f, x.z, v.z);
+    v.w = fmaf(f, x.w, v.w);
+    sum = fmaf(f, p[D + 1], sum);
+  };
+  if (gridDim.y == 1) {
+    for (int r = sub; r < rows; r += SUBS) {
+      float mt = M_NONE;
 #pragma unroll 4
-    for (int i = sub; i < n; i += 128 / LANES) {
-      const float* p = part(i);
-      const float f = ex2(p[D] - mt);
-      const float4 x = *reinterpret_cast<const float4*>(p + d);
-      v.x = fmaf(f, x.x, v.x);
-      v.y = fmaf(f, x.y, v.y);
-      v.z = fmaf(f, x.z, v.z);
-      v.w = fmaf(f, x.w, v.w);
-      sum = fmaf(f, p[D + 1], sum);
+      for (int i = 0; i < n; ++i) mt = fmaxf(mt, part(i, r)[D]);
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sum = 0.0f;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) add(part(i, r), mt, v, sum);
+      store(r, v, sum, mt);
     }
-    acc[threadIdx.x] = v;
-    if (d == 0) sums[sub] = sum;
-    __syncthreads();
-    if (sub == 0) {
-      sum = sums[0];
-      for (int i = 1; i < 128 / LANES; ++i) {
-        const float4 x = acc[threadIdx.x + i * LANES];
-        v.x += x.x;
-        v.y += x.y;
-        v.z += x.z;
-        v.w += x.w;
-        sum += sums[i];
-      }
-      const int tok = (row0 + r) / a.rep, hr = row0 + r - tok * a.rep;
-      const int64_t orow = (s.first + tok) * (int64_t)(a.heads * a.rep) + mm.head * a.rep + hr;
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-      uint2 h;
-      h.x = pack_h2(v.x * inv, v.y * inv);
-      h.y = pack_h2(v.z * inv, v.w * inv);
-      *reinterpret_cast<uint2*>(a.out + orow * D + d) = h;
-      if (a.lse && d == 0) a.lse[orow] = sum > 0.0f ? (mt + log2f(sum)) * LN2 : -INFINITY;
+    return;
+  }
+  const int r = blockIdx.y;
+  if (r >= rows) return;
+  float mt = M_NONE;
+  for (int i = threadIdx.x; i < n; i += 256) mt = fmaxf(mt, part(i, r)[D]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mt;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mt = fmaxf(mt, red[i]);
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int i = sub; i < n; i += SUBS) add(part(i, r), mt, v, sum);
+  acc[threadIdx.x] = v;
+  if (d == 0) sums[sub] = sum;
+  __syncthreads();
+  if (sub == 0) {
+    sum = sums[0];
+    for (int i = 1; i < SUBS; ++i) {
+      const float4 x = acc[threadIdx.x + i * LANES];
+      v.x += x.x;
+      v.y += x.y;
+      v.z += x.z;
+      v.w += x.w;
+      sum += sums[i];
     }
-    __syncthreads();
+    store(r, v, sum, mt);
   }
 }
 
@@ -860,37 +909,48 @@ inline int row_tiles(int64_t rep, int64_t max_q, int64_t D) {
 // (and joined), or one block takes each unit.
 inline bool split(int64_t max_len) { return max_len > DIRECT_LEN; }
 
+// Few units have many parts each: a block of the join takes one row of one.
+constexpr int64_t FEW_UNITS = 32;
+
+inline size_t meta_bytes(size_t grid) { return (grid * sizeof(Meta) + 15) / 16 * 16; }
+
 inline int split_grid(int64_t D, int nt) { return sm_count() * blocks_per_sm((int)D, nt); }
 
-template <int D, int NG, int NT>
-cudaError_t launch(const AttnParams& p, const AttnKv4Args& a, cudaStream_t stream) {
-  using C = Cfg<D, NG, NT>;
-  if (!split(a.max_len)) {
-    const int64_t units = a.B * p.qtiles * p.heads;
-    if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
-    auto kern = attn_kv4_kernel<D, NG, NT, false>;
-    cudaError_t e = set_smem_once(kern, C::SMEM);
-    if (e != cudaSuccess) return e;
-    kern<<<(unsigned)units, AW * 32, C::SMEM, stream>>>(p);
-    return cudaGetLastError();
-  }
-  auto kern = attn_kv4_kernel<D, NG, NT, true>;
-  cudaError_t e = set_smem_once(kern, C::SMEM);
-  if (e != cudaSuccess) return e;
-  const int grid = split_grid(D, NT);
-  kern<<<grid, AW * 32, C::SMEM, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+// Programmatic dependent launch: a kernel's blocks come up while the one before it ends, and wait for it.
+template <class K>
+cudaError_t launch_after(K kern, dim3 grid, int threads, int smem, cudaStream_t stream, const AttnParams& p) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, C::ROWS);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_kv4_join_kernel<D, NT>, p);
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int D, int NG, int NT>
+cudaError_t launch(const AttnParams& p, const AttnKv4Args& a, cudaStream_t stream) {
+  using C = Cfg<D, NG, NT>;
+  const int64_t units = a.B * p.qtiles * p.heads;
+  if (!split(a.max_len)) {
+    if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
+    auto kern = attn_kv4_kernel<D, NG, NT, false>;
+    cudaError_t e = set_smem_once(kern, C::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_after(kern, dim3((unsigned)units), AW * 32, C::SMEM, stream, p);
+  }
+  auto kern = attn_kv4_kernel<D, NG, NT, true>;
+  cudaError_t e = set_smem_once(kern, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int grid = split_grid(D, NT);
+  e = launch_after(kern, dim3((unsigned)grid), AW * 32, C::SMEM, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_after(attn_kv4_join_kernel<D, NT>, p.by_unit ? dim3((unsigned)units, C::ROWS) : dim3((unsigned)grid), 256, 0,
+                      stream, p);
 }
 
 template <int D, int NG>
@@ -908,7 +968,7 @@ size_t attn_kv4_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t 
   if (!split(max_len)) return 0;
   const int nt = row_tiles(q_heads / kv_heads, max_q, D);
   const size_t grid = (size_t)split_grid(D, nt);
-  return grid * sizeof(Meta) + 2 * grid * 8 * nt * (D + 4) * sizeof(float);
+  return meta_bytes(grid) + 2 * grid * 8 * nt * (D + 4) * sizeof(float);
 }
 
 cudaError_t launch_attn_kv4(const AttnKv4Args& a, cudaStream_t stream) {
@@ -944,7 +1004,8 @@ cudaError_t launch_attn_kv4(const AttnKv4Args& a, cudaStream_t stream) {
   if (split(a.max_len)) {
     const size_t grid = (size_t)split_grid(a.pool.D, rows / 8);
     p.meta = static_cast<Meta*>(a.workspace);
-    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + grid * sizeof(Meta));
+    p.by_unit = a.B * p.qtiles * p.heads <= FEW_UNITS;
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + meta_bytes(grid));
   }
   const int D = a.pool.D, ng = D / a.pool.group;
   if (D == 64) return ng == 1 ? launch_nt<64, 1>(p, a, stream) : launch_nt<64, 2>(p, a, stream);
