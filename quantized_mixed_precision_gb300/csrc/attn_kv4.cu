@@ -3,7 +3,7 @@
 // A value of the cache is x = low + step * u with a code u in 0..15 for each
 // group of dims, so for a query q and weights p
 //   q . k[t]        = sum_g step[t, g] * (sum_{d in g} q[d] u[t, d]) + low[t, g] * (sum_{d in g} q[d])
-//   sum_t p[t] v[t] = sum_t (p[t] step[t, g]) u[t, d] + sum_t p[t] low[t, g]
+//   sum_t p[t] v[t] = sum_t (p[t] step[t, g]) (u[t, d] - 7.5) + sum_t p[t] (low[t, g] + 7.5 step[t, g])
 // and the tensor cores multiply the codes themselves: as fp16 subnormals they
 // need one LOP3 per two codes and no arithmetic (kv4_device.cuh).
 //
@@ -13,6 +13,16 @@
 // and none of an MMA is idle at q_heads / kv_heads = 8.  Scores leave the
 // first MMA with a key per lane row, where its step and low are applied, and
 // movmatrix turns the weights into the second MMA's B operand.
+//
+// Two things keep the second sum exact where it cancels.  The weights p step are
+// rounded to fp16, so the codes count from their middle: from 0, the weights'
+// errors met values of 2.5 to 5 times the size, and the result was 2.4 to 5 times
+// as far off.  And codes are not negative, while the tensor cores truncate as
+// they add: every second 16 keys enter as -(p step) (15 - u), which turns about
+// the middle and costs nothing (a LOP3 takes the complement), so that the
+// accumulators stay as small as the result instead of growing with the sum of
+// the weights (128k keys: 7e-4 off without, 2e-4 being the rounding of the result).
+// What turns them back, 7.5 sum_t +-(p step), comes from an MMA with a constant A.
 //
 // Work is split over warps by tiles of 32 keys.  A unit is one (sequence,
 // kv head, block of query rows); the blocks of the grid take equal contiguous
@@ -489,6 +499,10 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
 
     float o[NT][NG][C::MT][4];
     P2 lowacc[NT][NG], m[NT], l[NT];      // columns 2t, 2t + 1
+    float wsum[NT][NG][4];                // 7.5 times the sums of the signed weights (all rows alike)
+    uint32_t mid[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("mov.b32 %0, 0x47804780;" : "=r"(mid[i]));
     float vf = pow2f(30);                 // power of two that the values' steps carry into fp16
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -496,6 +510,8 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         lowacc[nt][gr] = p2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wsum[nt][gr][j] = 0.0f;
 #pragma unroll
         for (int i = 0; i < C::MT; ++i)
 #pragma unroll
@@ -514,7 +530,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
       cp_async_wait<C::STAGES - 2>();
       __syncwarp();
       issue(k + C::STAGES - 1);
-#pragma unroll 1
+#pragma unroll
       for (int h0 = 0; h0 < 2; h0 += HB) {
       const uint32_t sth = st + 16 * h0 * C::R;
       const uint8_t* sp = smem + (sth - smem_u32(smem));
@@ -659,6 +675,8 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
           for (int gr = 0; gr < NG; ++gr) {
             lowacc[nt][gr] = mul2(lowacc[nt][gr], ff);
 #pragma unroll
+            for (int e = 0; e < 4; ++e) wsum[nt][gr][e] *= f[e & 1] * fv;
+#pragma unroll
             for (int i = 0; i < C::MT; ++i)
 #pragma unroll
               for (int e = 0; e < 4; e += 2) {
@@ -674,6 +692,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
       // ---- weights, their sums, and the second product ----
 #pragma unroll
       for (int h = 0; h < HB; ++h) {
+        const bool turned = (h0 + h) & 1;
         uint32_t pf[NT][NG][2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -681,8 +700,9 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
             const float2 v = unpack_h2(vp[h][r][gr]);
-            vs[gr] = p2(v.x * vf, v.x * vf);
-            vl[gr] = p2(v.y, v.y);
+            const float w = v.x * (turned ? -vf : vf), low = fmaf(7.5f, v.x, v.y);
+            vs[gr] = p2(w, w);
+            vl[gr] = p2(low, low);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -699,6 +719,11 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
           }
         }
 #pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr)
+            mma_f16(wsum[nt][gr], mid[0], mid[1], mid[2], mid[3], pf[nt][gr][0], pf[nt][gr][1]);
+#pragma unroll
         for (int c = 0; c < C::PER; c += 2) {
           // 16-byte pieces c and c + 1 (32 dims each) of 16 tokens
           uint32_t w[4];
@@ -707,10 +732,10 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
           for (int x = 0; x < 4; ++x) {
             const int gr = (c + x / 2) * 32 / C::G, i = ((c + x / 2) * 32 % C::G) / 16 + (x & 1);
             const uint32_t e = w[x] >> 8;
+            const uint32_t a0 = (turned ? ~w[x] : w[x]) & CODE_LO, a1 = (turned ? ~w[x] : w[x]) & CODE_HI;
+            const uint32_t a2 = (turned ? ~e : e) & CODE_LO, a3 = (turned ? ~e : e) & CODE_HI;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16(o[nt][gr][i], w[x] & CODE_LO, w[x] & CODE_HI, e & CODE_LO, e & CODE_HI, pf[nt][gr][0],
-                      pf[nt][gr][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][gr][i], a0, a1, a2, a3, pf[nt][gr][0], pf[nt][gr][1]);
           }
         }
       }
@@ -738,6 +763,8 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) low[gr] += __shfl_xor_sync(0xffffffffu, low[gr], x);
         }
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) low[gr] = fmaf(wsum[nt][gr][j], -1.0f / vf, low[gr]);
         float* row = js + (warp * C::ROWS + 8 * nt + 2 * t + j) * JS;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr)
