@@ -22,7 +22,7 @@
 // the middle and costs nothing (a LOP3 takes the complement), so that the
 // accumulators stay as small as the result instead of growing with the sum of
 // the weights (128k keys: 7e-4 off without, 2e-4 being the rounding of the result).
-// What turns them back, 7.5 sum_t +-(p step), comes from an MMA with a constant A.
+// What turns them back, 7.5 sum_t +-(p step), is summed beside from the rounded weights.
 //
 // Work is split over warps by tiles of 32 keys.  A unit is one (sequence,
 // kv head, block of query rows); the blocks of the grid take equal contiguous
@@ -46,11 +46,13 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float M_NONE = -1e30f;  // running maximum before any key
 
-// A unit that has to be joined: its first block, whether that holds it in its second slot, and its blocks
+// A unit that has to be joined: its blocks, the first of them, whether that holds it in its second slot, and what the
+// join needs of the sequence
 struct Meta {
   int32_t parts;       // 0: nothing to join
   int32_t block, slot;
-  int32_t b, head, qt;
+  int32_t head, row0, rows;
+  int64_t first;
 };
 
 struct AttnParams {
@@ -498,20 +500,16 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
     };
 
     float o[NT][NG][C::MT][4];
-    P2 lowacc[NT][NG], m[NT], l[NT];      // columns 2t, 2t + 1
-    float wsum[NT][NG][4];                // 7.5 times the sums of the signed weights (all rows alike)
-    uint32_t mid[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) asm volatile("mov.b32 %0, 0x47804780;" : "=r"(mid[i]));
+    P2 mid[NT][NG], m[NT], l[NT];         // columns 2t, 2t + 1; mid: what the codes' middles add, times vf
+    P2 back[NR][NG];                      // - 7.5 times the signed weights (with many rows, for the registers' sake, in mid)
     float vf = pow2f(30);                 // power of two that the values' steps carry into fp16
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt] = l[nt] = p2(0.0f, 0.0f);
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        lowacc[nt][gr] = p2(0.0f, 0.0f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) wsum[nt][gr][j] = 0.0f;
+        mid[nt][gr] = p2(0.0f, 0.0f);
+        if (!C::WIDE) back[nt % NR][gr] = p2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < C::MT; ++i)
 #pragma unroll
@@ -673,9 +671,8 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
             for (int r = 0; r < 2; ++r) sv[h][nt][r] = add2(sv[h][nt][r], down);
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
-            lowacc[nt][gr] = mul2(lowacc[nt][gr], ff);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) wsum[nt][gr][e] *= f[e & 1] * fv;
+            mid[nt][gr] = mul2(mid[nt][gr], of);
+            if (!C::WIDE) back[nt % NR][gr] = mul2(back[nt % NR][gr], of);
 #pragma unroll
             for (int i = 0; i < C::MT; ++i)
 #pragma unroll
@@ -700,7 +697,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
             const float2 v = unpack_h2(vp[h][r][gr]);
-            const float w = v.x * (turned ? -vf : vf), low = fmaf(7.5f, v.x, v.y);
+            const float w = v.x * (turned ? -vf : vf), low = vf * fmaf(7.5f, v.x, v.y);
             vs[gr] = p2(w, w);
             vl[gr] = p2(low, low);
           }
@@ -711,18 +708,16 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
             l[nt] = add2(l[nt], w);
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-              lowacc[nt][gr] = fma2(w, vl[gr], lowacc[nt][gr]);
               // the only rounding to 16 bits: weight times step, 2**-11 relative
               const float2 v = f2(mul2(w, vs[gr]));
-              pf[nt][gr][r] = movmatrix_trans(pack_h2(v.x, v.y));
+              const uint32_t w16 = pack_h2(v.x, v.y);
+              mid[nt][gr] = fma2(w, vl[gr], mid[nt][gr]);
+              P2& to = C::WIDE ? mid[nt][gr] : back[nt % NR][gr];
+              to = fma_h2(w16, 0xc780u, to);       // 0xc780: -7.5
+              pf[nt][gr][r] = movmatrix_trans(w16);
             }
           }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr)
-            mma_f16(wsum[nt][gr], mid[0], mid[1], mid[2], mid[3], pf[nt][gr][0], pf[nt][gr][1]);
 #pragma unroll
         for (int c = 0; c < C::PER; c += 2) {
           // 16-byte pieces c and c + 1 (32 dims each) of 16 tokens
@@ -748,7 +743,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
     __syncthreads();                      // every warp is done with its ring
     float* const js = reinterpret_cast<float*>(smem);
     constexpr int JS = D + 4;             // floats of a row: D values, maximum, sum, padding
-    const float back = pow2f(24) / vf;
+    const float unit_v = pow2f(24) / vf;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 mm = f2(m[nt]), ll = f2(l[nt]);
@@ -756,15 +751,16 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
       for (int j = 0; j < 2; ++j) {
         float sum = j ? ll.y : ll.x, low[NG];
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) low[gr] = j ? f2(lowacc[nt][gr]).y : f2(lowacc[nt][gr]).x;
+        for (int gr = 0; gr < NG; ++gr) {
+          const float2 x = f2(C::WIDE ? mid[nt][gr] : add2(mid[nt][gr], back[nt % NR][gr]));
+          low[gr] = (j ? x.y : x.x) / vf;
+        }
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
           sum += __shfl_xor_sync(0xffffffffu, sum, x);
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) low[gr] += __shfl_xor_sync(0xffffffffu, low[gr], x);
         }
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr) low[gr] = fmaf(wsum[nt][gr][j], -1.0f / vf, low[gr]);
         float* row = js + (warp * C::ROWS + 8 * nt + 2 * t + j) * JS;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr)
@@ -772,8 +768,8 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
           for (int i = 0; i < C::MT; ++i) {
             // tile i of a group: byte g of its i-th 8, dims 2g and 2g + 1
             const int d = gr * C::G + 16 * i + 2 * g;
-            *reinterpret_cast<float2*>(row + d) = make_float2(fmaf(o[nt][gr][i][j], back, low[gr]),
-                                                              fmaf(o[nt][gr][i][2 + j], back * 0.0625f, low[gr]));
+            *reinterpret_cast<float2*>(row + d) = make_float2(fmaf(o[nt][gr][i][j], unit_v, low[gr]),
+                                                              fmaf(o[nt][gr][i][2 + j], unit_v * 0.0625f, low[gr]));
           }
         if (g == 0) {
           row[D] = sum > 0.0f ? (j ? mm.y : mm.x) : M_NONE;
@@ -829,9 +825,10 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
         mm.parts = (int32_t)(owner - blockIdx.x + 1);
         mm.block = (int32_t)blockIdx.x;
         mm.slot = at != at0 ? 1 : 0;
-        mm.b = (int32_t)b;
         mm.head = head;
-        mm.qt = qt;
+        mm.row0 = row0;
+        mm.rows = rows;
+        mm.first = s.first;
       }
       a.meta[a.by_unit ? (b * a.qtiles + qt) * a.heads + head : (int64_t)blockIdx.x] = mm;
     }
@@ -845,26 +842,23 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
 template <int D, int NT>
 __global__ void __launch_bounds__(256) attn_kv4_join_kernel(const AttnParams a) {
   constexpr int ROWS = 8 * NT, JS = D + 4, LANES = D / 4, SUBS = 256 / LANES;
-  __shared__ float sums[SUBS], red[8];
+  __shared__ float2 sums[SUBS];
   __shared__ float4 acc[256];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (a.by_unit) {
-    // units that do not exist (a short sequence of queries) have no meta
+  if (a.by_unit && a.cu_q) {
+    // units that do not exist (a sequence with fewer query tokens) have no meta
     const int qt = blockIdx.x / a.heads % a.qtiles;
-    if (qt > 0 && qt >= load_seq(a, blockIdx.x / (a.heads * a.qtiles), ROWS).qtiles) return;
-    if (qt == 0 && load_seq(a, blockIdx.x / (a.heads * a.qtiles), ROWS).n == 0) return;
+    if (qt >= load_seq(a, blockIdx.x / (a.heads * a.qtiles), ROWS).qtiles) return;
   }
   const Meta mm = a.meta[blockIdx.x];
-  const int n = mm.parts;
+  const int n = mm.parts, row0 = mm.row0, rows = mm.rows;
   if (n == 0) return;
-  const Seq s = load_seq(a, mm.b, ROWS);
-  const int row0 = mm.qt * ROWS, rows = min(ROWS, s.n * a.rep - row0);
   const int d = (threadIdx.x % LANES) * 4, sub = threadIdx.x / LANES;
   auto part = [&](int i, int r) { return a.parts + ((2 * (int64_t)(mm.block + i) + (i == 0 ? mm.slot : 0)) * ROWS + r) * JS; };
   auto store = [&](int r, float4 v, float sum, float mt) {
     const int tok = (row0 + r) / a.rep, hr = row0 + r - tok * a.rep;
-    const int64_t orow = (s.first + tok) * (int64_t)(a.heads * a.rep) + mm.head * a.rep + hr;
+    const int64_t orow = (mm.first + tok) * (int64_t)(a.heads * a.rep) + mm.head * a.rep + hr;
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     uint2 h;
     h.x = pack_h2(v.x * inv, v.y * inv);
@@ -872,56 +866,67 @@ __global__ void __launch_bounds__(256) attn_kv4_join_kernel(const AttnParams a) 
     *reinterpret_cast<uint2*>(a.out + orow * D + d) = h;
     if (a.lse && d == 0) a.lse[orow] = sum > 0.0f ? (mt + log2f(sum)) * LN2 : -INFINITY;
   };
-  auto add = [&](const float* p, float mt, float4& v, float& sum) {
-    const float f = ex2(p[D] - mt);
-    const float4 x = *reinterpret_cast<const float4*>(p + d);
-    v.x = fmaf(f, x.x, v.x);
-    v.y = fmaf(f, x.y, v.y);
-    v.z = fmaf(f, x.z, v.z);
-    v.w = fmaf(f, x.w, v.w);
-    sum = fmaf(f, p[D + 1], sum);
+  // Adds parts i, i + by, ... of row r below n to (v, sum), four loads at a time, and keeps their maximum in mt.
+  auto add = [&](int i, int by, int r, float4& v, float& sum, float& mt) {
+    for (; i < n; i += 4 * by) {
+      float4 x[4];
+      float2 ml[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float* p = part(min(i + u * by, n - 1), r);
+        x[u] = *reinterpret_cast<const float4*>(p + d);
+        ml[u] = *reinterpret_cast<const float2*>(p + D);
+        if (i + u * by >= n) ml[u] = make_float2(M_NONE, 0.0f);
+      }
+      const float top = fmaxf(fmaxf(mt, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+      const float f0 = ex2(mt - top);
+      mt = top;
+      v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
+      sum *= f0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = i + u * by < n ? ex2(ml[u].x - top) : 0.0f;
+        v.x = fmaf(f, x[u].x, v.x);
+        v.y = fmaf(f, x[u].y, v.y);
+        v.z = fmaf(f, x[u].z, v.z);
+        v.w = fmaf(f, x[u].w, v.w);
+        sum = fmaf(f, ml[u].y, sum);
+      }
+    }
   };
   if (gridDim.y == 1) {
     for (int r = sub; r < rows; r += SUBS) {
-      float mt = M_NONE;
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) mt = fmaxf(mt, part(i, r)[D]);
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float sum = 0.0f;
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) add(part(i, r), mt, v, sum);
+      float sum = 0.0f, mt = M_NONE;
+      add(0, 1, r, v, sum, mt);
       store(r, v, sum, mt);
     }
     return;
   }
   const int r = blockIdx.y;
   if (r >= rows) return;
-  float mt = M_NONE;
-  for (int i = threadIdx.x; i < n; i += 256) mt = fmaxf(mt, part(i, r)[D]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mt;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) mt = fmaxf(mt, red[i]);
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float sum = 0.0f;
-#pragma unroll 4
-  for (int i = sub; i < n; i += SUBS) add(part(i, r), mt, v, sum);
+  float sum = 0.0f, mt = M_NONE;
+  add(sub, SUBS, r, v, sum, mt);
   acc[threadIdx.x] = v;
-  if (d == 0) sums[sub] = sum;
+  if (d == 0) sums[sub] = make_float2(mt, sum);
   __syncthreads();
   if (sub == 0) {
-    sum = sums[0];
+    float top = mt;
+    for (int i = 1; i < SUBS; ++i) top = fmaxf(top, sums[i].x);
+    const float f0 = ex2(mt - top);
+    v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
+    sum *= f0;
     for (int i = 1; i < SUBS; ++i) {
       const float4 x = acc[threadIdx.x + i * LANES];
-      v.x += x.x;
-      v.y += x.y;
-      v.z += x.z;
-      v.w += x.w;
-      sum += sums[i];
+      const float f = ex2(sums[i].x - top);
+      v.x = fmaf(f, x.x, v.x);
+      v.y = fmaf(f, x.y, v.y);
+      v.z = fmaf(f, x.z, v.z);
+      v.w = fmaf(f, x.w, v.w);
+      sum = fmaf(f, sums[i].y, sum);
     }
-    store(r, v, sum, mt);
+    store(r, v, sum, top);
   }
 }
 

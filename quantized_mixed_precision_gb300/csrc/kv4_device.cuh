@@ -107,6 +107,18 @@ __device__ __forceinline__ P2 fma2(P2 a, P2 b, P2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return r;
 }
+// Two fp16 values times the fp16 constant c (its bits) added to two fp32 sums
+__device__ __forceinline__ P2 fma_h2(uint32_t h, uint16_t c, P2 sum) {
+  float2 v = f2(sum);
+  asm("{\n\t.reg .f16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "fma.rn.f32.f16 %0, lo, %3, %0;\n\t"
+      "fma.rn.f32.f16 %1, hi, %3, %1;\n\t}"
+      : "+f"(v.x), "+f"(v.y)
+      : "r"(h), "h"(c));
+  return p2(v.x, v.y);
+}
+
 // 16-byte asynchronous copy to a shared-memory address
 __device__ __forceinline__ void cp_async_16_u(uint32_t smem_dst, const void* gmem_src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gmem_src) : "memory");
