@@ -262,3 +262,16 @@ def test_refusals():
         bq.bq_attn_kv4(q, codes, params, table, lens, max_len=1000)
     with pytest.raises(bq.BqError):
         bq.bq_attn_kv4(q, codes, params, table, lens, window=-1)
+
+
+@pytest.mark.parametrize("q", [1, 6])
+def test_long_sums_keep_their_precision(q):
+    """Over many keys the result is far smaller than the sum of the weights times the codes.  Its 2-norm error comes
+    from two roundings to fp16, each 2.1e-4 relative (the mean of uniform mantissas): of the result, and of the
+    independent weights, whose terms step * (code - 7.5) are 1.02 times the values' size: 1.43 * 2.1e-4 = 3.0e-4
+    together; 3.4e-4 leaves 10 % for the spread of a sample of 1024 values and more."""
+    c = make(30, [60001], [q], 8, 1, 128, 128, 128, qstd=1.0)
+    out, _ = check(c)
+    want, _, _, _ = D.attention(c["q"], c["codes"], c["params"], c["table"], c["lens"], c["cu"], 128 ** -0.5)
+    got = host(out).astype(np.float64)
+    assert np.linalg.norm(got - want) <= 3.4e-4 * np.linalg.norm(want)
