@@ -56,7 +56,7 @@ def _build_binding() -> None:
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *[x for d in include for x in ("-isystem", d)], os.path.join(CSRC, "decode_binding.cpp"), "-o", tmp,
-           "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath," + lib]
+           "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath," + lib]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for decode_binding.cpp:\n{r.stdout}\n{r.stderr}")

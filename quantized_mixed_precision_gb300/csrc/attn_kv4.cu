@@ -630,12 +630,17 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
         }
         most = fmaxf(most, fmaxf(top[nt].x, top[nt].y));
       }
+      {
+        __half2 most_step = __float2half2_rn(0.0f);
 #pragma unroll
-      for (int h = 0; h < HB; ++h)
+        for (int h = 0; h < HB; ++h)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+          for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr) step_top = fmaxf(step_top, fabsf(unpack_h2(vp[h][r][gr]).x));
+            for (int gr = 0; gr < NG; ++gr)
+              most_step = __hmax2(most_step, __habs2(*reinterpret_cast<const __half2*>(&vp[h][r][gr])));
+        step_top = __low2float(most_step);
+      }
       // (weight < 2**8, so weight * step * vf stays below fp16's 65504 while step * vf <= 240)
       if (__any_sync(0xffffffffu, fresh || most > 8.0f || step_top * vf > 240.0f)) {
 #pragma unroll

@@ -10,7 +10,7 @@
 // against libbq.so.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -64,7 +64,7 @@ inline bool integer(PyObject* o, int64_t& v) {
 }
 
 inline at::Tensor fresh(at::IntArrayRef shape, const at::Tensor& like, at::ScalarType type) {
-  return at::empty(shape, like.options().dtype(type));
+  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);   // (at::empty past its dispatcher)
 }
 
 inline void* raw_stream(int dev) { return c10::cuda::getCurrentCUDAStream(dev).stream(); }

@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(640, 1) gemv_group_kernel(const __half* __rest
         const float z = ZP ? p.y : 8.0f;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
+          if (c > 0 && M == 1) break;        // uniform; odd columns are not stored then
           const int i = 2 * r + c;
           const float u = fmaf(hi[i], 0.0625f, lo[i]);
           acc[i] = fmaf(p.x, fmaf(u, 16777216.0f, -z * (sum[0][i] + sum[1][i])), acc[i]);
