@@ -28,12 +28,14 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int SMEM_MAX = 227 * 1024;
 
+constexpr int SUM_BYTES = 2 * 16 * 4;        // sums of two rows over a stage's groups of 32
+
 struct StagePlan {
   int k_log2;        // k of a stage: 256 or 512
   int stages;        // of a warp's ring
   int groups;        // most groups a warp meets
   // ring, then (step, zero) of 16 rows for each of the warp's groups
-  int warp_bytes(int M) const { return stages * ((8 + 2 * M) << k_log2) + 64 * groups; }
+  int warp_bytes(int M) const { return stages * ((8 + 2 * M) << k_log2) + 64 * groups + SUM_BYTES; }
 };
 
 // XOR of the address bits of weight row r: loads of 16, 8 or 4 bytes of each
@@ -78,6 +80,9 @@ __global__ void __launch_bounds__(640, 1) gemv_group_kernel(const __half* __rest
   constexpr int SG = (1 << KLOG) / G;                    // groups of a stage
   constexpr int WB = 8 << KLOG;                          // bytes of a stage's weights
   constexpr int WROW = 1 << (KLOG - 1), XROW = 2 << KLOG;   // bytes of a row of weights, of X
+  // The sums of X over a group: with one or two rows (the long stages) from the pieces as they are put in order, else
+  // from an MMA with A = 1 beside each product.  That MMA cost 1.3 of 8.2 us at M = 1.
+  constexpr bool SUMS = KLOG == 9;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -85,8 +90,9 @@ __global__ void __launch_bounds__(640, 1) gemv_group_kernel(const __half* __rest
   const int ngroups = K / G, nst = (K + (1 << KLOG) - 1) >> KLOG;
   const int mine_n = nst > warp ? (nst - warp + warps - 1) / warps : 0;
   const int stage = WB + M * XROW;
-  uint8_t* const mine = smem + warp * (plan.stages * stage + 64 * plan.groups);
+  uint8_t* const mine = smem + warp * (plan.stages * stage + 64 * plan.groups + SUM_BYTES);
   uint32_t* const sz = reinterpret_cast<uint32_t*>(mine + plan.stages * stage);   // [group][16 rows] (scale, zero)
+  float* const xsum = reinterpret_cast<float*>(sz + 16 * plan.groups);            // [row of X][group of the stage]
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -155,6 +161,14 @@ __global__ void __launch_bounds__(640, 1) gemv_group_kernel(const __half* __rest
     for (int c = lane; c < M * (XROW / 16); c += 32) {
       uint4* const p = reinterpret_cast<uint4*>(st + WB) + c;
       const uint4 v = *p;
+      if constexpr (SUMS) {
+        // (whole warps come here; past K the pieces are stale, in groups that are not used)
+        float s = sum_h8(v);
+#pragma unroll
+        for (int d = 1; d < G / 8; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        const int m = c / (XROW / 16), at = c % (XROW / 16) ^ (m & 1) << 2;
+        if (c % (G / 8) == 0) xsum[m * SG + at / (G / 8)] = s;
+      }
       *p = inter ? make_uint4(v.x, v.z, v.y, v.w)
                  : make_uint4(prmt(v.x, v.z, 0x5410u), prmt(v.y, v.w, 0x5410u), prmt(v.x, v.z, 0x7632u),
                               prmt(v.y, v.w, 0x7632u));
@@ -184,7 +198,8 @@ __global__ void __launch_bounds__(640, 1) gemv_group_kernel(const __half* __rest
           w1[0] = *reinterpret_cast<const uint32_t*>(p + WB / 2);
         }
       }
-      float lo[4], hi[4], sum[2][4];
+      float lo[4], hi[4];
+      [[maybe_unused]] float sum[2][4];
 #pragma unroll
       for (int i = 0; i < WORDS; ++i) {
         // odd rows have the halves of each 128 bytes swapped
@@ -199,13 +214,17 @@ __global__ void __launch_bounds__(640, 1) gemv_group_kernel(const __half* __rest
         if (i == 0) {
           mma_f16_zero(lo, l0, l1, l2, l3, v.x, v.y);
           mma_f16_zero(hi, h0, h1, h2, h3, v.z, v.w);
-          mma_f16_zero(sum[0], mk.one[0], mk.one[1], mk.one[2], mk.one[3], v.x, v.y);
-          mma_f16_zero(sum[1], mk.one[0], mk.one[1], mk.one[2], mk.one[3], v.z, v.w);
+          if constexpr (!SUMS) {
+            mma_f16_zero(sum[0], mk.one[0], mk.one[1], mk.one[2], mk.one[3], v.x, v.y);
+            mma_f16_zero(sum[1], mk.one[0], mk.one[1], mk.one[2], mk.one[3], v.z, v.w);
+          }
         } else {
           mma_f16(lo, l0, l1, l2, l3, v.x, v.y);
           mma_f16(hi, h0, h1, h2, h3, v.z, v.w);
-          mma_f16(sum[0], mk.one[0], mk.one[1], mk.one[2], mk.one[3], v.x, v.y);
-          mma_f16(sum[1], mk.one[0], mk.one[1], mk.one[2], mk.one[3], v.z, v.w);
+          if constexpr (!SUMS) {
+            mma_f16(sum[0], mk.one[0], mk.one[1], mk.one[2], mk.one[3], v.x, v.y);
+            mma_f16(sum[1], mk.one[0], mk.one[1], mk.one[2], mk.one[3], v.z, v.w);
+          }
         }
       }
 #pragma unroll
@@ -217,7 +236,8 @@ __global__ void __launch_bounds__(640, 1) gemv_group_kernel(const __half* __rest
           if (c > 0 && M == 1) break;        // uniform; odd columns are not stored then
           const int i = 2 * r + c;
           const float u = fmaf(hi[i], 0.0625f, lo[i]);
-          acc[i] = fmaf(p.x, fmaf(u, 16777216.0f, -z * (sum[0][i] + sum[1][i])), acc[i]);
+          const float all = SUMS ? xsum[c * SG + j] : sum[0][i] + sum[1][i];
+          acc[i] = fmaf(p.x, fmaf(u, 16777216.0f, -z * all), acc[i]);
         }
       }
     }

@@ -119,6 +119,20 @@ __device__ __forceinline__ P2 fma_h2(uint32_t h, uint16_t c, P2 sum) {
   return p2(v.x, v.y);
 }
 
+// Sum of 8 fp16 values in fp32
+__device__ __forceinline__ float sum_h8(const uint4& v) {
+  float a = 0.0f, b = 0.0f;
+  asm("{\n\t.reg .f16 l0, h0, l1, h1, l2, h2, l3, h3;\n\t"
+      "mov.b32 {l0, h0}, %2;\n\tmov.b32 {l1, h1}, %3;\n\tmov.b32 {l2, h2}, %4;\n\tmov.b32 {l3, h3}, %5;\n\t"
+      "add.rn.f32.f16 %0, l0, %0;\n\tadd.rn.f32.f16 %1, h0, %1;\n\t"
+      "add.rn.f32.f16 %0, l1, %0;\n\tadd.rn.f32.f16 %1, h1, %1;\n\t"
+      "add.rn.f32.f16 %0, l2, %0;\n\tadd.rn.f32.f16 %1, h2, %1;\n\t"
+      "add.rn.f32.f16 %0, l3, %0;\n\tadd.rn.f32.f16 %1, h3, %1;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+  return a + b;
+}
+
 // 16-byte asynchronous copy to a shared-memory address
 __device__ __forceinline__ void cp_async_16_u(uint32_t smem_dst, const void* gmem_src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gmem_src) : "memory");
