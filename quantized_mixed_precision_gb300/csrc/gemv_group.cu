@@ -325,7 +325,8 @@ struct BlockCfg {
   static constexpr int W_B = GB_COLS * GB_SLAB / 2;
   static constexpr int SG = GB_SLAB / G;
   static constexpr int SUMS = ROWS * SG;                             // sums of X over a slab's groups
-  static constexpr int STEPS = GB_COLS * SG;                         // (step, zero) of a slab
+  static constexpr int SB = 8 / SG;                                  // slabs with 8 groups
+  static constexpr int STEPS = GB_COLS * 8;                          // (step, zero) of 8 groups
   static constexpr int RING = GB_XS * X_B + GB_WS * W_B + 2 * SUMS * 4 + 2 * STEPS * 4;
   static constexpr int ACC = ROWS * (GB_COLS + 4) * 4;               // partial results, for the cluster
   static constexpr int SMEM = RING > ACC ? RING : ACC;
@@ -358,7 +359,10 @@ __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
   const int part = blockIdx.x % parts, unit = blockIdx.x / parts;   // a cluster is the parts of a unit
   const int m0 = blockIdx.y * C::ROWS, rows = min(C::ROWS, M - m0);
   const int slabs = (K + GB_SLAB - 1) / GB_SLAB, ngroups = K / G;
-  const int s0 = (int)((int64_t)slabs * part / parts), s1 = (int)((int64_t)slabs * (part + 1) / parts);
+  // this part's slabs, in whole eights of groups
+  const int eights = (slabs + C::SB - 1) / C::SB;
+  const int s0 = (int)((int64_t)eights * part / parts) * C::SB;
+  const int s1 = min((int)((int64_t)eights * (part + 1) / parts) * C::SB, slabs);
   uint8_t* const xr = smem;
   uint8_t* const wr = smem + GB_XS * C::X_B;
   float* const sums = reinterpret_cast<float*>(wr + GB_WS * C::W_B);
@@ -404,8 +408,7 @@ __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
         const uint4 p = *at;
         if (ZP) {
           // a group's pieces are those of G / 8 neighbouring lanes, in whatever order
-          const float2 a = unpack_h2(p.x), b = unpack_h2(p.y), c = unpack_h2(p.z), d = unpack_h2(p.w);
-          float v = ((a.x + a.y) + (b.x + b.y)) + ((c.x + c.y) + (d.x + d.y));
+          float v = sum_h8(p);
 #pragma unroll
           for (int o = 1; o < G / 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o, 16);
           if (xc % (G / 8) == 0) to[r * C::SG + xc / (G / 8)] = v;
@@ -427,42 +430,55 @@ __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[r][nt][i] = 0.0f;
-  // (step, zero) of a column for the groups of a slab: loaded two slabs before they are used (a load takes longer than
-  // a slab), and passed on through shared memory
+  // (step, zero) of the block's columns, 8 groups at a time (16 bytes of a column; two bytes a load, as many sectors as
+  // the weights have, took 700 cycles a slab), loaded a whole eight before they are passed on through shared memory
   const size_t s_at = (size_t)min(unit * GB_COLS + (tid & 127), N - 1) * ngroups;
-  constexpr int PER = (C::SG + RG - 1) / RG;                // groups of a thread: with two warps along the rows, half
-  const int j0 = PER * (tid >> 7);
-  auto load_steps = [&](int s, uint32_t (&v)[PER]) {
+  const bool whole = (ngroups & 7) == 0;                    // 16-byte loads of 8 groups are aligned
+  uint4 es = make_uint4(0, 0, 0, 0), ez = es;
+  auto load_eight = [&](int e) {
+    if (tid >= GB_COLS || e * 8 >= ngroups || e * C::SB >= s1) return;
+    if (whole) {
+      es = __ldg(reinterpret_cast<const uint4*>(scale + s_at + e * 8));
+      if (ZP) ez = __ldg(reinterpret_cast<const uint4*>(zero + s_at + e * 8));
+      return;
+    }
+    uint32_t a[4], b[4];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int group = s * C::SG + j0 + j;
-      v[j] = 0;
-      if (s < s1 && j0 + j < C::SG && group < ngroups)
-        v[j] = ZP ? __ldg(scale + s_at + group) | (uint32_t)__ldg(zero + s_at + group) << 16 : __ldg(scale + s_at + group);
+    for (int i = 0; i < 4; ++i) {
+      const int g0 = min(e * 8 + 2 * i, ngroups - 1), g1 = min(e * 8 + 2 * i + 1, ngroups - 1);
+      a[i] = scale[s_at + g0] | (uint32_t)scale[s_at + g1] << 16;
+      if (ZP) b[i] = zero[s_at + g0] | (uint32_t)zero[s_at + g1] << 16;
+    }
+    es = make_uint4(a[0], a[1], a[2], a[3]);
+    if (ZP) ez = make_uint4(b[0], b[1], b[2], b[3]);
+  };
+  auto store_eight = [&](int e) {
+    if (tid >= GB_COLS) return;
+    uint32_t* const to = steps + (e & 1) * C::STEPS + tid;
+    const uint32_t a[4] = {es.x, es.y, es.z, es.w}, b[4] = {ez.x, ez.y, ez.z, ez.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      to[2 * i * GB_COLS] = prmt(a[i], b[i], 0x5410u);
+      to[(2 * i + 1) * GB_COLS] = prmt(a[i], b[i], 0x7632u);
     }
   };
-  auto store_steps = [&](int s, const uint32_t (&v)[PER]) {
-#pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (j0 + j < C::SG) steps[((s - s0) & 1) * C::STEPS + (j0 + j) * GB_COLS + (tid & 127)] = v[j];
-  };
-  uint32_t st0[PER], st1[PER];
-  load_steps(s0, st0);
-  load_steps(s0 + 1, st1);
+  load_eight(s0 / C::SB);
   cp_async_wait<2>();
   __syncthreads();
   ready(s0);
-  store_steps(s0, st0);
+  store_eight(s0 / C::SB);
+  load_eight(s0 / C::SB + 1);
 
-  // (two sets of registers take turns: a copy between them would wait for the load)
-  auto slab = [&](int s, const uint32_t (&have)[PER], uint32_t (&next)[PER]) {
-    load_steps(s + 2, next);
+  for (int s = s0; s < s1; ++s) {
     cp_async_wait<1>();                      // slab s + 1 has come
     __syncthreads();                         // ... for everybody, slab s is ready, and slab s - 1 has been read
     issue(s + 3);
     ready(s + 1);
-    store_steps(s + 1, have);
-    const uint32_t* const sp = steps + ((s - s0) & 1) * C::STEPS + wcol * 32 + g;
+    if ((s + 1) % C::SB == 0) {              // the next slab begins an eight: its steps, and the loads of the one after
+      store_eight((s + 1) / C::SB);
+      load_eight((s + 1) / C::SB + 1);
+    }
+    const uint32_t* const sp = steps + ((s / C::SB) & 1) * C::STEPS + s % C::SB * C::SG * GB_COLS + wcol * 32 + g;
     const uint8_t* const xs = xr + ((s - s0) & (GB_XS - 1)) * C::X_B + wrow * NT * 8 * 256;
     const float* const sum = sums + ((s - s0) & 1) * C::SUMS + wrow * NT * 8 * C::SG;
     const uint8_t* const ws = wr + ((s - s0) & (GB_WS - 1)) * C::W_B + wcol * 32 * 64;
@@ -525,11 +541,6 @@ __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
         }
       }
     }
-  };
-
-  for (int s = s0; s < s1; s += 2) {
-    slab(s, st1, st0);
-    if (s + 1 < s1) slab(s + 1, st0, st1);
   }
 
   // ---- add the cluster's shares of K in rank order, each block a share of the columns ----
@@ -570,19 +581,11 @@ template <int NT, int RG, int G, bool ZP>
 cudaError_t launch_block(const GroupGemmArgs& a, cudaStream_t stream) {
   using C = BlockCfg<NT, RG, G>;
   const int64_t units = (a.N + GB_COLS - 1) / GB_COLS, zs = (a.M + C::ROWS - 1) / C::ROWS;
-  // K is split over as many blocks as make the fewest waves of resident blocks for their share of K, with a little
-  // for each part to join; at least four slabs a part
+  // K is split over up to four blocks with at least four slabs each: 61 x 8192 x 8192 took 41.8 us with four parts, 60
+  // with two or three, 96 with one; 64 x 11008 x 4096 37.7, 43 and 50; 256 x 8192 x 8192 138, 150 and 149.  Clusters of
+  // five to eight cost more than they bring (16 x 11008 x 4096: 12.4 us with four, 15 with eight).
   const int slabs = (int)((a.K + GB_SLAB - 1) / GB_SLAB);
-  const int64_t slots = (int64_t)sm_count() * block_slots(NT, RG);
-  int parts = 1;
-  double best = 1e30;
-  for (int p = 1; p <= 4 && (p == 1 || slabs >= 4 * p); ++p) {
-    const double cost = (double)((units * zs * p + slots - 1) / slots) / p * (1.0 + 0.02 * p);
-    if (cost < best) {
-      best = cost;
-      parts = p;
-    }
-  }
+  const int parts = slabs < 4 ? 1 : (slabs / 4 < 4 ? slabs / 4 : 4);
   auto kern = gemm_group_kernel<NT, RG, G, ZP>;
   cudaError_t e = set_smem_once(kern, C::SMEM);
   if (e != cudaSuccess) return e;
