@@ -16,8 +16,8 @@
  *   x[d] = low + step * code[d],   code in [0, 15].
  * Token `slot` of the pool is row slot % page_size of page slot / page_size.
  * Supported: D 64, 128 or 256; group 32, 64 or 128 with group <= D and
- * D / group <= 4; page_size 16, 32, 64, 128 or 256; num_pages * page_size
- * below 2**31.  Byte offsets into the pool are 64 bits wide.
+ * D / group <= 4; page_size 16, 32, 64, 128 or 256; at most 4096 kv_heads;
+ * num_pages * page_size below 2**31.  Byte offsets into the pool are 64 bits wide.
  */
 #ifndef BQ_DECODE_H_
 #define BQ_DECODE_H_
@@ -96,8 +96,8 @@ bq_status bq_gemm_f16xi4_group(const uint16_t* X, int64_t ld_x, const uint8_t* W
  *   and bq_device_status reports BQ_ERR_INVALID_ARG.
  *   NaN / Inf inputs are not supported.  kv_heads >= 1, q_heads >= 0; T = 0
  *   is an empty call.  rot is a multiple of 16, at most D.
- *   Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (D, group, page_size, rot,
- *   more than 65536 heads or 2**24 tokens), CUDA.
+ *   Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (the pool's shape, rot not
+ *   a multiple of 16, more than 65536 q_heads or 2**24 tokens), CUDA.
  */
 bq_status bq_qk_norm_rope_kv4(const uint16_t* q, int64_t ld_q, const uint16_t* k, int64_t ld_k, const uint16_t* v,
                               int64_t ld_v, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D,

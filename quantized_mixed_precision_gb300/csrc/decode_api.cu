@@ -10,6 +10,7 @@ using namespace bq;
 
 constexpr int64_t MAX_ROWS = 1LL << 24;
 constexpr int64_t MAX_HEADS = 65536;
+constexpr int64_t MAX_KV_HEADS = 4096;   // a page's bytes stay below 2**32
 constexpr int64_t MAX_LEN = 1LL << 30;   // keys of a sequence
 
 inline bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -62,7 +63,7 @@ bq_status bq_qk_norm_rope_kv4(const uint16_t* q, int64_t ld_q, const uint16_t* k
   if (T == 0) return BQ_OK;
   if (!k || !v || !slots || !codes || !params || (q_heads > 0 && (!q || !q_out))) return BQ_ERR_INVALID_ARG;
   if (rot > 0 ? (!cos || !sin || !positions) : (cos || sin)) return BQ_ERR_INVALID_ARG;
-  if (q_heads > MAX_HEADS || kv_heads > MAX_HEADS || T > MAX_ROWS || rot % 16 != 0) return BQ_ERR_UNSUPPORTED;
+  if (q_heads > MAX_HEADS || kv_heads > MAX_KV_HEADS || T > MAX_ROWS || rot % 16 != 0) return BQ_ERR_UNSUPPORTED;
   if (!valid_pool(D, group, page_size, num_pages)) return BQ_ERR_UNSUPPORTED;
   if (ld_k < kv_heads * D || ld_v < kv_heads * D || (q_heads > 0 && ld_q < q_heads * D)) return BQ_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v) || ld_k % 8 != 0 || ld_v % 8 != 0) return BQ_ERR_ALIGNMENT;
@@ -119,7 +120,8 @@ bq_status bq_attn_kv4(const uint16_t* q, int64_t ld_q, int64_t T, int64_t q_head
   if (max_q < 1 || (!cu_q && T != B)) return BQ_ERR_INVALID_ARG;
   if (!q || !out || !seq_lens || (max_len > 0 && (!codes || !params || !block_table || num_pages < 1)))
     return BQ_ERR_INVALID_ARG;
-  if (q_heads > MAX_HEADS || T > MAX_ROWS || B > MAX_ROWS || max_q > MAX_ROWS || max_len > MAX_LEN)
+  if (q_heads > MAX_HEADS || kv_heads > MAX_KV_HEADS || T > MAX_ROWS || B > MAX_ROWS || max_q > MAX_ROWS ||
+      max_len > MAX_LEN)
     return BQ_ERR_UNSUPPORTED;
   if (!valid_pool(D, group, page_size, num_pages)) return BQ_ERR_UNSUPPORTED;
   if (ld_q < q_heads * D || max_len > ld_table * page_size) return BQ_ERR_INVALID_ARG;

@@ -3,6 +3,10 @@
 Bound like the calls of the package: argument checks, device pointers and the
 current CUDA stream, ``BqError`` on a non-OK status.  The 4-bit cache is two
 tensors that ``bq_kv4_pool`` allocates and these calls share.
+
+A plain call (no ``out``, no ``stream``) goes through csrc/decode_binding.cpp,
+which makes the same checks and the same C call in less of the host's time;
+whatever it does not take as it is comes back here.
 """
 
 from __future__ import annotations
@@ -22,7 +26,8 @@ SIGNATURES = {
 }
 
 
-_CODES = {"plain": 0, "interleaved": 1, "none": 0, "relu": 1, "gelu": 2}
+_LAYOUTS = {"plain": 0, "interleaved": 1}
+_ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2}
 
 
 class _Bound:
@@ -108,8 +113,8 @@ def bq_gemm_f16xi4_group(X, Wp, scale, group, zero_point=None, layout="interleav
     codes, fp16 zero points of the same shape -> fp16 (M, N).  X may have a row stride."""
     import torch
     if out is None and stream is None:
-        r = (_bound or _load()).native.gemm(X, Wp, scale, group, zero_point, _CODES.get(layout, layout),
-                                            _CODES.get(activation, activation))
+        r = (_bound or _load()).native.gemm(X, Wp, scale, group, zero_point, _LAYOUTS.get(layout, layout),
+                                            _ACTIVATIONS.get(activation, activation))
         if r is not None:
             return r if type(r) is not int else _bound.bq._check(r, "bq_gemm_f16xi4_group")
     _need(X, torch.float16, "X", 2)
@@ -139,9 +144,9 @@ def bq_gemm_f16xi4_group(X, Wp, scale, group, zero_point=None, layout="interleav
         out = b.empty((M, N), dtype=f16, device=X.device)
     elif not _is_whole(out, f16, (M, N), dev):
         _need_whole(out, f16, "out", (M, N), dev)
-    st = b.gemm(X.data_ptr(), ld, Wp.data_ptr(), _CODES[layout] if isinstance(layout, str) else int(layout), M, N, K,
+    st = b.gemm(X.data_ptr(), ld, Wp.data_ptr(), _LAYOUTS[layout] if isinstance(layout, str) else int(layout), M, N, K,
                 group, scale.data_ptr(), None if zero_point is None else zero_point.data_ptr(),
-                _CODES[activation] if isinstance(activation, str) else int(activation), out.data_ptr(),
+                _ACTIVATIONS[activation] if isinstance(activation, str) else int(activation), out.data_ptr(),
                 b.raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         b.bq._check(st, "bq_gemm_f16xi4_group")

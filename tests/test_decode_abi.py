@@ -102,6 +102,15 @@ def test_attention_workspace(lib):
         assert lib.bq_attn_kv4(*args, None, need, None) == ARG
 
 
+def test_too_many_kv_heads(lib):
+    """A page's bytes have to fit 32 bits."""
+    big = 8192
+    assert lib.bq_attn_kv4(FAKE, big * 64, 1, big, big, 64, FAKE, FAKE, 1, 16, 64, FAKE, 1, FAKE, None, 1, 1, 16, 0.1, 0,
+                           FAKE, None, None, 0, None) == UNSUPPORTED
+    assert lib.bq_qk_norm_rope_kv4(FAKE, 64, FAKE, big * 64, FAKE, big * 64, 1, 1, big, 64, None, None, 1e-6, None, None,
+                                   0, 0, 0, None, FAKE, FAKE, FAKE, 1, 16, 64, FAKE, None, None, None) == UNSUPPORTED
+
+
 def test_binding_refuses_cpu_tensors():
     torch = pytest.importorskip("torch")
     x = torch.zeros((1, 64), dtype=torch.float16)

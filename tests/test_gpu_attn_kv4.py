@@ -129,6 +129,37 @@ def test_max_len_and_workspace():
     check(c)
 
 
+def test_no_keys_at_all():
+    """max_len 0, with an empty pool and table: zeros and -inf."""
+    q = torch.randn((3, 4, 64), device="cuda").half()
+    codes, params = bq.bq_kv4_pool(0, 2, 64, page_size=16, group=32)
+    out, lse = bq.bq_attn_kv4(q, codes, params, torch.zeros((3, 0), dtype=torch.int32, device="cuda"),
+                              torch.zeros((3,), dtype=torch.int32, device="cuda"), max_len=0, lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+    table = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    with pytest.raises(bq.BqError):         # keys, but no pool to read them from
+        bq.bq_attn_kv4(q, codes, params, table, torch.ones((3,), dtype=torch.int32, device="cuda"))
+
+
+def test_constant_values():
+    """Groups whose step is 0: all of a value is in its low."""
+    c = make(31, [200], [1], 4, 1, 64, 16, 32, stale=False)
+    c["params"][:, 1, ..., 0] = 0
+    check(c)
+    c["params"][:3, 1, ..., 0] = np.float16(0.25)
+    c["params"][:, 1, ..., 1] = np.float16(30000.0)
+    check(c)
+
+
+def test_both_bindings_agree():
+    """The plain call (native binding) and the one with out= (Python) are the same call."""
+    c = make(32, [700, 30], [1, 1], 8, 2, 128, 64, 64)
+    args = [dev(c[n]) for n in ("q", "codes", "params", "table", "lens")]
+    a, la = bq.bq_attn_kv4(*args, lse=True, window=300)
+    b, lb = bq.bq_attn_kv4(*args, lse=True, window=300, out=torch.empty_like(args[0]))
+    assert torch.equal(a, b) and torch.equal(la, lb)
+
+
 def test_large_and_tiny_magnitudes():
     """Values and steps near the fp16 limits and in its subnormals, and scores far apart."""
     c = make(18, [150, 150], [1, 1], 4, 1, 128, 16, 64, stale=False)
