@@ -107,10 +107,15 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // box_rows rows.  Out-of-range elements read as zero and are not written.
 cudaError_t make_map(CUtensorMap* map, const void* base, int elem, uint64_t row_elems, uint64_t rows, uint32_t box_x,
                      uint32_t box_rows, CUtensorMapSwizzle swz) {
+  return make_map_rows(map, base, elem, row_elems, row_elems, rows, box_x, box_rows, swz);
+}
+
+cudaError_t make_map_rows(CUtensorMap* map, const void* base, int elem, uint64_t row_elems, uint64_t ld, uint64_t rows,
+                          uint32_t box_x, uint32_t box_rows, CUtensorMapSwizzle swz) {
   auto fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {row_elems, rows};
-  const cuuint64_t strides[1] = {row_elems * (uint64_t)elem};
+  const cuuint64_t strides[1] = {ld * (uint64_t)elem};
   const cuuint32_t box[2] = {box_x, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   const CUtensorMapDataType dt = elem == 4   ? CU_TENSOR_MAP_DATA_TYPE_INT32

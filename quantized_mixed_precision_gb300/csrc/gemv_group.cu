@@ -12,6 +12,7 @@
 
 #include "bq_device.cuh"
 #include "decode_internal.h"
+#include "gemm_common.cuh"
 #include "kv4_device.cuh"
 
 namespace bq {
@@ -42,8 +43,8 @@ struct StagePlan {
 // quad lane of rows 0..7 (a multiple of 128 bytes apart) then touch every bank once.
 __device__ __forceinline__ int row_swizzle(int r) { return (r & 1) << 6 | (r & 2) << 4 | (r & 4) << 2; }
 
-// The same for rows of 64 bytes (two of them share 128 bytes).
-__device__ __forceinline__ int weight_swizzle(int r) { return (r & 2) << 4 | (r & 4) << 2; }
+// TMA's swizzle of rows of 64 bytes.
+__device__ __forceinline__ int weight_swizzle(int r) { return (r & 6) << 3; }
 
 // Codes of a word as MMA operands; signed codes become u = c + 8 by flipping their top bit, in the same LOP3.  The
 // masks come in registers that the compiler cannot see through: with constants it put one of the two into a register
@@ -311,8 +312,8 @@ cudaError_t launch_gemv(const GroupGemmArgs& a, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 constexpr int GB_SLAB = 128;                 // k of a slab
 constexpr int GB_COLS = 128;                 // columns j of a block
-constexpr int GB_XS = 4;                     // slabs of X in the ring
-constexpr int GB_WS = 4;                     // slabs of weights in the ring
+constexpr int GB_STAGES = 4;                 // slabs in the ring
+constexpr uint64_t DRAIN_NS = 2000000000;    // limit of the wait for copies in flight after another wait gave up
 
 // Blocks an SM: NT row tiles of 8 a warp, RG warps along the rows
 constexpr int block_slots(int nt, int rg) { return rg == 2 ? 2 : (nt == 4 ? 3 : 4); }
@@ -327,9 +328,10 @@ struct BlockCfg {
   static constexpr int SUMS = ROWS * SG;                             // sums of X over a slab's groups
   static constexpr int SB = 8 / SG;                                  // slabs with 8 groups
   static constexpr int STEPS = GB_COLS * 8;                          // (step, zero) of 8 groups
-  static constexpr int RING = GB_XS * X_B + GB_WS * W_B + 2 * SUMS * 4 + 2 * STEPS * 4;
+  static constexpr int STAGE_B = X_B + W_B;
+  static constexpr int RING = GB_STAGES * STAGE_B + 2 * SUMS * 4 + 2 * STEPS * 4;
   static constexpr int ACC = ROWS * (GB_COLS + 4) * 4;               // partial results, for the cluster
-  static constexpr int SMEM = RING > ACC ? RING : ACC;
+  static constexpr int SMEM = (RING > ACC ? RING : ACC) + 1024;      // TMA's swizzles repeat every 1024 bytes
 };
 
 // Exact signed fp16 pairs of a word's codes, in the order of its masks: signed codes c, or unsigned ones less 8.
@@ -348,12 +350,14 @@ __device__ __forceinline__ void signed_codes(uint32_t w, uint32_t (&h)[4]) {
 
 template <int NT, int RG, int G, bool ZP>
 __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
-    gemm_group_kernel(const __half* __restrict__ x, int64_t ld_x, const uint8_t* __restrict__ w, bool inter, int M, int N,
-                      int K, const uint16_t* __restrict__ scale, const uint16_t* __restrict__ zero, int actfn,
-                      __half* __restrict__ y, int parts) {
+    gemm_group_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w, bool inter,
+                      int M, int N, int K, const uint16_t* __restrict__ scale, const uint16_t* __restrict__ zero, int actfn,
+                      __half* __restrict__ y, int parts, uint64_t timeout_ns, int* status) {
   using C = BlockCfg<NT, RG, G>;
   constexpr int WORDS = G / 32;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[GB_STAGES];
+  uint8_t* const smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int wcol = warp & 3, wrow = warp >> 2;              // this warp's columns and rows
   const int part = blockIdx.x % parts, unit = blockIdx.x / parts;   // a cluster is the parts of a unit
@@ -363,51 +367,43 @@ __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
   const int eights = (slabs + C::SB - 1) / C::SB;
   const int s0 = (int)((int64_t)eights * part / parts) * C::SB;
   const int s1 = min((int)((int64_t)eights * (part + 1) / parts) * C::SB, slabs);
-  uint8_t* const xr = smem;
-  uint8_t* const wr = smem + GB_XS * C::X_B;
-  float* const sums = reinterpret_cast<float*>(wr + GB_WS * C::W_B);
+  float* const sums = reinterpret_cast<float*>(smem + GB_STAGES * C::STAGE_B);
   uint32_t* const steps = reinterpret_cast<uint32_t*>(sums + 2 * C::SUMS);
-  const int row_b = K / 2;
 
-  // copies: 16 pieces of 8 k a row of X (piece of word i, quad lane t at 4 i + t of its group, halves of 128 bytes
-  // swapped in odd rows); 4 pieces of a weight row
-  constexpr int XR = C::THREADS / 16, WR = C::THREADS / 4;  // rows of one copy of the block
-  const int xc = tid & 15, x_row = tid >> 4;
-  const __half* const xsrc = x + (int64_t)(m0 + x_row) * ld_x + xc * 8;
-  const uint32_t x_to = smem_u32(xr) + x_row * 256 +
-                        (((xc / (G / 8) * (G / 8) + xc % (G / 32) * 4 + xc % (G / 8) / (G / 32)) ^ ((x_row & 1) << 2)) << 4);
-  const int w_row = tid >> 2;
-  const uint32_t w_to = smem_u32(wr) + ((w_row * 64 + (tid & 3) * 16) ^ weight_swizzle(w_row));
-  const uint8_t* wsrc[GB_COLS / WR];
+  // A slab is three TMA boxes: two of 64 k of X (rows of 128 bytes, 16-byte piece c of row r at c ^ (r & 7)) and the
+  // codes (rows of 64 bytes, piece c at c ^ (r >> 1 & 3)).  What lies past M, N and K comes as zeros.
+  if (tid == 0) {
 #pragma unroll
-  for (int i = 0; i < GB_COLS / WR; ++i)
-    wsrc[i] = w + (size_t)min(unit * GB_COLS + w_row + WR * i, N - 1) * row_b + (tid & 3) * 16;
-  auto issue = [&](int s) {
-    if (s < s1) {
-      if (s * GB_SLAB + xc * 8 < K)
-#pragma unroll
-        for (int r = 0; r < C::ROWS; r += XR)
-          if (r + x_row < rows)
-            cp_async_16_l1(x_to + ((s - s0) & (GB_XS - 1)) * C::X_B + r * 256, xsrc + (int64_t)r * ld_x + s * GB_SLAB);
-      if (s * (GB_SLAB / 2) + (tid & 3) * 16 < row_b)
-#pragma unroll
-        for (int i = 0; i < GB_COLS / WR; ++i)
-          cp_async_16_u(w_to + ((s - s0) & (GB_WS - 1)) * C::W_B + i * WR * 64, wsrc[i] + s * (GB_SLAB / 2));
-    }
-    cp_async_commit();
+    for (int i = 0; i < GB_STAGES; ++i) mbar_init(&full[i], 1);
+    mbar_fence_init();
+  }
+  __syncthreads();
+  auto issue = [&](int s) {                                 // (thread 0)
+    if (s >= s1) return;
+    const int st = (s - s0) & (GB_STAGES - 1);
+    uint8_t* const to = smem + st * C::STAGE_B;
+    mbar_arrive_expect_tx(&full[st], C::STAGE_B);
+    tma_load_2d(to, &tmap_x, s * GB_SLAB, m0, &full[st]);
+    tma_load_2d(to + C::X_B / 2, &tmap_x, s * GB_SLAB + 64, m0, &full[st]);
+    tma_load_2d(to + C::X_B, &tmap_w, s * (GB_SLAB / 2), unit * GB_COLS, &full[st]);
   };
+  auto arrived = [&](int s) {                               // every thread sees the copies of slab s
+    return s >= s1 || mbar_wait(&full[(s - s0) & (GB_STAGES - 1)], ((s - s0) / GB_STAGES) & 1, timeout_ns, status);
+  };
+  const int xc = tid & 15, x_row = tid >> 4;                // a piece of a row of X
+  constexpr int XR = C::THREADS / 16;
   // What slab s needs besides its copies
   auto ready = [&](int s) {
     if (s >= s1) return;
-    uint8_t* const xs = xr + ((s - s0) & (GB_XS - 1)) * C::X_B;
+    uint8_t* const xs = smem + ((s - s0) & (GB_STAGES - 1)) * C::STAGE_B;
     if (ZP || !inter) {
       float* const to = sums + ((s - s0) & 1) * C::SUMS;
 #pragma unroll
       for (int r = x_row; r < C::ROWS; r += XR) {           // (whole warps: rows past the last are not used)
-        uint4* const at = reinterpret_cast<uint4*>(xs + r * 256 + ((xc ^ ((r & 1) << 2)) << 4));
+        uint4* const at = reinterpret_cast<uint4*>(xs + (xc >> 3) * (C::X_B / 2) + r * 128 + (((xc ^ r) & 7) << 4));
         const uint4 p = *at;
         if (ZP) {
-          // a group's pieces are those of G / 8 neighbouring lanes, in whatever order
+          // a group's pieces are those of G / 8 neighbouring lanes
           float v = sum_h8(p);
 #pragma unroll
           for (int o = 1; o < G / 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o, 16);
@@ -419,9 +415,11 @@ __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
       }
     }
   };
-  issue(s0);
-  issue(s0 + 1);
-  issue(s0 + 2);
+  if (tid == 0) {
+    issue(s0);
+    issue(s0 + 1);
+    issue(s0 + 2);
+  }
 
   float acc[2][NT][4];
 #pragma unroll
@@ -463,25 +461,40 @@ __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
     }
   };
   load_eight(s0 / C::SB);
-  cp_async_wait<2>();
-  __syncthreads();
+  // A wait that gives up is reported and nothing is copied from then on; the sums go on with what is there.
+  bool ok = true;
+  int lost = s0;
+  auto await = [&](int s) {
+    if (!ok) return;
+    ok = arrived(s);
+    lost = s;
+  };
+  await(s0);
   ready(s0);
   store_eight(s0 / C::SB);
   load_eight(s0 / C::SB + 1);
 
+  // Word i of group j: piece t * WORDS + i of the group.  With four words (groups of 128) the lanes 2 and 3, whose
+  // pieces lie in the other box, take them in the order 2, 3, 0, 1, which keeps eight lanes' loads on different banks.
+  const uint32_t x_row0 = g * 128;
+  auto x_at = [&](int i, int j) -> uint32_t {
+    const int piece = j * (G / 8) + t * WORDS + (WORDS == 4 ? i ^ (t & 2) : i);
+    return x_row0 + (piece >> 3) * (C::X_B / 2) + (((piece ^ g) & 7) << 4);
+  };
   for (int s = s0; s < s1; ++s) {
-    cp_async_wait<1>();                      // slab s + 1 has come
-    __syncthreads();                         // ... for everybody, slab s is ready, and slab s - 1 has been read
-    issue(s + 3);
+    if (!inter) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // X was put in order before the next copy
+    __syncthreads();                         // slab s is ready, and slab s - 1 has been read
+    if (tid == 0 && ok) issue(s + 3);
+    await(s + 1);
     ready(s + 1);
     if ((s + 1) % C::SB == 0) {              // the next slab begins an eight: its steps, and the loads of the one after
       store_eight((s + 1) / C::SB);
       load_eight((s + 1) / C::SB + 1);
     }
     const uint32_t* const sp = steps + ((s / C::SB) & 1) * C::STEPS + s % C::SB * C::SG * GB_COLS + wcol * 32 + g;
-    const uint8_t* const xs = xr + ((s - s0) & (GB_XS - 1)) * C::X_B + wrow * NT * 8 * 256;
+    const uint8_t* const xs = smem + ((s - s0) & (GB_STAGES - 1)) * C::STAGE_B + wrow * NT * 8 * 128;
     const float* const sum = sums + ((s - s0) & 1) * C::SUMS + wrow * NT * 8 * C::SG;
-    const uint8_t* const ws = wr + ((s - s0) & (GB_WS - 1)) * C::W_B + wcol * 32 * 64;
+    const uint8_t* const ws = smem + ((s - s0) & (GB_STAGES - 1)) * C::STAGE_B + C::X_B + wcol * 32 * 64;
 #pragma unroll
     for (int j = 0; j < C::SG; ++j) {
       if (s * C::SG + j >= ngroups) break;           // uniform
@@ -490,7 +503,13 @@ __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint8_t* p = ws + (((g * 64) + j * (G / 2) + t * (G / 8)) ^ weight_swizzle(g)) + i * 512;
-        if constexpr (WORDS == 4) *reinterpret_cast<uint4*>(wd[i]) = *reinterpret_cast<const uint4*>(p);
+        if constexpr (WORDS == 4) {
+          const uint4 q = *reinterpret_cast<const uint4*>(p);
+          wd[i][0] = t & 2 ? q.z : q.x;
+          wd[i][1] = t & 2 ? q.w : q.y;
+          wd[i][2] = t & 2 ? q.x : q.z;
+          wd[i][3] = t & 2 ? q.y : q.w;
+        }
         else if constexpr (WORDS == 2) *reinterpret_cast<uint2*>(wd[i]) = *reinterpret_cast<const uint2*>(p);
         else wd[i][0] = *reinterpret_cast<const uint32_t*>(p);
       }
@@ -506,8 +525,7 @@ __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
           uint4 v[NB];
 #pragma unroll
           for (int n = 0; n < NB; ++n)
-            v[n] = *reinterpret_cast<const uint4*>(xs + (8 * (nb + n) + g) * 256 +
-                                                   (((j * (G / 8) + i * 4 + t) ^ ((g & 1) << 2)) << 4));
+            v[n] = *reinterpret_cast<const uint4*>(xs + 8 * (nb + n) * 128 + x_at(i, j));
 #pragma unroll
           for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -544,7 +562,9 @@ __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
   }
 
   // ---- add the cluster's shares of K in rank order, each block a share of the columns ----
-  cp_async_wait<0>();
+  if (tid == 0 && !ok)                                      // copies in flight end before their memory is used again
+    for (int s = lost; s < min(lost + 3, s1); ++s)
+      mbar_wait(&full[(s - s0) & (GB_STAGES - 1)], ((s - s0) / GB_STAGES) & 1, DRAIN_NS, status);
   __syncthreads();
   float* const pa = reinterpret_cast<float*>(smem);         // [row of X][column], padded
   constexpr int LD = GB_COLS + 4;
@@ -589,6 +609,12 @@ cudaError_t launch_block(const GroupGemmArgs& a, cudaStream_t stream) {
   auto kern = gemm_group_kernel<NT, RG, G, ZP>;
   cudaError_t e = set_smem_once(kern, C::SMEM);
   if (e != cudaSuccess) return e;
+  CUtensorMap tmap_x, tmap_w;
+  e = make_map_rows(&tmap_x, a.x, 2, a.K, a.ld_x, a.M, 64, C::ROWS, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e == cudaSuccess) e = make_map(&tmap_w, a.w, 1, a.K / 2, a.N, 64, GB_COLS, CU_TENSOR_MAP_SWIZZLE_64B);
+  int* status = nullptr;
+  if (e == cudaSuccess) e = device_status_ptr(&status);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(parts * units), (unsigned)zs);
   cfg.blockDim = dim3(C::THREADS);
@@ -601,9 +627,9 @@ cudaError_t launch_block(const GroupGemmArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, reinterpret_cast<const __half*>(a.x), a.ld_x, a.w,
-                            a.layout == BQ_LAYOUT_INTERLEAVED, (int)a.M, (int)a.N, (int)a.K, a.scale, a.zero_point,
-                            a.actfn, reinterpret_cast<__half*>(a.y), parts);
+  return cudaLaunchKernelEx(&cfg, kern, tmap_x, tmap_w, a.layout == BQ_LAYOUT_INTERLEAVED, (int)a.M, (int)a.N, (int)a.K,
+                            a.scale, a.zero_point, a.actfn, reinterpret_cast<__half*>(a.y), parts,
+                            (uint64_t)wait_timeout_ns(), status);
 }
 
 template <int G, bool ZP>
