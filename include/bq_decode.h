@@ -49,6 +49,8 @@ extern "C" {
  *   zero_point  device fp16 (N, K / group), contiguous, or NULL
  *   Y           device fp16 (M, N), contiguous
  *   Any M and any N.  M = 0 or N = 0 is an empty call; K = 0 writes zeros.
+ *   With M > 8 the waits for copies are bounded (bq_set_wait_timeout_ns); one
+ *   that gives up is reported as BQ_ERR_TIMEOUT by bq_device_status.
  *   Limits: group 32, 64 or 128, K a multiple of it, K <= 65536.
  *   Errors: INVALID_ARG (null pointers, negative sizes, ld_x < K, bad
  *   group, layout or activation), ALIGNMENT, UNSUPPORTED (K not a multiple

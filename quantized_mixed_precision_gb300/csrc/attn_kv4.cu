@@ -24,6 +24,18 @@
 // the weights (128k keys: 7e-4 off without, 2e-4 being the rounding of the result).
 // What turns them back, 7.5 sum_t +-(p step), is summed beside from the rounded weights.
 //
+// What bounds it.  One new token a sequence should be bound by reading the cache:
+// 32 sequences of 32k keys (D 128, 8 kv heads, 4 query heads each, groups of 64:
+// 739 MB) take 137 us, 5.4 TB/s, 79 % of a plain copy's rate.  What is left is
+// instructions (about 600 for a warp's tile, 60 % of the issue slots over the
+// whole launch), the first data 4.6 us after the launch, and blocks that end up to
+// 16 us apart.  A short cache is bound by the fixed 10 us or
+// so of scan, first data, straddled units and join (16 sequences of 4k keys 21.4 us,
+// one of 128k 34.3), and the direct form by its latency (97 keys 4.4 us).  Many
+// queries are bound by arithmetic: 2 x 256 tokens on 16k keys take 381 us
+// (240 TFLOP/s of the formula's), the tensor pipe busy 41 % of the time at the
+// two warps a scheduler that 255 registers allow.
+//
 // Work is split over warps by tiles of 32 keys.  A unit is one (sequence,
 // kv head, block of query rows); the blocks of the grid take equal contiguous
 // ranges of the tiles of all units, whatever the lengths are, and a unit that
@@ -129,7 +141,8 @@ __device__ __forceinline__ int64_t seq_cost(const AttnParams& a, const Seq& s) {
 }
 
 // Blocks per SM, by the registers of the accumulators: what fits without spills.  With D = 128 and 8 query rows, 3 blocks
-// (168 registers a thread) take 133 us for 739 MB of cache, 4 blocks (128 registers) 147 us, 2 blocks 138 us.
+// (168 registers a thread) took 133 us for 739 MB of cache, 4 blocks (128 registers) 147 us, 2 blocks 138 us (before
+// the second sum's signs, which cost 3 us).
 constexpr int blocks_per_sm(int D, int nt) { return D < 256 && D * nt <= 256 ? 3 : 2; }
 
 template <int D, int NG, int NT>

@@ -3,10 +3,16 @@
 // CUDA error of the launch.
 #pragma once
 
+#include <cuda.h>
+
 #include "bq_decode.h"
 #include "bq_internal.h"
 
 namespace bq {
+
+// As make_map (gemm_common.cuh), with rows `ld` elements apart (a multiple of 16 bytes).
+cudaError_t make_map_rows(CUtensorMap* map, const void* base, int elem, uint64_t row_elems, uint64_t ld, uint64_t rows,
+                          uint32_t box_x, uint32_t box_rows, CUtensorMapSwizzle swz);
 
 struct GroupGemmArgs {
   const uint16_t* x;

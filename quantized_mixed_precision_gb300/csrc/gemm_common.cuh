@@ -16,9 +16,6 @@ namespace bq {
 // written by stores.
 cudaError_t make_map(CUtensorMap* map, const void* base, int elem, uint64_t row_elems, uint64_t rows, uint32_t box_x,
                      uint32_t box_rows, CUtensorMapSwizzle swz);
-// The same with rows `ld` elements apart (a multiple of 16 bytes).
-cudaError_t make_map_rows(CUtensorMap* map, const void* base, int elem, uint64_t row_elems, uint64_t ld, uint64_t rows,
-                          uint32_t box_x, uint32_t box_rows, CUtensorMapSwizzle swz);
 // The same over `batch` matrices `item_stride` bytes apart: always a 3-D map
 // (third coordinate = batch item, box depth 1), also for one item, so that a
 // kernel's 3-D copies may use it; load and store only with 3-D copies.

@@ -45,6 +45,7 @@
 
 #include "bq_device.cuh"
 #include "bq_internal.h"
+#include "decode_internal.h"
 #include "gemm_common.cuh"
 #include "quant_math.cuh"
 

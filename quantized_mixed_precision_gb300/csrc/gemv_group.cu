@@ -4,9 +4,9 @@
 // with unsigned codes u; signed codes are u - 8 once their top bit is flipped, so
 // they are the case z = 8.  The tensor cores multiply the codes as fp16
 // subnormals (kv4_device.cuh: one LOP3 for two codes, exact), weights as the A
-// operand (16 columns j a tile) and up to 8 rows i as its columns.  Beside each
-// product an MMA with A = 1 sums the same activations, so that the zero point
-// costs no pass over X.  A group's sums start from zero, are scaled in fp32 and
+// operand (16 columns j a tile) and up to 8 rows i as its columns.  The sums of X
+// over a group, which the zero point needs, are made from the same tiles, so that
+// it costs no pass over X.  A group's sums start from zero, are scaled in fp32 and
 // added to fp32 accumulators: nothing is rounded to 16 bits before Y.
 #include <cuda_fp16.h>
 
@@ -20,12 +20,17 @@ namespace bq {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Up to 8 rows of X: bound by one read of the weights.  A block owns 16 columns
-// and its warps take stages of K in turn, each through a ring of its own, so
-// that no warp waits for another before the end.  A stage is 512 k (256 with
-// more than two rows of X, whose share of the ring would leave fewer blocks on
-// an SM): N = 11008, K = 4096 takes 7.9 us at M = 1 with 512, 8.5 with 1024, and
-// 18.1 at M = 8 with 256, 23 with 512 (two blocks fewer an SM).
+// Up to 8 rows of X: one read of the weights is what it cannot do without.  A
+// block owns 16 columns and its warps take stages of K in turn, each through a
+// ring of its own, so that no warp waits for another before the end.  A stage is
+// 512 k (256 with more than two rows of X, whose share of the ring would leave
+// fewer blocks on an SM): 512 against 1024 at M = 1 was 7.9 against 8.5 us, 256
+// against 512 at M = 8 18.1 against 23 (two blocks fewer an SM).
+// 1 x 11008 x 4096 in groups of 128, one call after another on weights larger
+// than L2: 7.1 us, 3.3 TB/s.  The copies alone take 3.7; the arithmetic, about 170
+// instructions for 16 columns and 128 k in a warp, 3.8 after a block's data has
+// come, and the blocks of the next call get their shared memory when this one's
+// are done, so that the two overlap in part only.
 // ---------------------------------------------------------------------------
 constexpr int SMEM_MAX = 227 * 1024;
 
@@ -306,9 +311,17 @@ cudaError_t launch_gemv(const GroupGemmArgs& a, cudaStream_t stream) {
 // X, a slab of 128 k at a time, and two warps with the same columns their
 // weights.  The codes are converted to exact signed fp16 (a conversion serves all
 // rows of a warp, so its subtraction is cheap here and one accumulator a group is
-// enough).  What a slab needs besides (the order of X for plain codes, its sums
+// enough).  A slab comes by TMA, which one thread asks for: with 16-byte copies by
+// all of them a third of a slab's time went into issuing those (61 x 8192 x 8192
+// took 41.9 us, 256 rows 138).  What a slab needs besides (the order of X for plain codes, its sums
 // over groups for zero points, which add (8 - z) s sum) is made while the slab
 // before it is multiplied, so that a slab costs one barrier.
+// What bounds it is mma.sync, whose pipe is busy 42 % of a launch at 61 rows and
+// what most warps wait for, with the fill of the ring before and the cluster's
+// sum after it; at 16 rows (15 %) it is those two and the latency of a slab.
+// 61 x 8192 x 8192 in groups of 128 takes 37.9 us (216 TFLOP/s, 0.9 TB/s of
+// weights), 256 x 8192 x 8192 120.4 (285 TFLOP/s), 16 x 11008 x 4096 in groups of 64
+// with zero points 15.8 (1.6 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int GB_SLAB = 128;                 // k of a slab
 constexpr int GB_COLS = 128;                 // columns j of a block
@@ -378,6 +391,8 @@ __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
     mbar_fence_init();
   }
   __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   auto issue = [&](int s) {                                 // (thread 0)
     if (s >= s1) return;
     const int st = (s - s0) & (GB_STAGES - 1);
@@ -601,9 +616,8 @@ template <int NT, int RG, int G, bool ZP>
 cudaError_t launch_block(const GroupGemmArgs& a, cudaStream_t stream) {
   using C = BlockCfg<NT, RG, G>;
   const int64_t units = (a.N + GB_COLS - 1) / GB_COLS, zs = (a.M + C::ROWS - 1) / C::ROWS;
-  // K is split over up to four blocks with at least four slabs each: 61 x 8192 x 8192 took 41.8 us with four parts, 60
-  // with two or three, 96 with one; 64 x 11008 x 4096 37.7, 43 and 50; 256 x 8192 x 8192 138, 150 and 149.  Clusters of
-  // five to eight cost more than they bring (16 x 11008 x 4096: 12.4 us with four, 15 with eight).
+  // K is split over up to four blocks with at least four slabs each: 61 x 8192 x 8192 takes 38.3 us with four parts, 45.3
+  // with two, 44.4 with eight; 16 x 11008 x 4096 16.2, 23.9 and 19.1; 256 x 8192 x 8192 121.6, 133.1 and 141.1.
   const int slabs = (int)((a.K + GB_SLAB - 1) / GB_SLAB);
   const int parts = slabs < 4 ? 1 : (slabs / 4 < 4 ? slabs / 4 : 4);
   auto kern = gemm_group_kernel<NT, RG, G, ZP>;
@@ -620,13 +634,15 @@ cudaError_t launch_block(const GroupGemmArgs& a, cudaStream_t stream) {
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)parts;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, tmap_x, tmap_w, a.layout == BQ_LAYOUT_INTERLEAVED, (int)a.M, (int)a.N, (int)a.K,
                             a.scale, a.zero_point, a.actfn, reinterpret_cast<__half*>(a.y), parts,
                             (uint64_t)wait_timeout_ns(), status);

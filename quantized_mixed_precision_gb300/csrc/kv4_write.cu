@@ -9,6 +9,11 @@
 // several heads are issued before the first is used.  What then competes with
 // memory is the issue of instructions, so the fp32 work runs in packed pairs
 // (each lane of a packed operation is an ordinary IEEE operation).
+// 8192 tokens of 32 + 2 x 8 heads of 128 dims take 46.6 us: 4.6 TB/s of the 6.8 that
+// a plain copy has, with 76 % of the issue slots taken (219 instructions for two
+// heads and warp), which is what bounds it; 777 tokens of 16 + 2 x 16 heads of 64
+// dims 5.3 us, 5 tokens 2.7, both the latency of one launch.  Bounded at
+// 7 blocks an SM (72 registers): 8 took 49.7 us, 6 47.9, unbounded 51.2.
 //
 // Every step is one IEEE fp32 operation in the order the header states, so
 // codes and steps are bit-exact: the sum of squares is a tree over neighbouring

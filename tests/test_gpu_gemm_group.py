@@ -82,6 +82,35 @@ def test_strided_rows_and_out():
     assert check(wide[:, 128:384], codes, s, z, 32, "plain", out=out) is out
 
 
+@pytest.mark.parametrize("zp", [False, True])
+@pytest.mark.parametrize("group", [32, 64])
+@pytest.mark.parametrize("m,k", [(9, 64), (20, 192), (40, 1088), (70, 1216)])
+def test_strided_rows_with_a_ragged_end(m, k, group, zp):
+    """Rows apart by more than K, K that ends inside a slab of 128, and NaN beside every row; the last row ends the storage."""
+    x, codes, s, z = make(m + k, m, 150, k, group, zp)
+    flat = torch.full(((m - 1) * (k + 24) + k,), float("nan"), dtype=torch.float16, device="cuda")
+    view = flat.as_strided((m, k), (k + 24, 1))
+    view.copy_(dev(x))
+    for layout in ("plain", "interleaved"):
+        check(view, codes, s, z, group, layout)
+
+
+def test_wait_limit_is_reported():
+    """With no time to wait, waits for the copies of a slab give up: reported once, and the next call is right."""
+    x, codes, s, z = make(12, 64, 256, 4096, 128, False)
+    xd, w, sd = dev(x), pack(codes, "interleaved"), dev(s)
+    torch.cuda.synchronize()
+    assert bq.bq_device_status(reset=True) == bq.BQ_OK
+    old = bq.bq_set_wait_timeout_ns(0)
+    try:
+        bq.bq_gemm_f16xi4_group(xd, w, sd, 128)
+        torch.cuda.synchronize()
+        assert bq.bq_device_status(reset=True) == bq.BQ_ERR_TIMEOUT
+    finally:
+        bq.bq_set_wait_timeout_ns(old)
+    check(x, codes, s, z, 128, "interleaved")
+
+
 def test_large_and_tiny_activations():
     """Activations up to the fp16 limits: nothing overflows or vanishes on the way."""
     x, codes, s, z = make(6, 4, 64, 512, 64, False)
