@@ -83,8 +83,8 @@ def test_strided_rows_and_out():
 
 
 @pytest.mark.parametrize("zp", [False, True])
-@pytest.mark.parametrize("group", [32, 64])
-@pytest.mark.parametrize("m,k", [(9, 64), (20, 192), (40, 1088), (70, 1216)])
+@pytest.mark.parametrize("m,k,group", [(9, 64, 32), (12, 32, 32), (20, 192, 64), (40, 1088, 32), (40, 1088, 64),
+                                       (70, 1216, 64), (33, 1248, 32), (17, 4224, 128)])
 def test_strided_rows_with_a_ragged_end(m, k, group, zp):
     """Rows apart by more than K, K that ends inside a slab of 128, and NaN beside every row; the last row ends the storage."""
     x, codes, s, z = make(m + k, m, 150, k, group, zp)
