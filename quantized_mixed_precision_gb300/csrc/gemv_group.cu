@@ -319,8 +319,8 @@ cudaError_t launch_gemv(const GroupGemmArgs& a, cudaStream_t stream) {
 // What bounds it is mma.sync, whose pipe is busy 42 % of a launch at 61 rows and
 // what most warps wait for, with the fill of the ring before and the cluster's
 // sum after it; at 16 rows (15 %) it is those two and the latency of a slab.
-// 61 x 8192 x 8192 in groups of 128 takes 37.9 us (216 TFLOP/s, 0.9 TB/s of
-// weights), 256 x 8192 x 8192 120.4 (285 TFLOP/s), 16 x 11008 x 4096 in groups of 64
+// 61 x 8192 x 8192 in groups of 128 takes 38.3 us (214 TFLOP/s, 0.9 TB/s of
+// weights), 256 x 8192 x 8192 122 (282 TFLOP/s), 16 x 11008 x 4096 in groups of 64
 // with zero points 15.8 (1.6 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int GB_SLAB = 128;                 // k of a slab
@@ -376,10 +376,7 @@ __global__ void __launch_bounds__(128 * RG, block_slots(NT, RG))
   const int part = blockIdx.x % parts, unit = blockIdx.x / parts;   // a cluster is the parts of a unit
   const int m0 = blockIdx.y * C::ROWS, rows = min(C::ROWS, M - m0);
   const int slabs = (K + GB_SLAB - 1) / GB_SLAB, ngroups = K / G;
-  // this part's slabs, in whole eights of groups
-  const int eights = (slabs + C::SB - 1) / C::SB;
-  const int s0 = (int)((int64_t)eights * part / parts) * C::SB;
-  const int s1 = min((int)((int64_t)eights * (part + 1) / parts) * C::SB, slabs);
+  const int s0 = slabs * part / parts, s1 = slabs * (part + 1) / parts;   // this part's slabs (at most 512 in all)
   float* const sums = reinterpret_cast<float*>(smem + GB_STAGES * C::STAGE_B);
   uint32_t* const steps = reinterpret_cast<uint32_t*>(sums + 2 * C::SUMS);
 
@@ -616,10 +613,23 @@ template <int NT, int RG, int G, bool ZP>
 cudaError_t launch_block(const GroupGemmArgs& a, cudaStream_t stream) {
   using C = BlockCfg<NT, RG, G>;
   const int64_t units = (a.N + GB_COLS - 1) / GB_COLS, zs = (a.M + C::ROWS - 1) / C::ROWS;
-  // K is split over up to four blocks with at least four slabs each: 61 x 8192 x 8192 takes 38.3 us with four parts, 45.3
-  // with two, 44.4 with eight; 16 x 11008 x 4096 16.2, 23.9 and 19.1; 256 x 8192 x 8192 121.6, 133.1 and 141.1.
+  // K is split over up to four blocks with at least two slabs each, so that the fullest block's share times the rounds
+  // of the grid is least; where that is equal, over more blocks.  61 x 8192 x 8192 takes 38.3 us with four parts, 45.3 with
+  // two; 61 x 11008 x 4096 in groups of 64 43.9 with four (40 blocks wait for a second round), 36.7 with three; 256 x 8192 x
+  // 8192 121.6 with four, 133.1 with two; 16 x 4096 x 1024 8.6 with two, 5.7 with four.  Clusters of eight cost more than
+  // they bring (44.4, and 16 x 11008 x 4096 19.1 instead of 16.2).
   const int slabs = (int)((a.K + GB_SLAB - 1) / GB_SLAB);
-  const int parts = slabs < 4 ? 1 : (slabs / 4 < 4 ? slabs / 4 : 4);
+  constexpr int FIT = 228 * 1024 / (C::SMEM + 1024);
+  const int64_t slots = (int64_t)sm_count() * (FIT < block_slots(NT, RG) ? FIT : block_slots(NT, RG));
+  int parts = 1;
+  int64_t least = INT64_MAX;
+  for (int p = 1; p <= 4 && (p == 1 || slabs >= 2 * p); ++p) {
+    const int64_t time = (units * zs * p + slots - 1) / slots * ((slabs + p - 1) / p);
+    if (time <= least) {
+      least = time;
+      parts = p;
+    }
+  }
   auto kern = gemm_group_kernel<NT, RG, G, ZP>;
   cudaError_t e = set_smem_once(kern, C::SMEM);
   if (e != cudaSuccess) return e;
