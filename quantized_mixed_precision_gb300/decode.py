@@ -11,6 +11,7 @@ whatever it does not take as it is comes back here.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 _c_i64, _vp, _int, _f32, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -97,7 +98,23 @@ def _row_stride(t, name):
     s = t.stride()
     if width and ((dims > 1 and s[2] != 1) or (heads > 1 and s[1] != dims)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s[0] if n > 1 and s[0] > width else width
+    return _apart(n, s[0], width, name)
+
+
+def _apart(rows, stride, width, name):
+    """The leading dimension of `rows` rows of `width` elements: rows that overlap (an expanded tensor's, which are
+    the same one) have none."""
+    if rows < 2:
+        return width
+    if stride < width:
+        raise ValueError(f"{name}: rows overlap (stride {stride}, width {width})")
+    return stride
+
+
+def _on(stream):
+    """Where what a call enqueues beside its kernels belongs: the caller's stream, or the current one."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _hold(stream, *tensors):
@@ -110,7 +127,7 @@ def _hold(stream, *tensors):
 def bq_gemm_f16xi4_group(X, Wp, scale, group, zero_point=None, layout="interleaved", activation="none", out=None,
                          stream=None):
     """fp16 X (M, K) times 4-bit weights Wp (N, K // 2 bytes) with fp16 scales (N, K // group) and, for unsigned
-    codes, fp16 zero points of the same shape -> fp16 (M, N).  X may have a row stride."""
+    codes, fp16 zero points of the same shape -> fp16 (M, N).  X may have a row stride of at least K."""
     import torch
     if out is None and stream is None:
         r = (_bound or _load()).native.gemm(X, Wp, scale, group, zero_point, _LAYOUTS.get(layout, layout),
@@ -138,7 +155,7 @@ def bq_gemm_f16xi4_group(X, Wp, scale, group, zero_point=None, layout="interleav
     if not X.is_contiguous():
         if X.stride(1) != 1:
             raise ValueError("X must have unit column stride")
-        ld = max(X.stride(0), K) if M > 1 else K
+        ld = _apart(M, X.stride(0), K, "X")
     made = out is None
     if made:
         out = b.empty((M, N), dtype=f16, device=X.device)
@@ -191,7 +208,8 @@ def bq_qk_norm_rope_kv4(q, k, v, codes, params, slots, positions=None, cos=None,
                         k_weight=None, eps=1e-6, pairs=False, values=False, out=None, stream=None):
     """Norm and rotate the heads of q (T, q_heads, D) and k (T, kv_heads, D), and write k and v into the pool at
     ``slots``.  Returns (q_out, k_values, v_values); the last two are None unless ``values``: they are what the cache
-    then holds.  q, k and v may be views of one QKV matrix.  cos and sin are fp32 (positions, rot // 2)."""
+    then holds.  q, k and v may be views of one QKV matrix (tokens apart by at least their heads).  cos and sin are
+    fp32 (positions, rot // 2)."""
     import torch
     if out is None and stream is None:
         r = (_bound or _load()).native.write(q, k, v, codes, params, slots, positions, cos, sin, q_weight, k_weight, eps,
@@ -258,7 +276,8 @@ def bq_attn_kv4(q, codes, params, block_table, seq_lens, cu_q=None, max_q=1, max
                 lse=False, out=None, workspace=None, stream=None):
     """Causal attention of q (T, q_heads, D) over the 4-bit cache -> (out fp16 (T, q_heads, D), lse fp32
     (T, q_heads) or None).  Sequence b's query tokens are rows cu_q[b] .. cu_q[b + 1] - 1 of q (None: row b) and the
-    last of its seq_lens[b] tokens in the cache.  ``max_len`` bounds the lengths (None: the width of the table);
+    last of its seq_lens[b] tokens in the cache.  ``block_table`` may have a row stride; where its rows overlap (one row
+    expanded over the batch) it is copied.  ``max_len`` bounds the lengths (None: the width of the table);
     ``scale`` defaults to D ** -0.5; ``workspace`` (uint8) is allocated for the call when it is not given."""
     import torch
     if out is None and stream is None:
@@ -278,7 +297,12 @@ def bq_attn_kv4(q, codes, params, block_table, seq_lens, cu_q=None, max_q=1, max
     if not block_table.is_contiguous():
         if width > 1 and block_table.stride(1) != 1:
             raise ValueError("block_table must have unit column stride")
-        ld_table = max(block_table.stride(0), width) if B > 1 else width
+        if B > 1 and block_table.stride(0) < width:
+            # rows that overlap, such as one row expanded over a batch: the C call takes rows of their own
+            with _on(stream):
+                block_table = block_table.contiguous()
+        elif B > 1:
+            ld_table = block_table.stride(0)
     if not _is_whole(seq_lens, i32, (B,), dev):
         _need_whole(seq_lens, i32, "seq_lens", (B,), dev)
     if cu_q is not None:

@@ -1,0 +1,129 @@
+"""What the Python binding of the decoder-layer calls hands to the C calls, on CPU tensors with the C calls recorded."""
+
+import types
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import quantized_mixed_precision_gb300 as bq  # noqa: E402
+from quantized_mixed_precision_gb300 import decode  # noqa: E402
+
+
+class Recorder:
+    """Stands in for the library: every call is kept and answered with BQ_OK."""
+
+    def __init__(self, monkeypatch):
+        self.calls = []
+        none = staticmethod(lambda *a: None)
+        self.bound = types.SimpleNamespace(
+            bq=bq, torch=torch, f16=torch.float16, f32=torch.float32, u8=torch.uint8, i32=torch.int32,
+            empty=self.empty, raw_stream=lambda dev: 0, native=types.SimpleNamespace(gemm=none, write=none, attn=none),
+            gemm=self.record("gemm"), write=self.record("write"), attn=self.record("attn"), workspace=lambda *a: 64)
+        self.made = []
+        monkeypatch.setattr(decode, "_bound", self.bound)
+        monkeypatch.setattr(decode, "_need", self.need)
+
+    def record(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+    def empty(self, *args, **kw):
+        t = torch.empty(*args, **kw)
+        self.made.append(t)
+        return t
+
+    @staticmethod
+    def need(t, dtype, name, ndim, device=None):
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+            raise TypeError(name)
+        if t.dim() != ndim:
+            raise ValueError(name)
+
+
+@pytest.fixture
+def rec(monkeypatch):
+    return Recorder(monkeypatch)
+
+
+def f16(*shape):
+    return torch.zeros(shape, dtype=torch.float16)
+
+
+def weights(n=8, k=64, group=32):
+    return torch.zeros((n, k // 2), dtype=torch.uint8), f16(n, k // group)
+
+
+def pool(heads=2, d=64, pages=4, page=16, group=32):
+    return bq.bq_kv4_pool(pages, heads, d, page_size=page, group=group, device="cpu")
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+# ---- rows that lie closer together than they are wide -------------------------------------------------------------
+
+
+def close_rows(t, n=5):
+    """n rows of the shape of t's first: expanded, and overlapping by half."""
+    w = t[0].numel()
+    flat = torch.zeros((w * n,), dtype=t.dtype)
+    inner = torch.zeros(t.shape[1:]).stride()
+    return [t[:1].expand(n, *t.shape[1:]), flat.as_strided((n, *t.shape[1:]), (w // 2, *inner))]
+
+
+def test_linear_refuses_rows_that_overlap(rec):
+    w, s = weights()
+    for x in close_rows(f16(1, 64)):
+        with pytest.raises(ValueError):
+            bq.bq_gemm_f16xi4_group(x, w, s, 32)
+    assert not rec.calls
+    bq.bq_gemm_f16xi4_group(f16(5, 96)[:, :64], w, s, 32)
+    bq.bq_gemm_f16xi4_group(f16(1, 64).expand(1, 64), w, s, 32)
+    assert [c[1][1] for c in rec.calls] == [96, 64]
+
+
+def test_write_refuses_rows_that_overlap(rec):
+    codes, params = pool()
+    whole, slots = f16(5, 2, 64), ints(*range(5))
+    for bad in close_rows(f16(1, 2, 64)):
+        for args in ((bad, whole, whole), (whole, bad, whole), (whole, whole, bad)):
+            with pytest.raises(ValueError):
+                bq.bq_qk_norm_rope_kv4(*args, codes, params, slots)
+    assert not rec.calls
+    wide = f16(5, 6, 64)
+    bq.bq_qk_norm_rope_kv4(wide[:, :2], wide[:, 2:4], wide[:, 4:], codes, params, slots)
+    assert [rec.calls[0][1][i] for i in (1, 3, 5)] == [384] * 3
+
+
+def test_attention_refuses_queries_that_overlap(rec):
+    codes, params = pool()
+    table, lens = torch.zeros((5, 1), dtype=torch.int32), ints(1, 2, 3, 4, 5)
+    for bad in close_rows(f16(1, 4, 64)):
+        with pytest.raises(ValueError):
+            bq.bq_attn_kv4(bad, codes, params, table, lens)
+    assert not rec.calls
+
+
+def test_attention_takes_tables_whose_rows_overlap(rec):
+    """One prefix for the whole batch (an expanded row), or windows of one list: the C call gets rows of their own."""
+    codes, params = pool()
+    q, lens = f16(3, 4, 64), ints(1, 2, 3)
+    seen = {}
+    real = torch.Tensor.contiguous
+
+    def contiguous(t, *a, **kw):
+        r = real(t, *a, **kw)
+        seen[r.data_ptr()] = r
+        return r
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(torch.Tensor, "contiguous", contiguous)
+        for table in (ints(3, 1).expand(3, 2), ints(0, 1, 2, 3).unfold(0, 2, 1)):
+            bq.bq_attn_kv4(q, codes, params, table, lens)
+            ptr, ld = rec.calls[-1][1][11:13]
+            assert ld == 2 and seen[ptr].is_contiguous() and torch.equal(seen[ptr], table)
+    bq.bq_attn_kv4(q, codes, params, torch.zeros((3, 5), dtype=torch.int32)[:, :2], lens)
+    assert rec.calls[-1][1][12] == 5

@@ -1,0 +1,68 @@
+"""The decoder-layer operators on the GPU at the edges of what they accept, against the float64 oracle."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+import quantized_mixed_precision_gb300 as bq  # noqa: E402
+from oracle import decode_oracle as D  # noqa: E402
+from tests import test_gpu_attn_kv4 as attn  # noqa: E402
+from tests import test_gpu_gemm_group as linear  # noqa: E402
+from tests.test_gpu_parity import dev, host  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    bq.lib()
+    yield
+    torch.cuda.synchronize()
+    assert bq.bq_device_status(reset=True) == bq.BQ_OK
+
+
+def args_of(c):
+    return [dev(c[n]) for n in ("q", "codes", "params", "table", "lens")]
+
+
+# ---- rows that overlap ----------------------------------------------------------------------------------------------
+
+
+def test_overlapping_rows_are_refused():
+    """Nothing is launched for rows that lie closer together than they are wide."""
+    x, codes, s, _ = linear.make(1, 1, 40, 256, 64, False)
+    w, sd = linear.pack(codes, "plain"), dev(s)
+    with pytest.raises(ValueError):
+        bq.bq_gemm_f16xi4_group(dev(x).expand(6, 256), w, sd, 64, layout="plain")
+    with pytest.raises(ValueError):
+        bq.bq_gemm_f16xi4_group(torch.zeros(640, device="cuda").half().unfold(0, 256, 64), w, sd, 64, layout="plain")
+    pool = bq.bq_kv4_pool(1, 2, 64, page_size=16, group=32)
+    row = torch.zeros((1, 2, 64), dtype=torch.float16, device="cuda")
+    many, slots = row.expand(9, 2, 64), torch.arange(9, dtype=torch.int32, device="cuda")
+    for q, k, v in ((many, many.clone(), many.clone()), (many.clone(), many, many.clone()),
+                    (many.clone(), many.clone(), many)):
+        with pytest.raises(ValueError):
+            bq.bq_qk_norm_rope_kv4(q, k, v, *pool, slots)
+    with pytest.raises(ValueError):
+        bq.bq_attn_kv4(many, *pool, torch.zeros((9, 1), dtype=torch.int32, device="cuda"), slots)
+
+
+@pytest.mark.parametrize("n", [40, 700])
+def test_one_table_row_for_the_batch(n):
+    """Sequences that share one prefix: the table's only row expanded over them, each as long as it says."""
+    c = attn.make(n, [n], [1], 8, 2, 128, 16, 64, stale=False)
+    q, codes, params, table, _ = args_of(c)
+    lens = torch.tensor([n, n // 2, n - 3], dtype=torch.int32, device="cuda")
+    q = torch.cat([q, q * 0.5, -q])
+    out, _ = bq.bq_attn_kv4(q, codes, params, table.expand(3, -1), lens)
+    want, _, tol, _ = D.attention(host(q), c["codes"], c["params"], np.repeat(c["table"], 3, 0), host(lens), None,
+                                  128 ** -0.5)
+    assert (np.abs(host(out) - want) <= tol).all()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    again, _ = bq.bq_attn_kv4(q, codes, params, table.expand(3, -1), lens, stream=side)
+    side.synchronize()
+    assert torch.equal(out, again)
