@@ -132,7 +132,8 @@ bq_status bq_qk_norm_rope_kv4(const uint16_t* q, int64_t ld_q, const uint16_t* k
  *                (j + 1) * page_size) of a sequence; entries past its length
  *                are not read
  *   seq_lens     device int32 (B);  cu_q device int32 (B + 1) or NULL
- *   max_q        at least every sequence's number of query tokens
+ *   max_q        at least every sequence's number of query tokens (taken as 1
+ *                where cu_q is NULL)
  *   max_len      at least every sequence's length (the size of the grid and
  *                of the workspace follow it), at most ld_table * page_size
  *   out          device fp16 (T, q_heads, D), contiguous

@@ -130,6 +130,9 @@ bq_status bq_attn_kv4(const uint16_t* q, int64_t ld_q, int64_t T, int64_t q_head
   if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(lse, 4) ||
       !aligned16(workspace))
     return BQ_ERR_ALIGNMENT;
+  // Without cu_q a sequence has one query token whatever its bound says: the grids, the records of the parts and the
+  // workspace follow what there is (never more workspace than a larger max_q asks for).
+  if (!cu_q) max_q = 1;
   const size_t need = attn_kv4_workspace(B, q_heads, kv_heads, D, max_q, max_len);
   if (need > 0 && (!workspace || workspace_bytes < need)) return BQ_ERR_INVALID_ARG;
   AttnKv4Args a{};

@@ -1,5 +1,6 @@
 """What the Python binding of the decoder-layer calls hands to the C calls, on CPU tensors with the C calls recorded."""
 
+import os
 import types
 
 import pytest
@@ -127,3 +128,15 @@ def test_attention_takes_tables_whose_rows_overlap(rec):
             assert ld == 2 and seen[ptr].is_contiguous() and torch.equal(seen[ptr], table)
     bq.bq_attn_kv4(q, codes, params, torch.zeros((3, 5), dtype=torch.int32)[:, :2], lens)
     assert rec.calls[-1][1][12] == 5
+
+
+# ---- workspace ------------------------------------------------------------------------------------------------------
+
+
+@pytest.mark.skipif(not os.path.exists(bq.LIB_PATH), reason="libbq.so is not built")
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rep", [1, 4, 7, 64])
+def test_workspace_grows_with_max_q(d, rep):
+    """A workspace for some number of query tokens serves every smaller one."""
+    sizes = [bq.lib().bq_attn_kv4_workspace(3, 2 * rep, 2, d, q, 5000) for q in range(1, 70)]
+    assert sizes == sorted(sizes) and sizes[0] > 0

@@ -66,3 +66,29 @@ def test_one_table_row_for_the_batch(n):
     again, _ = bq.bq_attn_kv4(q, codes, params, table.expand(3, -1), lens, stream=side)
     side.synchronize()
     assert torch.equal(out, again)
+
+
+# ---- a bound on the query tokens that is more than there are --------------------------------------------------------
+
+
+@pytest.mark.parametrize("b,hq,hkv,d", [(1, 32, 8, 128), (2, 4, 1, 64), (1, 8, 2, 256)])
+def test_max_q_without_cu_q(b, hq, hkv, d):
+    """cu_q None: one token a sequence, whatever max_q says, on a workspace that a call with many tokens has left."""
+    c = attn.make(b + d, [900 + i for i in range(b)], [1] * b, hq, hkv, d, 16, 64)
+    args = args_of(c)
+    plain, lse = bq.bq_attn_kv4(*args, lse=True)
+    need = bq.bq_attn_kv4_workspace(b, hq, hkv, d, 1, 1000)
+    few, _ = bq.bq_attn_kv4(*args, max_q=16, max_len=900 + b, workspace=torch.zeros(need, dtype=torch.uint8,
+                                                                                  device="cuda"))
+    assert torch.equal(few, plain)
+    # records of a prompt's units in the workspace, and guard rows around the outputs
+    p = attn.make(3, [1000], [16], hq, hkv, d, 16, 64)
+    q, codes, params, table, lens = args_of(p)
+    ws = torch.zeros(bq.bq_attn_kv4_workspace(b, hq, hkv, d, 16, 1000), dtype=torch.uint8, device="cuda")
+    bq.bq_attn_kv4(q, codes, params, table, lens, cu_q=dev(p["cu"]), max_q=16, max_len=1000, workspace=ws)
+    room = torch.full((b + 64, hq, d), 7.0, dtype=torch.float16, device="cuda")
+    out, _ = bq.bq_attn_kv4(*args, max_q=16, max_len=900 + b, out=room[32:32 + b], workspace=ws)
+    assert torch.equal(out, plain)
+    assert (room[:32] == 7).all() and (room[32 + b:] == 7).all()
+    again, lse2 = bq.bq_attn_kv4(*args, max_q=1000, lse=True)
+    assert torch.equal(again, plain) and torch.equal(lse, lse2)
