@@ -6,7 +6,8 @@ tensors that ``bq_kv4_pool`` allocates and these calls share.
 
 A plain call (no ``out``, no ``stream``) goes through csrc/decode_binding.cpp,
 which makes the same checks and the same C call in less of the host's time;
-whatever it does not take as it is comes back here.
+whatever it does not take as it is comes back here.  With ``stream`` a call
+allocates and runs on that stream; what it reads has to be ready there.
 """
 
 from __future__ import annotations
@@ -112,16 +113,20 @@ def _apart(rows, stride, width, name):
 
 
 def _on(stream):
-    """Where what a call enqueues beside its kernels belongs: the caller's stream, or the current one."""
+    """Where a call allocates and enqueues: the caller's stream, or the current one.  Memory for a stream has to come
+    from that stream: what was just freed on another one may still be in use there."""
     import torch
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _hold(stream, *tensors):
-    """Memory allocated here and used on a stream given by the caller stays until that stream has run the call."""
+def _share(device, *tensors):
+    """Outputs allocated on a stream of the caller's are likely to be read on the current one: their memory stays until
+    that is done with them."""
+    import torch
+    current = torch.cuda.current_stream(device)
     for t in tensors:
         if t is not None:
-            t.record_stream(stream)
+            t.record_stream(current)
 
 
 def bq_gemm_f16xi4_group(X, Wp, scale, group, zero_point=None, layout="interleaved", activation="none", out=None,
@@ -158,7 +163,8 @@ def bq_gemm_f16xi4_group(X, Wp, scale, group, zero_point=None, layout="interleav
         ld = _apart(M, X.stride(0), K, "X")
     made = out is None
     if made:
-        out = b.empty((M, N), dtype=f16, device=X.device)
+        with _on(stream):
+            out = b.empty((M, N), dtype=f16, device=X.device)
     elif not _is_whole(out, f16, (M, N), dev):
         _need_whole(out, f16, "out", (M, N), dev)
     st = b.gemm(X.data_ptr(), ld, Wp.data_ptr(), _LAYOUTS[layout] if isinstance(layout, str) else int(layout), M, N, K,
@@ -168,7 +174,7 @@ def bq_gemm_f16xi4_group(X, Wp, scale, group, zero_point=None, layout="interleav
     if st:
         b.bq._check(st, "bq_gemm_f16xi4_group")
     if stream is not None and made:
-        _hold(stream, out)
+        _share(X.device, out)
     return out
 
 
@@ -245,13 +251,14 @@ def bq_qk_norm_rope_kv4(q, k, v, codes, params, slots, positions=None, cos=None,
         max_pos, rot = want
         rot *= 2
     made = out is None
-    if made:
-        out = b.empty((T, q_heads, D), dtype=f16, device=q.device)
-    elif not _is_whole(out, f16, (T, q_heads, D), dev):
+    if not made and not _is_whole(out, f16, (T, q_heads, D), dev):
         _need_whole(out, f16, "out", (T, q_heads, D), dev)
     k_values = v_values = None
-    if values:
-        k_values, v_values = b.empty(shape, dtype=f16, device=q.device), b.empty(shape, dtype=f16, device=q.device)
+    with _on(stream):
+        if made:
+            out = b.empty((T, q_heads, D), dtype=f16, device=q.device)
+        if values:
+            k_values, v_values = (b.empty(shape, dtype=f16, device=q.device) for _ in range(2))
     st = b.write(q.data_ptr(), _row_stride(q, "q"), k.data_ptr(), _row_stride(k, "k"), v.data_ptr(),
                  _row_stride(v, "v"), T, q_heads, heads, D, None if q_weight is None else q_weight.data_ptr(),
                  None if k_weight is None else k_weight.data_ptr(), eps, cos.data_ptr() if rot else None,
@@ -263,7 +270,7 @@ def bq_qk_norm_rope_kv4(q, k, v, codes, params, slots, positions=None, cos=None,
     if st:
         b.bq._check(st, "bq_qk_norm_rope_kv4")
     if stream is not None:
-        _hold(stream, out if made else None, k_values, v_values)
+        _share(q.device, out if made else None, k_values, v_values)
     return out, k_values, v_values
 
 
@@ -314,20 +321,19 @@ def bq_attn_kv4(q, codes, params, block_table, seq_lens, cu_q=None, max_q=1, max
     elif max_len > width * page:
         raise ValueError("max_len is more than block_table holds")
     made = out is None
-    if made:
-        out = b.empty((T, q_heads, D), dtype=f16, device=q.device)
-    elif not _is_whole(out, f16, (T, q_heads, D), dev):
+    if not made and not _is_whole(out, f16, (T, q_heads, D), dev):
         _need_whole(out, f16, "out", (T, q_heads, D), dev)
-    logs = b.empty((T, q_heads), dtype=b.f32, device=q.device) if lse else None
-    own = None
-    size = 0
-    if workspace is None:
-        size = b.workspace(B, q_heads, heads, D, max_q, max_len)
-        if size:
-            workspace = own = b.empty((size,), dtype=b.u8, device=q.device)
-    else:
+    if workspace is not None:
         _need_whole(workspace, b.u8, "workspace", (None,), dev)
         size = workspace.numel()
+    with _on(stream):
+        if made:
+            out = b.empty((T, q_heads, D), dtype=f16, device=q.device)
+        logs = b.empty((T, q_heads), dtype=b.f32, device=q.device) if lse else None
+        if workspace is None:
+            size = b.workspace(B, q_heads, heads, D, max_q, max_len)
+            if size:
+                workspace = b.empty((size,), dtype=b.u8, device=q.device)
     st = b.attn(q.data_ptr(), _row_stride(q, "q"), T, q_heads, heads, D, codes.data_ptr(), params.data_ptr(), pages,
                 page, group, block_table.data_ptr(), ld_table, seq_lens.data_ptr(),
                 None if cu_q is None else cu_q.data_ptr(), B, max_q, max_len, D ** -0.5 if scale is None else scale,
@@ -337,5 +343,5 @@ def bq_attn_kv4(q, codes, params, block_table, seq_lens, cu_q=None, max_q=1, max
     if st:
         b.bq._check(st, "bq_attn_kv4")
     if stream is not None:
-        _hold(stream, out if made else None, logs, own)
+        _share(q.device, out if made else None, logs)
     return out, logs

@@ -140,3 +140,63 @@ def test_workspace_grows_with_max_q(d, rep):
     """A workspace for some number of query tokens serves every smaller one."""
     sizes = [bq.lib().bq_attn_kv4_workspace(3, 2 * rep, 2, d, q, 5000) for q in range(1, 70)]
     assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+# ---- a stream of the caller's ---------------------------------------------------------------------------------------
+
+
+class Place:
+    """Stands in for torch.cuda.stream: notes which stream is the current one."""
+
+    def __init__(self, monkeypatch):
+        self.now = []
+        place = self
+
+        class On:
+            def __init__(self, stream):
+                self.stream = stream
+
+            def __enter__(self):
+                place.now.append(self.stream)
+
+            def __exit__(self, *a):
+                place.now.pop()
+        monkeypatch.setattr(torch.cuda, "stream", On)
+
+
+def on_their_stream(rec, monkeypatch):
+    """Runs every operator on a stream; returns (stream, where outputs and workspaces were allocated, where copies
+    were made, who was recorded on which stream)."""
+    place = Place(monkeypatch)
+    made, copied, recorded = [], [], []
+    empty, contiguous = rec.bound.empty, torch.Tensor.contiguous
+    monkeypatch.setattr(rec.bound, "empty", lambda *a, **kw: made.append(list(place.now)) or empty(*a, **kw))
+    monkeypatch.setattr(torch.Tensor, "contiguous", lambda t: copied.append(list(place.now)) or contiguous(t))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s)))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: "current")
+    stream = types.SimpleNamespace(cuda_stream=77, device=torch.device("cpu"), device_index=-1)
+    w, s = weights()
+    codes, params = pool()
+    x = f16(3, 2, 64)
+    y = bq.bq_gemm_f16xi4_group(f16(3, 64), w, s, 32, stream=stream)
+    z = bq.bq_qk_norm_rope_kv4(x, x, x, codes, params, ints(0, 1, 2), values=True, stream=stream)
+    o = bq.bq_attn_kv4(x, codes, params, ints(3, 1).expand(3, 2), ints(1, 2, 3), lse=True, stream=stream)
+    return stream, made, copied, recorded, [y, *z, *o]
+
+
+def test_memory_comes_from_the_stream_that_uses_it(rec, monkeypatch):
+    """What a call on another stream allocates is that stream's: memory just freed on the current stream may still be
+    in use there.  The outputs are recorded on the current stream, where they are likely to be read."""
+    stream, made, copied, recorded, outputs = on_their_stream(rec, monkeypatch)
+    assert len(made) == 7 and all(m == [stream] for m in made)          # y; q, k, v; out, log-sums, workspace
+    assert copied == [[stream]]
+    assert [c[1][-1] for c in rec.calls] == [77] * 3
+    assert sorted(recorded) == sorted((t.data_ptr(), "current") for t in outputs)
+
+
+def test_the_current_stream_needs_neither(rec, monkeypatch):
+    place = Place(monkeypatch)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: place.now.append(s))
+    w, s = weights()
+    bq.bq_gemm_f16xi4_group(f16(3, 64), w, s, 32)
+    assert not place.now

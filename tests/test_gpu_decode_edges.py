@@ -92,3 +92,42 @@ def test_max_q_without_cu_q(b, hq, hkv, d):
     assert (room[:32] == 7).all() and (room[32 + b:] == 7).all()
     again, lse2 = bq.bq_attn_kv4(*args, max_q=1000, lse=True)
     assert torch.equal(again, plain) and torch.equal(lse, lse2)
+
+
+# ---- a stream of the caller's ---------------------------------------------------------------------------------------
+
+
+def freed_while_in_use(sizes, value=7):
+    """Frees memory of the given sizes on the current stream, with work queued there that still writes it."""
+    blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda._sleep(20_000_000)            # about 10 ms
+    for t in blocks:
+        t.fill_(value)
+
+
+def test_outputs_on_a_stream_are_not_memory_in_use_elsewhere():
+    """An earlier tensor of the same size, freed on the current stream and still written there, is not what a call on
+    another stream gets for its outputs or its workspace."""
+    side = torch.cuda.Stream()
+    x, codes, s, _ = linear.make(2, 4, 512, 256, 64, False)
+    xd, w, sd = dev(x), linear.pack(codes, "interleaved"), dev(s)
+    c = attn.make(5, [1500, 90], [1, 1], 8, 2, 128, 64, 64)
+    args = args_of(c)
+    t = torch.randn((512, 6, 64), device="cuda").half()
+    slots = torch.arange(512, dtype=torch.int32, device="cuda")
+    pool = bq.bq_kv4_pool(8, 1, 64, page_size=64, group=32)
+
+    def calls(**kw):
+        y = bq.bq_gemm_f16xi4_group(xd, w, sd, 64, **kw)
+        q, k, v = bq.bq_qk_norm_rope_kv4(t[:, :4], t[:, 4:5], t[:, 5:], *pool, slots, values=True, **kw)
+        o, lse = bq.bq_attn_kv4(*args, lse=True, **kw)
+        return y, q, k, v, o, lse
+    want = [r.clone() for r in calls()]
+    need = bq.bq_attn_kv4_workspace(2, 8, 2, 128, 1, c["table"].shape[1] * 64)
+    torch.cuda.synchronize()
+    sizes = [r.numel() * r.element_size() for r in want] + [need]
+    freed_while_in_use(sizes)
+    got = calls(stream=side)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
