@@ -1,5 +1,6 @@
 """Builds libbq.so in-tree from csrc/*.cu for sm_103a (nvcc, no cmake), and the
-native form of the decoder-layer binding from csrc/decode_binding.cpp (g++).
+native form of the decoder-layer binding from csrc/decode_binding.cpp (g++ and
+torch's headers; without them the build warns and the calls go through Python).
 
 Translation units compile in parallel; the CUDA runtime is linked statically
 so the library loads on a machine without a GPU (for symbol checks) as well
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -72,12 +74,16 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
         binding = ex.submit(_build_binding)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-        binding.result()
     tmp = LIB + ".tmp"
     r = subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    if binding.exception() is not None:
+        # the calls do without it, from Python; an older one does not go with this library
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        warnings.warn(f"the native decoder-layer binding is not built: {binding.exception()}", RuntimeWarning, stacklevel=2)
     return LIB
 
 
