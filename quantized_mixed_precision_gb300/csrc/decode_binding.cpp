@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -124,6 +125,7 @@ PyObject* py_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       z = tensor(a[4]);
       if (!shaped(z, at::kHalf, dev, N, K / group)) Py_RETURN_NONE;
     }
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(dev));   // the C calls look at the current device
     at::Tensor out = fresh({M, N}, *x, at::kHalf);
     const bq_status st = f_gemm(u16(x), K, static_cast<const uint8_t*>(w->data_ptr()), (int)layout, M, N, K, (int)group,
                                 u16(s), u16(z), (int)act, static_cast<uint16_t*>(out.data_ptr()), raw_stream(dev));
@@ -170,6 +172,7 @@ PyObject* py_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
       PyErr_Clear();
       Py_RETURN_NONE;
     }
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(dev));
     at::Tensor out = fresh({T, hq, D}, *q, at::kHalf), kval, vval;
     if (values) {
       kval = fresh({T, p.heads, D}, *q, at::kHalf);
@@ -221,6 +224,7 @@ PyObject* py_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
       PyErr_Clear();
       Py_RETURN_NONE;
     }
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(dev));
     at::Tensor out = fresh({T, hq, D}, *q, at::kHalf), logs, own;
     if (lse) logs = fresh({T, hq}, *q, at::kFloat);
     void* ws = nullptr;

@@ -7,7 +7,8 @@ tensors that ``bq_kv4_pool`` allocates and these calls share.
 A plain call (no ``out``, no ``stream``) goes through csrc/decode_binding.cpp,
 which makes the same checks and the same C call in less of the host's time;
 whatever it does not take as it is comes back here.  With ``stream`` a call
-allocates and runs on that stream; what it reads has to be ready there.
+allocates and runs on that stream; what it reads has to be ready there.  Calls
+run on their tensors' device, whichever is the current one.
 """
 
 from __future__ import annotations
@@ -49,7 +50,7 @@ class _Bound:
         self.bq, self.torch, self.lib = bq, torch, lib
         self.f16, self.f32, self.u8, self.i32 = torch.float16, torch.float32, torch.uint8, torch.int32
         self.empty = torch.empty
-        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.raw_stream, self.device_now = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
         self.gemm, self.write, self.attn = lib.bq_gemm_f16xi4_group, lib.bq_qk_norm_rope_kv4, lib.bq_attn_kv4
         self.workspace = lib.bq_attn_kv4_workspace
         # the native form of this module; it returns None for calls that it leaves to the code here
@@ -121,11 +122,14 @@ def _apart(rows, stride, width, name):
     return stride
 
 
-def _on(stream):
-    """Where a call allocates and enqueues: the caller's stream, or the current one.  Memory for a stream has to come
-    from that stream: what was just freed on another one may still be in use there."""
-    import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _on(b, dev, stream):
+    """Where a call allocates and enqueues: the tensors' device, on the caller's stream or the current one.  Memory for
+    a stream has to come from that stream: what was just freed on another one may still be in use there."""
+    if stream is not None:
+        if stream.device_index != dev:
+            raise ValueError("stream is on another device")
+        return b.torch.cuda.stream(stream)
+    return contextlib.nullcontext() if b.device_now() == dev else b.torch.cuda.device(dev)
 
 
 def _share(device, *tensors):
@@ -171,15 +175,15 @@ def bq_gemm_f16xi4_group(X, Wp, scale, group, zero_point=None, layout="interleav
             raise ValueError("X must have unit column stride")
         ld = _apart(M, X.stride(0), K, "X")
     made = out is None
-    if made:
-        with _on(stream):
-            out = b.empty((M, N), dtype=f16, device=X.device)
-    elif not _is_whole(out, f16, (M, N), dev):
+    if not made and not _is_whole(out, f16, (M, N), dev):
         _need_whole(out, f16, "out", (M, N), dev)
-    st = b.gemm(X.data_ptr(), ld, Wp.data_ptr(), _LAYOUTS[layout] if isinstance(layout, str) else int(layout), M, N, K,
-                group, scale.data_ptr(), None if zero_point is None else zero_point.data_ptr(),
-                _ACTIVATIONS[activation] if isinstance(activation, str) else int(activation), out.data_ptr(),
-                b.raw_stream(dev) if stream is None else stream.cuda_stream)
+    with _on(b, dev, stream):
+        if made:
+            out = b.empty((M, N), dtype=f16, device=X.device)
+        st = b.gemm(X.data_ptr(), ld, Wp.data_ptr(), _LAYOUTS[layout] if isinstance(layout, str) else int(layout), M, N,
+                    K, group, scale.data_ptr(), None if zero_point is None else zero_point.data_ptr(),
+                    _ACTIVATIONS[activation] if isinstance(activation, str) else int(activation), out.data_ptr(),
+                    b.raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         b.bq._check(st, "bq_gemm_f16xi4_group")
     if stream is not None and made:
@@ -263,19 +267,20 @@ def bq_qk_norm_rope_kv4(q, k, v, codes, params, slots, positions=None, cos=None,
     if not made and not _is_whole(out, f16, (T, q_heads, D), dev):
         _need_whole(out, f16, "out", (T, q_heads, D), dev)
     k_values = v_values = None
-    with _on(stream):
+    ld_q, ld_k, ld_v = _row_stride(q, "q"), _row_stride(k, "k"), _row_stride(v, "v")
+    with _on(b, dev, stream):
         if made:
             out = b.empty((T, q_heads, D), dtype=f16, device=q.device)
         if values:
             k_values, v_values = (b.empty(shape, dtype=f16, device=q.device) for _ in range(2))
-    st = b.write(q.data_ptr(), _row_stride(q, "q"), k.data_ptr(), _row_stride(k, "k"), v.data_ptr(),
-                 _row_stride(v, "v"), T, q_heads, heads, D, None if q_weight is None else q_weight.data_ptr(),
-                 None if k_weight is None else k_weight.data_ptr(), eps, cos.data_ptr() if rot else None,
-                 sin.data_ptr() if rot else None, max_pos, rot, 1 if pairs else 0,
-                 positions.data_ptr() if rot else None, slots.data_ptr(), codes.data_ptr(), params.data_ptr(), pages,
-                 page, group, out.data_ptr(), k_values.data_ptr() if values else None,
-                 v_values.data_ptr() if values else None,
-                 b.raw_stream(dev) if stream is None else stream.cuda_stream)
+        st = b.write(q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, T, q_heads, heads, D,
+                     None if q_weight is None else q_weight.data_ptr(),
+                     None if k_weight is None else k_weight.data_ptr(), eps, cos.data_ptr() if rot else None,
+                     sin.data_ptr() if rot else None, max_pos, rot, 1 if pairs else 0,
+                     positions.data_ptr() if rot else None, slots.data_ptr(), codes.data_ptr(), params.data_ptr(),
+                     pages, page, group, out.data_ptr(), k_values.data_ptr() if values else None,
+                     v_values.data_ptr() if values else None,
+                     b.raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         b.bq._check(st, "bq_qk_norm_rope_kv4")
     if stream is not None:
@@ -315,7 +320,7 @@ def bq_attn_kv4(q, codes, params, block_table, seq_lens, cu_q=None, max_q=1, max
             raise ValueError("block_table must have unit column stride")
         if B > 1 and block_table.stride(0) < width:
             # rows that overlap, such as one row expanded over a batch: the C call takes rows of their own
-            with _on(stream):
+            with _on(b, dev, stream):
                 block_table = block_table.contiguous()
         elif B > 1:
             ld_table = block_table.stride(0)
@@ -335,7 +340,8 @@ def bq_attn_kv4(q, codes, params, block_table, seq_lens, cu_q=None, max_q=1, max
     if workspace is not None:
         _need_whole(workspace, b.u8, "workspace", (None,), dev)
         size = workspace.numel()
-    with _on(stream):
+    ld_q = _row_stride(q, "q")
+    with _on(b, dev, stream):
         if made:
             out = b.empty((T, q_heads, D), dtype=f16, device=q.device)
         logs = b.empty((T, q_heads), dtype=b.f32, device=q.device) if lse else None
@@ -343,12 +349,11 @@ def bq_attn_kv4(q, codes, params, block_table, seq_lens, cu_q=None, max_q=1, max
             size = b.workspace(B, q_heads, heads, D, max_q, max_len)
             if size:
                 workspace = b.empty((size,), dtype=b.u8, device=q.device)
-    st = b.attn(q.data_ptr(), _row_stride(q, "q"), T, q_heads, heads, D, codes.data_ptr(), params.data_ptr(), pages,
-                page, group, block_table.data_ptr(), ld_table, seq_lens.data_ptr(),
-                None if cu_q is None else cu_q.data_ptr(), B, max_q, max_len, D ** -0.5 if scale is None else scale,
-                window, out.data_ptr(), logs.data_ptr() if lse else None,
-                None if workspace is None else workspace.data_ptr(), size,
-                b.raw_stream(dev) if stream is None else stream.cuda_stream)
+        st = b.attn(q.data_ptr(), ld_q, T, q_heads, heads, D, codes.data_ptr(), params.data_ptr(), pages, page, group,
+                    block_table.data_ptr(), ld_table, seq_lens.data_ptr(), None if cu_q is None else cu_q.data_ptr(),
+                    B, max_q, max_len, D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                    logs.data_ptr() if lse else None, None if workspace is None else workspace.data_ptr(), size,
+                    b.raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         b.bq._check(st, "bq_attn_kv4")
     if stream is not None:

@@ -19,7 +19,8 @@ class Recorder:
         none = staticmethod(lambda *a: None)
         self.bound = types.SimpleNamespace(
             bq=bq, torch=torch, f16=torch.float16, f32=torch.float32, u8=torch.uint8, i32=torch.int32,
-            empty=self.empty, raw_stream=lambda dev: 0, native=types.SimpleNamespace(gemm=none, write=none, attn=none),
+            empty=self.empty, raw_stream=lambda dev: 0, device_now=lambda: -1,
+            native=types.SimpleNamespace(gemm=none, write=none, attn=none),
             gemm=self.record("gemm"), write=self.record("write"), attn=self.record("attn"), workspace=lambda *a: 64)
         self.made = []
         monkeypatch.setattr(decode, "_bound", self.bound)
@@ -200,3 +201,53 @@ def test_the_current_stream_needs_neither(rec, monkeypatch):
     w, s = weights()
     bq.bq_gemm_f16xi4_group(f16(3, 64), w, s, 32)
     assert not place.now
+
+
+# ---- a device that is not the current one ---------------------------------------------------------------------------
+
+
+def test_calls_run_on_their_tensors_device(rec, monkeypatch):
+    """Kernels are launched, sized and given their status word on the current device: that has to be the tensors'."""
+    now = []
+
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            now.append(self.device)
+
+        def __exit__(self, *a):
+            now.pop()
+    monkeypatch.setattr(torch.cuda, "device", On)
+    seen = []
+    for name in ("gemm", "write", "attn"):
+        monkeypatch.setattr(rec.bound, name, lambda *a: seen.append(list(now)) or 0)
+    monkeypatch.setattr(rec.bound, "workspace", lambda *a: seen.append(list(now)) or 64)
+    w, s = weights()
+    codes, params = pool()
+    x = f16(3, 2, 64)
+
+    def calls():
+        seen.clear()
+        bq.bq_gemm_f16xi4_group(f16(3, 64), w, s, 32)
+        bq.bq_qk_norm_rope_kv4(x, x, x, codes, params, ints(0, 1, 2))
+        bq.bq_attn_kv4(x, codes, params, ints(3, 1).expand(3, 2), ints(1, 2, 3))
+        return seen
+    assert calls() == [[]] * 4                                   # already there
+    monkeypatch.setattr(rec.bound, "device_now", lambda: 5)
+    assert calls() == [[-1]] * 4                                 # -1: what CPU tensors say
+
+
+def test_a_stream_of_another_device_is_refused(rec):
+    other = types.SimpleNamespace(cuda_stream=7, device_index=1)
+    w, s = weights()
+    codes, params = pool()
+    x = f16(3, 2, 64)
+    with pytest.raises(ValueError):
+        bq.bq_gemm_f16xi4_group(f16(3, 64), w, s, 32, stream=other)
+    with pytest.raises(ValueError):
+        bq.bq_qk_norm_rope_kv4(x, x, x, codes, params, ints(0, 1, 2), stream=other)
+    with pytest.raises(ValueError):
+        bq.bq_attn_kv4(x, codes, params, torch.zeros((3, 2), dtype=torch.int32), ints(1, 2, 3), stream=other)
+    assert not rec.calls
