@@ -144,7 +144,8 @@ bq_status bq_qk_norm_rope_kv4(const uint16_t* q, int64_t ld_q, const uint16_t* k
  *   4-byte alignment is enough for block_table, seq_lens and cu_q.
  *   Lengths beyond max_len and more than max_q query tokens are cut off, a
  *   sequence whose rows are not in [0, T) is left out, a page outside the pool
- *   is read as page 0, and bq_device_status reports BQ_ERR_INVALID_ARG.
+ *   is read as page 0, and bq_device_status reports BQ_ERR_INVALID_ARG.  Rows
+ *   of out and lse that are cut off, left out or in no sequence are not written.
  *   T = 0 or B = 0 is an empty call.
  *   Errors: INVALID_ARG (null pointers, q_heads not a multiple of kv_heads,
  *   negative sizes, max_len above ld_table * page_size, an empty pool with

@@ -207,8 +207,9 @@ PyObject* py_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor *table = tensor(a[3]), *lens = tensor(a[4]), *cu = nullptr;
     if (!pool(a[1], a[2], D, dev, p) || !whole(table, at::kInt, 2, dev)) Py_RETURN_NONE;
     const int64_t B = table->size(0), width = table->size(1);
-    int64_t max_q, max_len = width * p.page, window;
-    if (!shaped(lens, at::kInt, dev, B) || !integer(a[6], max_q) || !integer(a[9], window)) Py_RETURN_NONE;
+    int64_t max_q = a[5] == Py_None || T < 1 ? 1 : T, max_len = width * p.page, window;
+    if (!shaped(lens, at::kInt, dev, B) || !integer(a[9], window)) Py_RETURN_NONE;
+    if (a[6] != Py_None && !integer(a[6], max_q)) Py_RETURN_NONE;
     if (a[5] != Py_None ? !shaped(cu = tensor(a[5]), at::kInt, dev, B + 1) : T != B) Py_RETURN_NONE;
     if (a[7] != Py_None && (!integer(a[7], max_len) || max_len > width * p.page)) Py_RETURN_NONE;
     double scale;

@@ -293,13 +293,15 @@ def bq_attn_kv4_workspace(batch, q_heads, kv_heads, head_dim, max_q, max_len) ->
     return int(_load().workspace(int(batch), int(q_heads), int(kv_heads), int(head_dim), int(max_q), int(max_len)))
 
 
-def bq_attn_kv4(q, codes, params, block_table, seq_lens, cu_q=None, max_q=1, max_len=None, scale=None, window=0,
+def bq_attn_kv4(q, codes, params, block_table, seq_lens, cu_q=None, max_q=None, max_len=None, scale=None, window=0,
                 lse=False, out=None, workspace=None, stream=None):
     """Causal attention of q (T, q_heads, D) over the 4-bit cache -> (out fp16 (T, q_heads, D), lse fp32
     (T, q_heads) or None).  Sequence b's query tokens are rows cu_q[b] .. cu_q[b + 1] - 1 of q (None: row b) and the
     last of its seq_lens[b] tokens in the cache.  ``block_table`` may have a row stride; where its rows overlap (one row
-    expanded over the batch) it is copied.  ``max_len`` bounds the lengths (None: the width of the table);
-    ``scale`` defaults to D ** -0.5; ``workspace`` (uint8) is allocated for the call when it is not given."""
+    expanded over the batch) it is copied.  ``max_q`` bounds the query tokens of a sequence (None: all of q's with
+    cu_q, which is right but plans for that many; give it where it is known) and ``max_len`` the lengths (None: the
+    width of the table); what is past a bound is cut off and reported by bq_device_status.  Rows of q that belong to no
+    sequence are left as they are in out.  ``scale`` defaults to D ** -0.5; ``workspace`` (uint8) is allocated for the call when it is not given."""
     import torch
     if out is None and stream is None:
         r = (_bound or _load()).native.attn(q, codes, params, block_table, seq_lens, cu_q, max_q, max_len, scale, window,
@@ -330,6 +332,8 @@ def bq_attn_kv4(q, codes, params, block_table, seq_lens, cu_q=None, max_q=1, max
         _need_whole(cu_q, i32, "cu_q", (B + 1,), dev)
     elif T != B:
         raise ValueError("without cu_q, q has one token for each sequence")
+    if max_q is None:
+        max_q = 1 if cu_q is None else max(T, 1)
     if max_len is None:
         max_len = width * page
     elif max_len > width * page:

@@ -251,3 +251,23 @@ def test_a_stream_of_another_device_is_refused(rec):
     with pytest.raises(ValueError):
         bq.bq_attn_kv4(x, codes, params, torch.zeros((3, 2), dtype=torch.int32), ints(1, 2, 3), stream=other)
     assert not rec.calls
+
+
+# ---- how many query tokens a sequence may have ----------------------------------------------------------------------
+
+
+def test_max_q_is_never_too_small_by_default(rec):
+    """Without max_q no row is cut off: one token a sequence without cu_q, as many as there are with it."""
+    codes, params = pool()
+    table, lens = torch.zeros((3, 1), dtype=torch.int32), ints(9, 9, 9)
+    asked = []
+    rec.bound.workspace = lambda *a: asked.append(a) or 64
+
+    def max_q(t, **kw):
+        bq.bq_attn_kv4(f16(t, 4, 64), codes, params, table, lens, **kw)
+        assert asked[-1][4] == rec.calls[-1][1][16]
+        return asked[-1][4]
+    assert max_q(3) == 1
+    assert max_q(7, cu_q=ints(0, 1, 6, 7)) == 7
+    assert max_q(7, cu_q=ints(0, 1, 6, 7), max_q=5) == 5
+    assert max_q(0, cu_q=ints(0, 0, 0, 0)) == 1

@@ -131,3 +131,17 @@ def test_outputs_on_a_stream_are_not_memory_in_use_elsewhere():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("python", [False, True])
+@pytest.mark.parametrize("n", [60, 800])
+def test_every_row_is_answered_without_max_q(n, python):
+    """With cu_q and no max_q, sequences of several tokens are not cut off after the first, by either binding."""
+    c = attn.make(n, [n, 9, n - 5], [5, 1, 17], 4, 2, 64, 16, 32)
+    args = args_of(c)
+    out = dict(out=torch.full((23, 4, 64), float("nan"), dtype=torch.float16, device="cuda")) if python else {}
+    got, _ = bq.bq_attn_kv4(*args, cu_q=dev(c["cu"]), **out)
+    torch.cuda.synchronize()
+    assert bq.bq_device_status(reset=True) == bq.BQ_OK
+    want, _, tol, _ = D.attention(c["q"], c["codes"], c["params"], c["table"], c["lens"], c["cu"], 64 ** -0.5)
+    assert (np.abs(host(got) - want) <= tol).all()
