@@ -145,3 +145,61 @@ def test_every_row_is_answered_without_max_q(n, python):
     assert bq.bq_device_status(reset=True) == bq.BQ_OK
     want, _, tol, _ = D.attention(c["q"], c["codes"], c["params"], c["table"], c["lens"], c["cu"], 64 ** -0.5)
     assert (np.abs(host(got) - want) <= tol).all()
+
+
+# ---- forms that depend on the sizes ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("group", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (16, 1), (6, 3)])
+def test_heads_of_256_over_many_keys(hq, hkv, group):
+    """D = 256 on more than 512 keys: ranges of several blocks, and their join."""
+    attn.check(attn.make(hq, [9001], [1], hq, hkv, 256, 64, group))
+    attn.check(attn.make(hq + 1, [1, 5000, 0, 70], [1] * 4, hq, hkv, 256, 16, group))
+    attn.check(attn.make(hq + 2, [2000, 700], [5, 9], hq, hkv, 256, 32, group))
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 64), (8, 2, 128), (4, 1, 256)])
+@pytest.mark.parametrize("batch", [128, 129, 300])
+def test_many_sequences_on_many_keys(batch, hq, hkv, d):
+    """More sequences than a block has threads: each thread sums the lengths of several."""
+    rng = np.random.default_rng(batch + d)
+    lens = [int(x) for x in rng.integers(0, 250, batch)]
+    lens[batch // 2], lens[-1] = 1500, 900
+    attn.check(attn.make(batch, lens, [1] * batch, hq, hkv, d, 16, 64))
+    qs = [int(x) for x in rng.integers(0, 4, batch)]
+    attn.check(attn.make(batch + 1, lens, qs, hq, hkv, d, 16, 64), window=200 if d == 128 else 0)
+
+
+@pytest.mark.parametrize("layout", ["plain", "interleaved"])
+@pytest.mark.parametrize("zp", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m,n,k", [(1, 4880, 2048), (2, 4880, 2048), (2, 4865, 2304), (1, 40, 8192), (2, 33, 8576),
+                                   (2, 17, 65536)])
+def test_one_and_two_rows_in_long_stages(m, n, k, group, zp, layout):
+    """One or two rows on stages of 512 k, whose sums of X come from its pieces."""
+    x, codes, s, z = linear.make(m * n + k, m, n, k, group, zp)
+    linear.check(x, codes, s, z, group, layout)
+
+
+@pytest.mark.parametrize("m", [32769, 32768 + 5, 32768 + 40])
+@pytest.mark.parametrize("zp", [False, True])
+def test_more_rows_than_one_launch_takes(m, zp):
+    x, codes, s, z = linear.make(m, m, 20, 160, 32, zp)
+    linear.check(x, codes, s, z, 32, "interleaved")
+    wide = torch.full((m, 168), float("nan"), dtype=torch.float16, device="cuda")
+    wide[:, :160] = dev(x)
+    linear.check(wide[:, :160], codes, s, z, 32, "plain")
+
+
+@pytest.mark.parametrize("zp", [False, True])
+@pytest.mark.parametrize("m,n,k,group", [(1, 600, 2048, 128), (5, 600, 2048, 64), (12, 600, 4096, 128),
+                                         (16, 4096, 1024, 32), (61, 1024, 8192, 128), (150, 900, 2048, 64)])
+def test_repeats_give_the_same_bits(m, n, k, group, zp):
+    """The warps', blocks' and cluster's shares of K are joined in a fixed order: a call's bits repeat."""
+    x, codes, s, z = linear.make(m + k, m, n, k, group, zp)
+    xd, w, sd, zd = dev(x), linear.pack(codes, "interleaved"), dev(s), None if z is None else dev(z)
+    first = bq.bq_gemm_f16xi4_group(xd, w, sd, group, zero_point=zd)
+    for _ in range(5):
+        again = bq.bq_gemm_f16xi4_group(xd, w, sd, group, zero_point=zd)
+        assert torch.equal(first.view(torch.int16), again.view(torch.int16))
