@@ -198,6 +198,13 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
+// What a row's sum makes of its accumulator, and the log-sum: a row that has seen no key has the sum 0, any other at
+// least 1 (its largest weight) or NaN, which stays NaN.
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+__device__ __forceinline__ float log_sum(float top, float sum) {
+  return sum == 0.0f ? -INFINITY : (top + log2f(sum)) * LN2;
+}
+
 // The params of two consecutive tokens
 template <int NG>
 __device__ __forceinline__ void load_pair(const uint8_t* p, uint32_t (&w)[2][NG]) {
@@ -808,7 +815,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
                                                               fmaf(o[nt][gr][i][2 + j], unit_v * 0.0625f, low[gr]));
           }
         if (g == 0) {
-          row[D] = sum > 0.0f ? (j ? mm.y : mm.x) : M_NONE;
+          row[D] = sum == 0.0f ? M_NONE : (j ? mm.y : mm.x);
           row[D + 1] = sum;
         }
       }
@@ -836,12 +843,12 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
       if (whole) {
         const int tok = (row0 + r) / a.rep, hr = row0 + r - tok * a.rep;
         const int64_t orow = (s.first + tok) * (int64_t)(a.heads * a.rep) + head * a.rep + hr;
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const float inv = inverse(sum);
         uint2 h;
         h.x = pack_h2(v.x * inv, v.y * inv);
         h.y = pack_h2(v.z * inv, v.w * inv);
         *reinterpret_cast<uint2*>(a.out + orow * D + d) = h;
-        if (a.lse && d == 0) a.lse[orow] = sum > 0.0f ? (mt + log2f(sum)) * LN2 : -INFINITY;
+        if (a.lse && d == 0) a.lse[orow] = log_sum(mt, sum);
       } else {
         const int64_t slot = 2 * (int64_t)blockIdx.x + (at != at0 ? 1 : 0);
         float* part = a.parts + (slot * C::ROWS + r) * JS;
@@ -895,12 +902,12 @@ __global__ void __launch_bounds__(256) attn_kv4_join_kernel(const AttnParams a) 
   auto store = [&](int r, float4 v, float sum, float mt) {
     const int tok = (row0 + r) / a.rep, hr = row0 + r - tok * a.rep;
     const int64_t orow = (mm.first + tok) * (int64_t)(a.heads * a.rep) + mm.head * a.rep + hr;
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = inverse(sum);
     uint2 h;
     h.x = pack_h2(v.x * inv, v.y * inv);
     h.y = pack_h2(v.z * inv, v.w * inv);
     *reinterpret_cast<uint2*>(a.out + orow * D + d) = h;
-    if (a.lse && d == 0) a.lse[orow] = sum > 0.0f ? (mt + log2f(sum)) * LN2 : -INFINITY;
+    if (a.lse && d == 0) a.lse[orow] = log_sum(mt, sum);
   };
   // Adds parts i, i + by, ... of row r below n to (v, sum), four loads at a time, and keeps their maximum in mt.
   auto add = [&](int i, int by, int r, float4& v, float& sum, float& mt) {

@@ -203,3 +203,26 @@ def test_repeats_give_the_same_bits(m, n, k, group, zp):
     for _ in range(5):
         again = bq.bq_gemm_f16xi4_group(xd, w, sd, group, zero_point=zd)
         assert torch.equal(first.view(torch.int16), again.view(torch.int16))
+
+
+# ---- NaN and infinities that a row sees -----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("where", ["q", "q inf", "key", "value"])
+@pytest.mark.parametrize("hq,hkv,d,group", [(8, 2, 128, 64), (4, 1, 64, 32), (16, 1, 256, 128)])
+@pytest.mark.parametrize("n", [70, 3000])
+def test_nan_is_not_an_empty_row(n, hq, hkv, d, group, where):
+    """A NaN (or an infinite product) among what a row sees is NaN in its result, not the zeros of a row without keys;
+    other rows, and other groups of a value, do not notice."""
+    c = attn.make(n + d, [n, n], [1, 1], hq, hkv, d, 16, group, stale=False)
+    at = c["table"][0, 40 // 16], 40 % 16
+    if where.startswith("q"):
+        c["q"][0, 1, 5] = np.nan if where == "q" else np.inf
+    else:
+        c["params"][at[0], 0 if where == "key" else 1, 0, at[1], 1, 1] = np.nan
+    out, lse = (host(t) for t in bq.bq_attn_kv4(*args_of(c), lse=True))
+    with np.errstate(invalid="ignore"):
+        want, wlse, tol, tol_lse = D.attention(c["q"], c["codes"], c["params"], c["table"], c["lens"], None, d ** -0.5)
+    bad, badl = np.isnan(want), np.isnan(wlse)
+    assert bad.any() and (np.isnan(out) == bad).all() and (np.isnan(lse) == badl).all()
+    assert (np.abs(out - want) <= tol)[~bad].all() and (np.abs(lse - wlse) <= tol_lse)[~badl].all()
