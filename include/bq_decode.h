@@ -123,10 +123,14 @@ bq_status bq_qk_norm_rope_kv4(const uint16_t* q, int64_t ld_q, const uint16_t* k
  *   A row that sees no key (len = 0, or p < 0) gives out = 0 and lse = -inf.
  *   Scores, the running maximum and sum, and the accumulators are fp32; the
  *   weight of a key, times its value's step, is rounded to fp16 for the
- *   tensor cores.  What the pool holds past a sequence's length (NaN
- *   included) does not reach the result.  NaN in what a row sees makes its
- *   result NaN; NaN in the params of a key may also reach query tokens of the
- *   same sequence that stand before the key, whose weight for it is 0.
+ *   tensor cores, with a power of two that follows the steps of each group of
+ *   dims, 32 keys at a time (16 with D = 256 and several query rows): a weight
+ *   (of the row's largest so far) times a step that is below 2**-14 of the
+ *   largest step beside it is held to 2**-25 of that step instead of 11 bits.
+ *   What the pool holds past a sequence's length (NaN included) does not
+ *   reach the result.  NaN in what a row sees makes its result NaN; NaN in the
+ *   params of a key may also reach query tokens of the same sequence that
+ *   stand before the key, whose weight for it is 0.
  *
  *   q            device fp16, T rows of q_heads * D contiguous elements, leading
  *                dimension ld_q (a multiple of 8)

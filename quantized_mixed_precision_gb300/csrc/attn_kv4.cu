@@ -57,6 +57,7 @@ constexpr int64_t DIRECT_LEN = 512;   // up to here one block takes a whole unit
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float M_NONE = -1e30f;  // running maximum before any key
+constexpr float VF_MOST = 1073741824.0f;   // 2**30: the smallest step, 2**-24, times it is 64
 
 // A unit that has to be joined: its blocks, the first of them, whether that holds it in its second slot, and what the
 // join needs of the sequence
@@ -203,6 +204,15 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
 __device__ __forceinline__ float inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
 __device__ __forceinline__ float log_sum(float top, float sum) {
   return sum == 0.0f ? -INFINITY : (top + log2f(sum)) * LN2;
+}
+
+// x / p of a power of two p.  The inverse by its exponent saves 0.7 us at 97 keys and 3 at 16 sequences of 4k with D = 256;
+// with several tiles of query rows, whose registers are all taken, ptxas keeps it over the loop: 2 x 256 tokens on 16k
+// keys 404 us, 382 with a division, 16 x 4 tokens on 4k with D = 256 70 and 63.
+template <bool DIVIDE>
+__device__ __forceinline__ float over_power(float x, float p) {
+  if constexpr (DIVIDE) return x / p;
+  else return x * pow2f(-ilog2f(p));
 }
 
 // The params of two consecutive tokens
@@ -540,7 +550,9 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
     float o[NT][NG][C::MT][4];
     P2 mid[NT][NG], m[NT], l[NT];         // columns 2t, 2t + 1; mid: what the codes' middles add, times vf
     P2 back[NR][NG];                      // - 7.5 times the signed weights (with many rows, for the registers' sake, in mid)
-    float vf = pow2f(30);                 // power of two that the values' steps carry into fp16
+    float vf[NG];                         // powers of two that the steps of a group of the values carry into fp16
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) vf[gr] = VF_MOST;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt] = l[nt] = p2(0.0f, 0.0f);
@@ -656,7 +668,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
 
       // ---- running maximum, renewed only when a score passes it by 2**8 ----
       float2 top[NT];
-      float step_top = 0.0f, most = -INFINITY;
+      float step_top[NG], most = -INFINITY;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         top[nt] = f2(sv[0][nt][0]);
@@ -668,26 +680,34 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
         }
         most = fmaxf(most, fmaxf(top[nt].x, top[nt].y));
       }
-      {
+      // The largest step of a group times its factor is kept in [1, 240] (a lane that sees it elsewhere asks for the
+      // renewal below, which looks at all of them): a weight is below 2**8, so that weight * step * factor stays below
+      // fp16's 65504, and for that step weights down to 2**-14 stay normal numbers.  With one factor for all groups,
+      // only ever lowered, the smaller of two groups 2**27 apart was 37 times as far off as its bound.  A factor for each
+      // that also rises costs 0.5 us of 137 on 32 sequences of 32k keys.
+      bool renew = fresh || most > 8.0f;
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
         __half2 most_step = __float2half2_rn(0.0f);
 #pragma unroll
         for (int h = 0; h < HB; ++h)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr)
-              most_step = __hmax2(most_step, __habs2(*reinterpret_cast<const __half2*>(&vp[h][r][gr])));
-        step_top = __low2float(most_step);
+            most_step = __hmax2(most_step, __habs2(*reinterpret_cast<const __half2*>(&vp[h][r][gr])));
+        step_top[gr] = __low2float(most_step);
+        const float v = step_top[gr] * vf[gr];
+        renew = renew || !(v >= 1.0f && v <= 240.0f);
       }
-      // (weight < 2**8, so weight * step * vf stays below fp16's 65504 while step * vf <= 240)
-      if (__any_sync(0xffffffffu, fresh || most > 8.0f || step_top * vf > 240.0f)) {
+      if (__any_sync(0xffffffffu, renew)) {
+        float fv[NG];
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) step_top = fmaxf(step_top, __shfl_xor_sync(0xffffffffu, step_top, x));
-        float fv = 1.0f;
-        if (step_top * vf > 240.0f) {     // step_top to [2**6, 2**7)
-          const float nv = pow2f(6 - ilog2f(step_top));
-          fv = nv / vf;
-          vf = nv;
+        for (int gr = 0; gr < NG; ++gr) {
+          // (not negative, so that its bits compare as integers)
+          const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(step_top[gr])));
+          const bool keep = top * vf[gr] <= 240.0f && (top * vf[gr] >= 1.0f || vf[gr] == VF_MOST);
+          const float nv = keep ? vf[gr] : (top > 0.0f ? pow2f(6 - ilog2f(top)) : VF_MOST);   // top to [2**6, 2**7)
+          fv[gr] = over_power<C::WIDE && (NT > 1)>(nv, vf[gr]);
+          vf[gr] = nv;
         }
         bool all = true;
 #pragma unroll
@@ -705,7 +725,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
             all = all && (seen & bit);
             f[j] = ex2(fminf(-up[j], 0.0f));       // (nothing has been summed where up < 0)
           }
-          const P2 ff = p2(f[0], f[1]), down = p2(-up[0], -up[1]), of = p2(f[0] * fv, f[1] * fv);
+          const P2 ff = p2(f[0], f[1]), down = p2(-up[0], -up[1]);
           m[nt] = add2(m[nt], p2(up[0], up[1]));
           l[nt] = mul2(l[nt], ff);
 #pragma unroll
@@ -714,6 +734,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
             for (int r = 0; r < 2; ++r) sv[h][nt][r] = add2(sv[h][nt][r], down);
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
+            const P2 of = p2(f[0] * fv[gr], f[1] * fv[gr]);
             mid[nt][gr] = mul2(mid[nt][gr], of);
             if (!C::WIDE) back[nt % NR][gr] = mul2(back[nt % NR][gr], of);
 #pragma unroll
@@ -740,7 +761,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
             const float2 v = unpack_h2(vp[h][r][gr]);
-            const float w = v.x * (turned ? -vf : vf), low = vf * fmaf(7.5f, v.x, v.y);
+            const float w = v.x * (turned ? -vf[gr] : vf[gr]), low = vf[gr] * fmaf(7.5f, v.x, v.y);
             vs[gr] = p2(w, w);
             vl[gr] = p2(low, low);
           }
@@ -786,7 +807,9 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
     __syncthreads();                      // every warp is done with its ring
     float* const js = reinterpret_cast<float*>(smem);
     constexpr int JS = D + 4;             // floats of a row: D values, maximum, sum, padding
-    const float unit_v = pow2f(24) / vf;
+    float unit_v[NG];
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) unit_v[gr] = over_power<C::WIDE && (NT > 1)>(pow2f(24), vf[gr]);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 mm = f2(m[nt]), ll = f2(l[nt]);
@@ -796,7 +819,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
           const float2 x = f2(C::WIDE ? mid[nt][gr] : add2(mid[nt][gr], back[nt % NR][gr]));
-          low[gr] = (j ? x.y : x.x) / vf;
+          low[gr] = over_power<C::WIDE && (NT > 1)>(j ? x.y : x.x, vf[gr]);
         }
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
@@ -811,8 +834,8 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
           for (int i = 0; i < C::MT; ++i) {
             // tile i of a group: byte g of its i-th 8, dims 2g and 2g + 1
             const int d = gr * C::G + 16 * i + 2 * g;
-            *reinterpret_cast<float2*>(row + d) = make_float2(fmaf(o[nt][gr][i][j], unit_v, low[gr]),
-                                                              fmaf(o[nt][gr][i][2 + j], unit_v * 0.0625f, low[gr]));
+            *reinterpret_cast<float2*>(row + d) = make_float2(fmaf(o[nt][gr][i][j], unit_v[gr], low[gr]),
+                                                              fmaf(o[nt][gr][i][2 + j], unit_v[gr] * 0.0625f, low[gr]));
           }
         if (g == 0) {
           row[D] = sum == 0.0f ? M_NONE : (j ? mm.y : mm.x);

@@ -226,3 +226,62 @@ def test_nan_is_not_an_empty_row(n, hq, hkv, d, group, where):
     bad, badl = np.isnan(want), np.isnan(wlse)
     assert bad.any() and (np.isnan(out) == bad).all() and (np.isnan(lse) == badl).all()
     assert (np.abs(out - want) <= tol)[~bad].all() and (np.abs(lse - wlse) <= tol_lse)[~badl].all()
+
+
+# ---- values of very different size ----------------------------------------------------------------------------------
+
+
+def grow(c, dims, keys, by):
+    """Values of the groups `dims` of the keys `keys` of the first sequence, times a power of two."""
+    for t in keys:
+        row = c["params"][c["table"][0, t // 16], 1, :, t % 16, dims]
+        c["params"][c["table"][0, t // 16], 1, :, t % 16, dims] = (row.astype(np.float32) * 2.0 ** by).astype(np.float16)
+
+
+@pytest.mark.parametrize("hq,hkv,d,group", [(8, 1, 128, 64), (8, 2, 128, 32), (4, 1, 64, 32), (16, 1, 256, 64)])
+@pytest.mark.parametrize("n", [20, 50, 700])
+def test_groups_of_very_different_size(n, hq, hkv, d, group):
+    """One group of dims holds values 2**27 times as large as the others': each keeps its own precision."""
+    c = attn.make(n + d, [n], [1], hq, hkv, d, 16, group, stale=False)
+    grow(c, 0, range(n), 13)
+    for g in range(1, d // group):
+        grow(c, g, range(n), -13 - g)
+    attn.check(c)
+
+
+@pytest.mark.parametrize("hq,hkv,d,group", [(8, 1, 128, 64), (8, 2, 128, 128), (4, 1, 64, 32), (16, 1, 256, 64)])
+@pytest.mark.parametrize("large", [1, 32, 128])
+def test_large_values_without_weight(large, hq, hkv, d, group):
+    """The first keys hold values 2**27 times as large as the last ones', and only the last ones have any weight: these
+    keep their precision."""
+    n = 130
+    c = attn.make(large + d, [n], [1], hq, hkv, d, 16, group, stale=False)
+    c["q"] = np.abs(c["q"])
+    grow(c, slice(None), range(large), 13)
+    grow(c, slice(None), range(128, n), -14)
+    low = -30 * d ** 0.5 / c["q"].astype(np.float64).sum(-1).min()
+    for t in range(128):
+        c["params"][c["table"][0, t // 16], 0, :, t % 16] = (0, low)      # scores of -30 or less, others of about 2
+    attn.check(c)
+
+
+@pytest.mark.parametrize("hq,hkv,d,group", [(8, 1, 128, 64), (4, 1, 64, 32), (16, 1, 256, 64)])
+def test_steps_that_shrink_along_the_sequence(hq, hkv, d, group):
+    """The values' steps fall along the sequence by 2**20, and rise again by as much: a common factor has to follow them
+    both ways."""
+    c = attn.make(d, [800], [1], hq, hkv, d, 16, group, qstd=0.2, stale=False)
+    for t in range(800):
+        grow(c, slice(None), [t], 6 - abs(t // 16 - 25) * -0.8 - 20)
+    attn.check(c)
+
+
+def test_a_group_without_steps_beside_others():
+    """Steps of zero (constant groups) among large and small ones, key by key and group by group."""
+    c = attn.make(9, [500], [1], 8, 1, 128, 16, 32, stale=False)
+    grow(c, 0, range(500), 12)
+    grow(c, 2, range(500), -12)
+    for t in range(500):
+        c["params"][c["table"][0, t // 16], 1, :, t % 16, 1, 0] = 0
+        if t // 32 % 3 == 0:
+            c["params"][c["table"][0, t // 16], 1, :, t % 16, 2, 0] = 0
+    attn.check(c)
