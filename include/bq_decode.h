@@ -156,7 +156,7 @@ bq_status bq_qk_norm_rope_kv4(const uint16_t* q, int64_t ld_q, const uint16_t* k
  *   Errors: INVALID_ARG (null pointers, q_heads not a multiple of kv_heads,
  *   negative sizes, max_len above ld_table * page_size, an empty pool with
  *   max_len > 0, a workspace that is too small), ALIGNMENT, UNSUPPORTED (the
- *   pool's shape, max_len above 2**30), CUDA.
+ *   pool's shape, max_len above 2**30, T * q_heads of 2**31 or more), CUDA.
  */
 size_t bq_attn_kv4_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q,
                              int64_t max_len);

@@ -12,6 +12,7 @@ constexpr int64_t MAX_ROWS = 1LL << 24;
 constexpr int64_t MAX_HEADS = 65536;
 constexpr int64_t MAX_KV_HEADS = 4096;   // a page's bytes stay below 2**32
 constexpr int64_t MAX_LEN = 1LL << 30;   // keys of a sequence
+constexpr int64_t MAX_QUERY_ROWS = 1LL << 31;   // tokens times heads, counted in 32 bits
 
 inline bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 inline bool aligned16(const void* p) { return aligned(p, 16); }
@@ -121,7 +122,7 @@ bq_status bq_attn_kv4(const uint16_t* q, int64_t ld_q, int64_t T, int64_t q_head
   if (!q || !out || !seq_lens || (max_len > 0 && (!codes || !params || !block_table || num_pages < 1)))
     return BQ_ERR_INVALID_ARG;
   if (q_heads > MAX_HEADS || kv_heads > MAX_KV_HEADS || T > MAX_ROWS || B > MAX_ROWS || max_q > MAX_ROWS ||
-      max_len > MAX_LEN)
+      max_len > MAX_LEN || T * q_heads >= MAX_QUERY_ROWS)
     return BQ_ERR_UNSUPPORTED;
   if (!valid_pool(D, group, page_size, num_pages)) return BQ_ERR_UNSUPPORTED;
   if (ld_q < q_heads * D || max_len > ld_table * page_size) return BQ_ERR_INVALID_ARG;
@@ -130,9 +131,9 @@ bq_status bq_attn_kv4(const uint16_t* q, int64_t ld_q, int64_t T, int64_t q_head
   if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(lse, 4) ||
       !aligned16(workspace))
     return BQ_ERR_ALIGNMENT;
-  // Without cu_q a sequence has one query token whatever its bound says: the grids, the records of the parts and the
-  // workspace follow what there is (never more workspace than a larger max_q asks for).
-  if (!cu_q) max_q = 1;
+  // No sequence has more than T query tokens, and one each without cu_q, whatever the bound says: the grids, the records
+  // of the parts and the workspace follow what there can be (never more workspace than a larger max_q asks for).
+  max_q = cu_q ? (max_q < T ? max_q : T) : 1;
   const size_t need = attn_kv4_workspace(B, q_heads, kv_heads, D, max_q, max_len);
   if (need > 0 && (!workspace || workspace_bytes < need)) return BQ_ERR_INVALID_ARG;
   AttnKv4Args a{};

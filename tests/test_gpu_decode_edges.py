@@ -133,6 +133,21 @@ def test_outputs_on_a_stream_are_not_memory_in_use_elsewhere():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("n", [60, 800])
+def test_a_bound_far_above_what_there_is(n):
+    """max_q times the heads of a kv head passes 32 bits; the query tokens do not."""
+    c = attn.make(n, [n, 3], [2, 1], 4096, 1, 64, 16, 64, qstd=0.5)
+    args = args_of(c)
+    kw = dict(cu_q=dev(c["cu"]), lse=True)
+    got, lse = bq.bq_attn_kv4(*args, max_q=1 << 24, **kw)
+    want, wlse = bq.bq_attn_kv4(*args, max_q=2, **kw)
+    assert torch.equal(got, want) and torch.equal(lse, wlse)
+    rows = [0, 1, 2047, 4095]
+    few = {**c, "q": np.repeat(c["q"][:, rows], 2, 1)}
+    o, _, tol, _ = D.attention(few["q"], c["codes"], c["params"], c["table"], c["lens"], c["cu"], 64 ** -0.5)
+    assert (np.abs(host(got)[:, rows] - o[:, ::2]) <= tol[:, ::2]).all()
+
+
 @pytest.mark.parametrize("python", [False, True])
 @pytest.mark.parametrize("n", [60, 800])
 def test_every_row_is_answered_without_max_q(n, python):
