@@ -13,9 +13,12 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdint>
+#include <exception>
 
 #include "bq_decode.h"
 
@@ -100,10 +103,11 @@ inline PyObject* done(bq_status st, PyObject* value) {
   return PyLong_FromLong(st);
 }
 
-#define CATCH_ALL                                     \
-  catch (const std::exception& e) {                   \
-    PyErr_SetString(PyExc_RuntimeError, e.what());    \
-    return nullptr;                                   \
+// (as torch's own errors: memory that there is not is torch.OutOfMemoryError)
+#define CATCH_ALL                                                    \
+  catch (...) {                                                      \
+    torch::translate_exception_to_python(std::current_exception());  \
+    return nullptr;                                                  \
   }
 
 // (X, Wp, scale, group, zero_point or None, layout, activation)

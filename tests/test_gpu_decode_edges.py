@@ -300,3 +300,24 @@ def test_a_group_without_steps_beside_others():
         if t // 32 % 3 == 0:
             c["params"][c["table"][0, t // 16], 1, :, t % 16, 2, 0] = 0
     attn.check(c)
+
+
+# ---- memory that there is not ---------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("python", [False, True])
+def test_out_of_memory_is_torchs_own_error(python):
+    """An output that the process may not allocate: torch's error type, by either binding, and the next call works."""
+    x = torch.zeros((1 << 17, 32), dtype=torch.float16, device="cuda")
+    w = torch.zeros((1 << 15, 16), dtype=torch.uint8, device="cuda")
+    s = torch.ones((1 << 15, 1), dtype=torch.float16, device="cuda")
+    kw = dict(stream=torch.cuda.current_stream()) if python else {}
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 30)) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):      # 8 GB of an allowance of 1
+            bq.bq_gemm_f16xi4_group(x, w, s, 32, **kw)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert not bq.bq_gemm_f16xi4_group(x[:3], w[:40], s[:40], 32, **kw).any()
