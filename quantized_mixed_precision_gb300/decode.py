@@ -97,7 +97,7 @@ def _need_whole(t, dtype, name, shape, device):
 
 def _is_whole(t, dtype, shape, device):
     """_need_whole without the reasons."""
-    return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
+    return getattr(t, "dtype", None) is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
 
 
 def _row_stride(t, name):
@@ -205,10 +205,9 @@ def bq_kv4_pool(num_pages, kv_heads, head_dim, page_size=64, group=64, device="c
 
 def _pool(b, codes, params, D, dev):
     """(pages, kv heads, page size, group) of a pool of head dim D."""
-    _, u8, f16 = b, b.u8, b.f16
-    if codes.dim() != 5 or params.dim() != 6:
-        _need(codes, u8, "codes", 5, dev)
-        _need(params, f16, "params", 6, dev)
+    u8, f16 = b.u8, b.f16
+    _need(codes, u8, "codes", 5, dev)
+    _need(params, f16, "params", 6, dev)
     pages, two, heads, page, half = codes.shape
     groups = params.shape[4]
     if two != 2 or not groups or (2 * half) % groups:
@@ -216,10 +215,8 @@ def _pool(b, codes, params, D, dev):
     if 2 * half != D:
         raise ValueError("the pool's head dim is not q's")
     want = (pages, 2, heads, page, groups, 2)
-    if not (codes.dtype is u8 and codes.get_device() == dev and codes.is_contiguous()
-            and _is_whole(params, f16, want, dev)):
-        _need_whole(codes, u8, "codes", (pages, 2, heads, page, half), dev)
-        _need_whole(params, f16, "params", want, dev)
+    _need_whole(codes, u8, "codes", (pages, 2, heads, page, half), dev)
+    _need_whole(params, f16, "params", want, dev)
     return pages, heads, page, D // groups
 
 
@@ -243,7 +240,7 @@ def bq_qk_norm_rope_kv4(q, k, v, codes, params, slots, positions=None, cos=None,
     pages, heads, page, group = _pool(b, codes, params, D, dev)
     shape = (T, heads, D)
     for t, name in ((k, "k"), (v, "v")):
-        if t.dtype is not f16 or t.shape != shape or t.get_device() != dev:
+        if getattr(t, "dtype", None) is not f16 or t.shape != shape or t.get_device() != dev:
             _need(t, f16, name, 3, dev)
             raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if q_weight is not None and not _is_whole(q_weight, f16, (D,), dev):

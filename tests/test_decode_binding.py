@@ -271,3 +271,34 @@ def test_max_q_is_never_too_small_by_default(rec):
     assert max_q(7, cu_q=ints(0, 1, 6, 7)) == 7
     assert max_q(7, cu_q=ints(0, 1, 6, 7), max_q=5) == 5
     assert max_q(0, cu_q=ints(0, 0, 0, 0)) == 1
+
+
+# ---- arguments that are not tensors ---------------------------------------------------------------------------------
+
+
+def test_what_is_not_a_tensor_is_a_type_error(rec):
+    w, s = weights()
+    codes, params = pool()
+    x, i = f16(3, 2, 64), ints(0, 1, 2)
+    c = torch.zeros((4, 16))
+    calls = [
+        (bq.bq_gemm_f16xi4_group, dict(X=f16(3, 64), Wp=w, scale=s, group=32, zero_point=s, out=f16(3, 8)),
+         ("X", "Wp", "scale", "zero_point", "out")),
+        (bq.bq_qk_norm_rope_kv4, dict(q=x, k=x, v=x, codes=codes, params=params, slots=i, positions=i, cos=c, sin=c,
+                                      q_weight=f16(64), k_weight=f16(64), out=x),
+         ("q", "k", "v", "codes", "params", "slots", "positions", "cos", "sin", "q_weight", "k_weight", "out")),
+        (bq.bq_attn_kv4, dict(q=x, codes=codes, params=params, block_table=torch.zeros((3, 1), dtype=torch.int32),
+                              seq_lens=i, cu_q=ints(0, 1, 2, 3), out=x, workspace=torch.zeros(64, dtype=torch.uint8)),
+         ("q", "codes", "params", "block_table", "seq_lens", "cu_q", "out", "workspace")),
+    ]
+    optional = ("zero_point", "out", "q_weight", "k_weight", "cu_q", "workspace")
+    for f, kw, names in calls:
+        f(**kw)
+        for name in names:
+            for bad in ([0.0], "x") + (() if name in optional else (None,)):
+                if (name, bad) == ("cos", None):
+                    continue                                # (sin without cos, which is refused below)
+                with pytest.raises(TypeError):
+                    f(**{**kw, name: bad})
+    with pytest.raises(TypeError):
+        bq.bq_qk_norm_rope_kv4(x, x, x, codes, params, i, i, None, c)
