@@ -48,6 +48,9 @@ extern "C" {
  *   scale       device fp16 (N, K / group), contiguous
  *   zero_point  device fp16 (N, K / group), contiguous, or NULL
  *   Y           device fp16 (M, N), contiguous
+ *   X is finite: with M <= 8 or zero points the sums of X, and of X times the
+ *   codes, are made apart, so that an infinity makes its row NaN also where the
+ *   product would be infinite.
  *   Any M and any N.  M = 0 or N = 0 is an empty call; K = 0 writes zeros.
  *   With M > 8 the waits for copies are bounded (bq_set_wait_timeout_ns); one
  *   that gives up is reported as BQ_ERR_TIMEOUT by bq_device_status.

@@ -17,7 +17,8 @@
 // Two things keep the second sum exact where it cancels.  The weights p step are
 // rounded to fp16, so the codes count from their middle: from 0, the weights'
 // errors met values of 2.5 to 5 times the size, and the result was 2.4 to 5 times
-// as far off.  And codes are not negative, while the tensor cores truncate as
+// as far off.  (A power of two for each group carries weight * step into fp16's
+// range; it follows the steps, 32 keys at a time.)  And codes are not negative, while the tensor cores truncate as
 // they add: every second 16 keys enter as -(p step) (15 - u), which turns about
 // the middle and costs nothing (a LOP3 takes the complement), so that the
 // accumulators stay as small as the result instead of growing with the sum of
@@ -26,14 +27,14 @@
 //
 // What bounds it.  One new token a sequence should be bound by reading the cache:
 // 32 sequences of 32k keys (D 128, 8 kv heads, 4 query heads each, groups of 64:
-// 739 MB) take 137 us, 5.4 TB/s, 79 % of a plain copy's rate.  What is left is
+// 739 MB) take 138 us, 5.4 TB/s, 79 % of a plain copy's rate.  What is left is
 // instructions (about 600 for a warp's tile, 60 % of the issue slots over the
 // whole launch), the first data 4.6 us after the launch, and blocks that end up to
 // 16 us apart.  A short cache is bound by the fixed 10 us or
-// so of scan, first data, straddled units and join (16 sequences of 4k keys 21.4 us,
-// one of 128k 34.3), and the direct form by its latency (97 keys 4.4 us).  Many
-// queries are bound by arithmetic: 2 x 256 tokens on 16k keys take 382 us
-// (240 TFLOP/s of the formula's), the tensor pipe busy 41 % of the time at the
+// so of scan, first data, straddled units and join (16 sequences of 4k keys 20.9 us,
+// one of 128k 34.1), and the direct form by its latency (97 keys 3.7 us).  Many
+// queries are bound by arithmetic: 2 x 256 tokens on 16k keys take 383 us
+// (240 TFLOP/s of the formula's), the tensor pipe busy 42 % of the time at the
 // two warps a scheduler that 255 registers allow.
 //
 // Work is split over warps by tiles of 32 keys.  A unit is one (sequence,
@@ -53,7 +54,11 @@ namespace {
 
 constexpr int AW = 4;             // warps of a block
 constexpr int TILE = 32;          // keys of a warp's tile
-constexpr int64_t DIRECT_LEN = 512;   // up to here one block takes a whole unit
+// Up to here one block takes a whole unit, beyond it the grid shares the keys and a second kernel joins them.  Direct and
+// split, with 8 kv heads of 128: 16 sequences of 300 keys 5.4 and 11.9 us, of 500 6.0 and 11.7, of 1000 8.8 and 14.2, of
+// 1500 12.1 and 16.0; one sequence of 300 5.2 and 7.3, of 500 5.7 and 7.4, of 768 7.0 and 7.6, of 1000 8.6 and 7.7, of 2000
+// 13.8 and 10.7.  The bound is the largest power of two at which no batch loses; larger batches would gain up to 1500.
+constexpr int64_t DIRECT_LEN = 512;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float M_NONE = -1e30f;  // running maximum before any key
@@ -141,9 +146,10 @@ __device__ __forceinline__ int64_t seq_cost(const AttnParams& a, const Seq& s) {
   return (int64_t)s.tiles * s.qtiles * a.heads;
 }
 
-// Blocks per SM, by the registers of the accumulators: what fits without spills.  With D = 128 and 8 query rows, 3 blocks
-// (168 registers a thread) took 133 us for 739 MB of cache, 4 blocks (128 registers) 147 us, 2 blocks 138 us (before
-// the second sum's signs, which cost 3 us).
+// Blocks per SM, by the registers of the accumulators.  With D = 128 and 8 query rows, 3 blocks (168 registers a thread,
+// nothing spilled) took 133 us for 739 MB of cache, 4 blocks (128 registers) 147 us, 2 blocks 138 us (before the second
+// sum's signs, which cost 3 us).  With more query rows a thread spills some of its values (16 rows: 0.1 to 0.5 KB; 32 rows
+// at 255 registers: 0.2 to 0.9).
 constexpr int blocks_per_sm(int D, int nt) { return D < 256 && D * nt <= 256 ? 3 : 2; }
 
 template <int D, int NG, int NT>
@@ -1007,7 +1013,10 @@ inline int row_tiles(int64_t rep, int64_t max_q, int64_t D) {
 // (and joined), or one block takes each unit.
 inline bool split(int64_t max_len) { return max_len > DIRECT_LEN; }
 
-// Few units have many parts each: a block of the join takes one row of one.
+// Few units have many parts each: a block of the join takes one row of one, its threads a share of the parts.  That and a
+// block for all rows, on sequences of 4k keys with 8 kv heads: one sequence (8 units) 11.7 and 22.5 us, two 11.3 and 16.8,
+// four (32 units) 12.9 and 15.2, eight 18.1 and 18.4, sixteen (128 units) 24.3 and 25.7.  Beyond 32 units it would
+// still gain 0.3 to 1.5 us (the records hold as many units as the grid has blocks): not taken so far.
 constexpr int64_t FEW_UNITS = 32;
 
 inline size_t meta_bytes(size_t grid) { return (grid * sizeof(Meta) + 15) / 16 * 16; }

@@ -25,7 +25,8 @@ namespace {
 // ring of its own, so that no warp waits for another before the end.  A stage is
 // 512 k (256 with more than two rows of X, whose share of the ring would leave
 // fewer blocks on an SM): 512 against 1024 at M = 1 was 7.9 against 8.5 us, 256
-// against 512 at M = 8 18.1 against 23 (two blocks fewer an SM).
+// against 512 at M = 8 18.1 against 23 (two blocks fewer an SM; 16.1 and 19.9 now,
+// groups of 128 and groups of 64 with zero points).
 // 1 x 11008 x 4096 in groups of 128, one call after another on weights larger
 // than L2: 7.1 us, 3.3 TB/s.  The copies alone take 3.7; the arithmetic, about 170
 // instructions for 16 columns and 128 k in a warp, 3.8 after a block's data has
@@ -320,8 +321,9 @@ cudaError_t launch_gemv(const GroupGemmArgs& a, cudaStream_t stream) {
 // what most warps wait for, with the fill of the ring before and the cluster's
 // sum after it; at 16 rows (15 %) it is those two and the latency of a slab.
 // 61 x 8192 x 8192 in groups of 128 takes 38.3 us (214 TFLOP/s, 0.9 TB/s of
-// weights), 256 x 8192 x 8192 122 (282 TFLOP/s), 16 x 11008 x 4096 in groups of 64
-// with zero points 15.8 (1.6 TB/s).
+// weights), 16 x 11008 x 4096 in groups of 64 with zero points 16.0 (1.6 TB/s).  Every
+// 64 rows convert the weights again, which bounds prompts: 256 x 8192 x 8192 122 us
+// (282 TFLOP/s), 256 x 11008 x 4096 100 (231), 2048 x 4096 x 4096 269 (255).
 // ---------------------------------------------------------------------------
 constexpr int GB_SLAB = 128;                 // k of a slab
 constexpr int GB_COLS = 128;                 // columns j of a block
@@ -658,6 +660,14 @@ cudaError_t launch_block(const GroupGemmArgs& a, cudaStream_t stream) {
                             (uint64_t)wait_timeout_ns(), status);
 }
 
+// Up to 8 rows the GEMV, for more the blocks.  Both measured, us of the GEMV / of the blocks:
+//   rows                               1            2            4            6            8
+//   11008 x 4096, groups of 128     7.1 / 10.6  10.2 / 10.6  10.6 / 10.7  12.5 / 10.9  16.1 / 11.0
+//   the same, 64 with zero points   9.6 / 14.5  13.1 / 14.5  13.1 / 14.7  14.7 / 15.1  19.9 / 15.0
+//   8192 x 8192, groups of 128     12.7 / 17.8  13.0 / 17.9  19.3 / 17.9  23.3 / 18.3  23.2 / 18.4
+//   1000 x 1024, 32 with zeros      2.8 / 4.3    2.8 / 4.4    2.8 / 4.4    2.9 / 4.9    2.9 / 4.8
+// With many tiles the blocks are ahead from 4 to 7 rows on, with few never: the bound stands where the small call needs it,
+// and a rule on rows and tiles would take up to 5 us off 5 to 8 rows.
 template <int G, bool ZP>
 cudaError_t launch_rows(const GroupGemmArgs& a, cudaStream_t stream) {
   if (a.M <= 8) return launch_gemv<G, ZP>(a, stream);

@@ -286,7 +286,7 @@ def bq_qk_norm_rope_kv4(q, k, v, codes, params, slots, positions=None, cos=None,
 
 
 def bq_attn_kv4_workspace(batch, q_heads, kv_heads, head_dim, max_q, max_len) -> int:
-    """Bytes of workspace that bq_attn_kv4 needs for these sizes (0: none)."""
+    """Bytes of workspace that bq_attn_kv4 needs for these sizes on the current device (0: none)."""
     return int(_load().workspace(int(batch), int(q_heads), int(kv_heads), int(head_dim), int(max_q), int(max_len)))
 
 
