@@ -1,0 +1,164 @@
+/*
+ * bq_draft.h -- C ABI of the operators of a step that checks drafted tokens
+ * on the 4-bit cache of bq_decode.h: attention of a tree of drafted tokens,
+ * the choice of a token from logits, and the acceptance of a branch.
+ *
+ * The conventions are those of bq.h and bq_decode.h: device pointers owned by
+ * the caller, asynchronous launches on the caller's stream, no allocation,
+ * host validation before any launch, a bq_status.
+ *
+ * The tree.  Sequence b has len = seq_lens[b] tokens in the cache, the last
+ * of them its n drafted ones (its nodes), which are rows cu_q[b] ..
+ * cu_q[b + 1] - 1 of everything that has one row a drafted token; cu_q NULL
+ * means T / B nodes for every sequence.  Row i of `tree` holds `words` 64-bit
+ * words: bit j % 64 of word j / 64 says that node i of its sequence sees node
+ * j of it, so that a node of a tree has its ancestors' bits and its own.
+ * Bits of nodes that a sequence does not have are ignored.  A node without a
+ * bit is padding.
+ */
+#ifndef BQ_DRAFT_H_
+#define BQ_DRAFT_H_
+
+#include "bq_decode.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of logits */
+enum { BQ_LOGITS_F16 = 0, BQ_LOGITS_F32 = 1, BQ_LOGITS_BF16 = 2 };
+
+/*
+ * bq_attn_kv4_tree -- attention of drafted tokens over the 4-bit cache.
+ *
+ *   Node i sees the keys before its sequence's drafted ones (0 .. len - n -
+ *   1) and the drafted keys len - n + j of its bits.  With window > 0 it sees
+ *   of the former only those from len - n + (its number of bits) - window on:
+ *   it stands at the depth that its bits count, and the window is taken to
+ *   reach over the tree.  Query head h reads kv head h / (q_heads / kv_heads).
+ *     out = sum_t softmax_t(scale * q . k[t]) * v[t]
+ *     lse = log sum_t exp(scale * q . k[t])         (natural log, fp32)
+ *   A node without a bit, or one that sees no key, gives out = 0 and lse =
+ *   -inf.
+ *   Scores, the running maximum and sum, and the accumulators are fp32.  With
+ *   many query rows the cache's values are rounded to fp16 (as
+ *   bq_qk_norm_rope_kv4 hands them out, values beyond fp16's range held to
+ *   its largest) and the weights to fp16; with few the weights times the
+ *   values' steps are (as in bq_attn_kv4).
+ *   What the pool holds past a sequence's length, and at drafted places that
+ *   no node of the sequence sees, does not reach the result (NaN included).
+ *   NaN in what a node sees makes its result NaN; NaN in a drafted key or its
+ *   value may also reach nodes of the same sequence that do not see it.
+ *
+ *   q            device fp16, T rows of q_heads * D contiguous elements, leading
+ *                dimension ld_q (a multiple of 8)
+ *   tree         device uint64 (T, words), contiguous
+ *   block_table, seq_lens, cu_q, max_len, out, lse, workspace: as in
+ *                bq_attn_kv4
+ *   max_q        at least every sequence's number of nodes, at most 64 * words
+ *   8-byte alignment is enough for tree.
+ *   Lengths beyond max_len and more than max_q nodes are cut off, a sequence
+ *   whose rows are not in [0, T) is left out, a page outside the pool is read
+ *   as page 0, and bq_device_status reports BQ_ERR_INVALID_ARG.  Rows that are
+ *   cut off, left out or in no sequence are not written.
+ *   T = 0 or B = 0 is an empty call.
+ *   Errors: as bq_attn_kv4; INVALID_ARG also where T is not a multiple of B
+ *   without cu_q, or words < 1, or 64 * words < max_q; UNSUPPORTED where words
+ *   is above 16.
+ */
+size_t bq_attn_kv4_tree_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q,
+                                  int64_t max_len);
+bq_status bq_attn_kv4_tree(const uint16_t* q, int64_t ld_q, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D,
+                           const uint8_t* codes, const uint16_t* params, int64_t num_pages, int64_t page_size,
+                           int64_t group, const int32_t* block_table, int64_t ld_table, const int32_t* seq_lens,
+                           const uint64_t* tree, int64_t words, const int32_t* cu_q, int64_t B, int64_t max_q,
+                           int64_t max_len, float scale, int64_t window, uint16_t* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * bq_sample -- a token for each row of logits, from given random numbers.
+ *
+ *   Row i has logits x[0 .. V - 1], a temperature t and limits k, p, m:
+ *     w[j] = exp((x[j] - max x) / t)
+ *   In the order of falling logits (of equal ones the lower index first) the
+ *   kept tokens are the first k; of these the shortest prefix whose weight is
+ *   p of theirs or more (a token is kept when the weight before it is below p
+ *   times the whole, and the first one always); of these the ones with w[j] >=
+ *   m.  The token is the first kept one, by index, whose running sum of
+ *   kept weights passes u[i] times their sum.
+ *     logprob = log(w[token] / sum of the kept weights)
+ *   t <= 0 (or NaN) takes the largest logit (the lowest index of equal ones),
+ *   and so does a row whose largest logit is +inf; logprob is then 0.
+ *   k <= 0, p >= 1 (or NaN) and m <= 0 (or NaN) keep all; p <= 0 and m > 1
+ *   keep the first one.
+ *   -inf and NaN logits are never taken; a row of nothing else gives token -1
+ *   and logprob -inf.
+ *   Weights are held to 29 bits and 2**-44 of the largest, and summed exactly:
+ *   the choice is that of the formula but where u times the sum, or a limit,
+ *   lies within some 1e-10 of a border.  The same inputs give the same token,
+ *   whatever the other rows are.
+ *
+ *   logits       device, R rows of V contiguous elements of type ltype
+ *                (BQ_LOGITS_*), leading dimension ld >= V, element alignment
+ *   u            device fp32 (R), in [0, 1): values below 0 (or NaN) count as
+ *                0, others as the largest below 1
+ *   temperature, top_p, min_p   device fp32 (R) or NULL (1, keep all, keep all)
+ *   top_k        device int32 (R) or NULL (keep all)
+ *   tokens       device int32 (R);  logprob  device fp32 (R) or NULL
+ *   4-byte alignment is enough for all of these.
+ *   R = 0 is an empty call; V = 0 gives -1.
+ *   Errors: INVALID_ARG (null pointers, negative sizes, ld < V, a bad type),
+ *   ALIGNMENT, UNSUPPORTED (V above 2**19, R above 2**24), CUDA.
+ */
+bq_status bq_sample(const void* logits, int ltype, int64_t R, int64_t V, int64_t ld, const float* u,
+                    const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                    int32_t* tokens, float* logprob, void* stream);
+
+/*
+ * bq_kv4_accept -- the longest branch of each tree that the chosen tokens
+ * confirm, and the move of its cache lines behind the accepted ones.
+ *
+ *   A node's parent is the last node before it among its bits; a node without
+ *   one is a root.  tokens[i] is node i's token, targets[i] the one that was
+ *   chosen from its logits.  A node is confirmed when its own bit is set and
+ *   every node among its bits (up to its own) is a root or has the token that
+ *   was chosen at its parent.  Of the confirmed nodes the one with most bits
+ *   (the first of equal ones) ends the branch; the branch is its bits.
+ *     accepted[b] = nodes of the branch, path[b, k] = its k-th node, -1
+ *     behind the last; next[b] = targets at its end; new_lens[b] = len - n +
+ *     accepted[b]
+ *   In every layer's cache the line of the branch's k-th node moves from place
+ *   len - n + path[b, k] to len - n + k of the sequence.  Nothing else is
+ *   written.  No confirmed node (n = 0, padding alone): accepted 0, next -1.
+ *
+ *   tokens, targets  device int32 (T)
+ *   codes, params    device, `layers` pools as in bq_decode.h one after the
+ *                    other, all with the same block table
+ *   block_table      device int32 (B, ld_table); pages with places from len -
+ *                    n on belong to one sequence alone
+ *   max_q, max_len   at least every sequence's number of nodes and length
+ *   path             device int32 (B, max_q);  accepted, next, new_lens  device
+ *                    int32 (B), none of them seq_lens itself
+ *   8-byte alignment is enough for tree, 4-byte for all int32.
+ *   A sequence whose rows are not in [0, T), with more than max_q nodes, or
+ *   whose length is above max_len or below its number of nodes is left out
+ *   (accepted 0, next -1, its length as it was, no line moved); a line
+ *   from or to a page outside the pool is not moved; bq_device_status reports
+ *   BQ_ERR_INVALID_ARG for both.
+ *   B = 0 is an empty call.
+ *   Errors: INVALID_ARG (null pointers, negative sizes, T not a multiple of B
+ *   without cu_q, words < 1, 64 * words < max_q, max_len above ld_table *
+ *   page_size), ALIGNMENT, UNSUPPORTED (the pool's shape, words above 16, more
+ *   than 65536 layers, 2**24 rows or sequences), CUDA.
+ */
+bq_status bq_kv4_accept(const int32_t* tokens, const int32_t* targets, const uint64_t* tree, int64_t words, int64_t T,
+                        const int32_t* cu_q, int64_t B, int64_t max_q, const int32_t* block_table, int64_t ld_table,
+                        const int32_t* seq_lens, int64_t max_len, uint8_t* codes, uint16_t* params, int64_t layers,
+                        int64_t num_pages, int64_t kv_heads, int64_t page_size, int64_t D, int64_t group,
+                        int32_t* path, int32_t* accepted, int32_t* next, int32_t* new_lens, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* BQ_DRAFT_H_ */

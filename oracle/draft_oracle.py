@@ -1,0 +1,143 @@
+"""CPU oracle of the operators on drafted tokens (test infrastructure only).
+
+Plain numpy in float64, written from the formulas of include/bq_draft.h and
+sharing no code with the CUDA path.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+
+from oracle.decode_oracle import cache_values
+
+
+def bits_of(parents):
+    """Rows of truth values (n, n): each node's ancestors and itself (parent -1: a root; -2: padding)."""
+    n = len(parents)
+    m = np.zeros((n, n), bool)
+    for i, p in enumerate(parents):
+        if p == -2:
+            continue
+        if p >= 0:
+            m[i] = m[p]
+        m[i, i] = True
+    return m
+
+
+def words_of(masks, words):
+    """Truth values (n, n) of each sequence -> int64 (T, words)."""
+    rows = []
+    for m in masks:
+        for r in m:
+            v = np.zeros(words * 64, np.uint64)
+            v[: len(r)] = r
+            rows.append((v.reshape(words, 64) << np.arange(64, dtype=np.uint64)).sum(1, dtype=np.uint64))
+    return np.array(rows, np.uint64).reshape(-1, words).view(np.int64)
+
+
+def tree_attention(q, codes, params, table, lens, cu, masks, scale, window=0, rounded=False):
+    """(out, lse, bound of out, bound of lse), float64.
+
+    The bounds without `rounded` are those of bq_attn_kv4: fp32 scores (D + 16 additions), weights times the values'
+    steps rounded to fp16 (2**-11 of each weighted term |v| + 2 |low|), the result rounded to fp16 (2**-11).  With
+    `rounded` the keys and values are rounded to fp16 (2**-11 of each, 2**-25 of the smallest; a score moves by that of
+    sum |q| |k|, a weight by twice what a score does) and so are the weights, of which the smallest by 2**-25 of the
+    largest."""
+    T, heads, D = q.shape
+    rep = heads // codes.shape[2]
+    out, lse = np.zeros((T, heads, D)), np.full((T, heads), -np.inf)
+    tol, tol_lse = np.full((T, heads, D), 2.0 ** -25), np.zeros((T, heads))
+    for b, length in enumerate(lens):
+        first, n, length = int(cu[b]), int(cu[b + 1] - cu[b]), int(length)
+        if length == 0 or n == 0:
+            continue
+        x, low = cache_values(codes, params, table[b], length)
+        for i in range(n):
+            depth = int(masks[b][i].sum())
+            if depth == 0:
+                continue
+            base = length - n
+            seen = np.zeros(length, bool)
+            if base > 0:
+                seen[max(0, base + depth - window) if window else 0:base] = True
+            for j in np.nonzero(masks[b][i])[0]:
+                if base + j >= 0:
+                    seen[base + j] = True
+            if not seen.any():
+                continue
+            for h in range(heads):
+                k, v, lw = x[0, h // rep][seen], x[1, h // rep][seen], low[h // rep][seen]
+                qq = q[first + i, h].astype(np.float64)
+                s = k @ qq * scale
+                size = (np.abs(k) @ np.abs(qq)).max()
+                ds = abs(scale) * (D + 16) * 2.0 ** -23 * size * 2 + 2.0 ** -21 * np.abs(s).max()
+                if rounded:
+                    ds += abs(scale) * (2.0 ** -11 * size + 2.0 ** -25 * np.abs(qq).sum())
+                e = np.exp(s - s.max())
+                w = e / e.sum()
+                out[first + i, h] = w @ v
+                lse[first + i, h] = s.max() + np.log(e.sum())
+                term = w @ (np.abs(v) + 2 * lw)
+                t = 2.0 ** -11 * np.abs(out[first + i, h]) + (2.0 ** -11 + 2 * ds + 2.0 ** -20) * term
+                if rounded:
+                    t += 2.0 ** -11 * term + 2.0 ** -25 + 2.0 ** -25 * np.abs(v).sum(0) / e.sum()
+                tol[first + i, h] += t
+                tol_lse[first + i, h] = ds + 2.0 ** -20 + 2.0 ** -22 * abs(lse[first + i, h])
+    return out, lse, tol, tol_lse
+
+
+def sample(x, u, temperature=1.0, k=0, p=1.0, m=0.0):
+    """(token, logprob, kept tokens) of one row."""
+    x = np.where(np.isnan(x), -np.inf, x).astype(np.float64)
+    top = x.max() if len(x) else -np.inf
+    if top == -np.inf:
+        return -1, -np.inf, 0
+    if not temperature > 0 or top == np.inf:
+        return int(np.argmax(x)), 0.0, 1
+    order = np.argsort(-x, kind="stable")
+    order = order[x[order] > -np.inf]
+    w = np.exp((x - top) / float(temperature))
+    if k > 0:
+        order = order[:k]
+    if p < 1:
+        run = np.cumsum(w[order])
+        keep = np.concatenate([[0.0], run[:-1]]) < float(p) * run[-1]
+        order = order[: max(1, int(keep.sum()))]
+    if m > 0:
+        order = order[: max(1, int((w[order] >= float(m)).sum()))]
+    chosen = np.sort(order)
+    run = np.cumsum(w[chosen])
+    u = min(max(float(u), 0.0), 1 - 2.0 ** -24) if u == u else 0.0
+    at = min(int(np.searchsorted(run, u * run[-1], side="right")), len(chosen) - 1)
+    token = int(chosen[at])
+    return token, float((x[token] - top) / float(temperature) - np.log(run[-1])), len(chosen)
+
+
+def accept(tokens, targets, masks, cu, lens, table, codes, params):
+    """(path lists, accepted, next, lens) and codes and params (layers first) changed in place: a walk over all nodes."""
+    paths, nxt, new = [], [], []
+    page = codes.shape[4]
+    for b, length in enumerate(lens):
+        first, n = int(cu[b]), int(cu[b + 1] - cu[b])
+        best = []
+        for i in range(n):
+            chain = [j for j in range(i + 1) if masks[b][i][j]]
+            if not masks[b][i][i]:
+                continue
+            good = True
+            for j in chain:
+                up = [e for e in range(j) if masks[b][j][e]]
+                if up and tokens[first + j] != targets[first + up[-1]]:
+                    good = False
+            if good and len(chain) > len(best):
+                best = chain
+        base = int(length) - n
+        old_c, old_p = codes.copy(), params.copy()
+        for k, j in enumerate(best):
+            (np_, no), (op, oo) = divmod(base + k, page), divmod(base + j, page)
+            codes[:, table[b][np_], :, :, no] = old_c[:, table[b][op], :, :, oo]
+            params[:, table[b][np_], :, :, no] = old_p[:, table[b][op], :, :, oo]
+        paths.append(best)
+        nxt.append(int(targets[first + best[-1]]) if best else -1)
+        new.append(base + len(best))
+    return paths, [len(p) for p in paths], nxt, new

@@ -15,11 +15,13 @@ import os
 import re
 
 from . import decode as _decode
+from . import draft as _draft
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libbq.so")
 HEADER = os.path.join(os.path.dirname(PKG_DIR), "include", "bq.h")
 DECODE_HEADER = os.path.join(os.path.dirname(PKG_DIR), "include", "bq_decode.h")
+DRAFT_HEADER = os.path.join(os.path.dirname(PKG_DIR), "include", "bq_draft.h")
 
 BQ_OK, BQ_ERR_INVALID_ARG, BQ_ERR_UNSUPPORTED, BQ_ERR_ALIGNMENT, BQ_ERR_CUDA, BQ_ERR_TIMEOUT = range(6)
 BQ_F16, BQ_F32 = 0, 1
@@ -64,6 +66,7 @@ _SIGNATURES = {
     "bq_device_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int), ctypes.c_int]),
     "bq_set_wait_timeout_ns": (_c_i64, [_c_i64]),
     **_decode.SIGNATURES,
+    **_draft.SIGNATURES,
 }
 
 _lib = None
@@ -455,3 +458,9 @@ bq_kv4_pool = _decode.bq_kv4_pool
 bq_qk_norm_rope_kv4 = _decode.bq_qk_norm_rope_kv4
 bq_attn_kv4_workspace = _decode.bq_attn_kv4_workspace
 bq_attn_kv4 = _decode.bq_attn_kv4
+
+# The operators on drafted tokens (include/bq_draft.h)
+bq_attn_kv4_tree_workspace = _draft.bq_attn_kv4_tree_workspace
+bq_attn_kv4_tree = _draft.bq_attn_kv4_tree
+bq_sample = _draft.bq_sample
+bq_kv4_accept = _draft.bq_kv4_accept

@@ -1,0 +1,238 @@
+"""Operators on drafted tokens of libbq.so (the C ABI declared in include/bq_draft.h).
+
+A step that checks a tree of drafted tokens on the 4-bit cache writes their keys and values (``bq_qk_norm_rope_kv4``),
+attends with ``bq_attn_kv4_tree``, chooses a token at every node with ``bq_sample`` and keeps the longest branch that the
+choices confirm with ``bq_kv4_accept``.  The calls are bound like those of decode.py: argument checks, device pointers
+and the current CUDA stream, ``BqError`` on a non-OK status; with ``stream`` a call allocates and runs on that stream.
+
+A tree is an int64 tensor (T, words), one row a drafted token: bit j % 64 of word j // 64 says that the token sees token j
+of its sequence, its ancestors and itself.  A row of zeros is padding.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+from . import decode as _decode
+from .decode import _apart, _is_whole, _need, _need_whole, _on, _pool, _row_stride, _share
+
+_c_i64, _vp, _int, _f32, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+
+SIGNATURES = {
+    "bq_attn_kv4_tree_workspace": (_sz, [_c_i64] * 6),
+    "bq_attn_kv4_tree": (_int, [_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_i64, _c_i64, _c_i64, _vp,
+                                _c_i64, _vp, _vp, _c_i64, _vp, _c_i64, _c_i64, _c_i64, _f32, _c_i64, _vp, _vp, _vp, _sz,
+                                _vp]),
+    "bq_sample": (_int, [_vp, _int, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "bq_kv4_accept": (_int, [_vp, _vp, _vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _vp,
+                             _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp]),
+}
+
+
+class _Bound:
+    """What every call needs, looked up once."""
+
+    def __init__(self):
+        import torch
+
+        import quantized_mixed_precision_gb300 as bq
+        lib = bq.lib()
+        self.bq, self.torch, self.lib = bq, torch, lib
+        self.f16, self.f32, self.u8 = torch.float16, torch.float32, torch.uint8
+        self.i32, self.i64 = torch.int32, torch.int64
+        self.logits = {torch.float16: 0, torch.float32: 1, torch.bfloat16: 2}
+        self.empty = torch.empty
+        self.raw_stream, self.device_now = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+        self.attn, self.workspace = lib.bq_attn_kv4_tree, lib.bq_attn_kv4_tree_workspace
+        self.sample, self.accept = lib.bq_sample, lib.bq_kv4_accept
+
+
+_bound = None
+
+
+def _load():
+    global _bound
+    if _bound is None:
+        _bound = _Bound()
+    return _bound
+
+
+def _table(b, block_table, dev, stream):
+    """(table, sequences, columns, leading dimension); a table whose rows overlap is copied, as bq_attn_kv4 does."""
+    _need(block_table, b.i32, "block_table", 2, dev)
+    B, width = block_table.shape
+    ld = width
+    if not block_table.is_contiguous():
+        if width > 1 and block_table.stride(1) != 1:
+            raise ValueError("block_table must have unit column stride")
+        if B > 1 and block_table.stride(0) < width:
+            with _on(b, dev, stream):
+                block_table = block_table.contiguous()
+        elif B > 1:
+            ld = block_table.stride(0)
+    return block_table, B, width, ld
+
+
+def _nodes(b, T, B, tree, cu_q, max_q, dev):
+    """Words of the tree's rows and the bound on a sequence's nodes."""
+    _need_whole(tree, b.i64, "tree", (T, None), dev)
+    words = tree.shape[1]
+    if cu_q is not None:
+        _need_whole(cu_q, b.i32, "cu_q", (B + 1,), dev)
+    elif B and T % B:
+        raise ValueError("without cu_q, every sequence has the same number of drafted tokens")
+    each = T // B if B and cu_q is None else T
+    if max_q is None:
+        max_q = each if cu_q is None else min(each, 64 * words)
+    elif cu_q is None and max_q < each:
+        raise ValueError("max_q is less than every sequence's number of drafted tokens")
+    return words, max_q
+
+
+def bq_attn_kv4_tree_workspace(batch, q_heads, kv_heads, head_dim, max_q, max_len) -> int:
+    """Bytes of workspace that bq_attn_kv4_tree needs for these sizes on the current device (0: none)."""
+    return int(_load().workspace(int(batch), int(q_heads), int(kv_heads), int(head_dim), int(max_q), int(max_len)))
+
+
+def bq_attn_kv4_tree(q, codes, params, block_table, seq_lens, tree, cu_q=None, max_q=None, max_len=None, scale=None,
+                     window=0, lse=False, out=None, workspace=None, stream=None):
+    """Attention of drafted tokens q (T, q_heads, D) over the 4-bit cache -> (out fp16 (T, q_heads, D), lse fp32
+    (T, q_heads) or None).  A sequence's drafted tokens are the last of its seq_lens[b] tokens in the cache, and rows
+    cu_q[b] .. cu_q[b + 1] - 1 of q and ``tree`` (None: the same number for every sequence); each sees what was in the
+    cache before them and the drafted ones of its bits.  With ``window`` it sees that many keys at most, those of its
+    bits always.  Other arguments as in bq_attn_kv4; ``max_q`` bounds a sequence's drafted tokens (None: all of q's with
+    cu_q, up to what the tree's words hold)."""
+    b = _bound or _load()
+    f16 = b.f16
+    _need(q, f16, "q", 3)
+    dev = q.get_device()
+    T, q_heads, D = q.shape
+    pages, heads, page, group = _pool(b, codes, params, D, dev)
+    block_table, B, width, ld_table = _table(b, block_table, dev, stream)
+    if not _is_whole(seq_lens, b.i32, (B,), dev):
+        _need_whole(seq_lens, b.i32, "seq_lens", (B,), dev)
+    words, max_q = _nodes(b, T, B, tree, cu_q, max_q, dev)
+    if max_len is None:
+        max_len = width * page
+    elif max_len > width * page:
+        raise ValueError("max_len is more than block_table holds")
+    made = out is None
+    if not made and not _is_whole(out, f16, (T, q_heads, D), dev):
+        _need_whole(out, f16, "out", (T, q_heads, D), dev)
+    size = 0
+    if workspace is not None:
+        _need_whole(workspace, b.u8, "workspace", (None,), dev)
+        size = workspace.numel()
+    ld_q = _row_stride(q, "q")
+    with _on(b, dev, stream):
+        if made:
+            out = b.empty((T, q_heads, D), dtype=f16, device=q.device)
+        logs = b.empty((T, q_heads), dtype=b.f32, device=q.device) if lse else None
+        if workspace is None:
+            size = b.workspace(B, q_heads, heads, D, max_q, max_len)
+            if size:
+                workspace = b.empty((size,), dtype=b.u8, device=q.device)
+        st = b.attn(q.data_ptr(), ld_q, T, q_heads, heads, D, codes.data_ptr(), params.data_ptr(), pages, page, group,
+                    block_table.data_ptr(), ld_table, seq_lens.data_ptr(), tree.data_ptr(), words,
+                    None if cu_q is None else cu_q.data_ptr(), B, max_q, max_len, D ** -0.5 if scale is None else scale,
+                    window, out.data_ptr(), logs.data_ptr() if lse else None,
+                    None if workspace is None else workspace.data_ptr(), size,
+                    b.raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        b.bq._check(st, "bq_attn_kv4_tree")
+    if stream is not None:
+        _share(q.device, out if made else None, logs)
+    return out, logs
+
+
+def bq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, logprob=False, out=None, stream=None):
+    """A token for each row of logits (R, V), fp16, bf16 or fp32, from u (R) fp32 in [0, 1) -> (tokens int32 (R,),
+    logprob fp32 (R,) or None).  temperature, top_p and min_p are fp32 (R), top_k is int32 (R); None leaves a filter
+    out (temperature 1).  Of equal logits the lower index counts as the larger.  A temperature of 0 takes the largest
+    logit; ``logprob`` is the logarithm of the token's share of what the filters kept.  Rows may be apart by more than
+    V."""
+    b = _bound or _load()
+    torch = b.torch
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in b.logits:
+        raise TypeError("logits must be a CUDA tensor of fp16, bf16 or fp32")
+    _need(logits, logits.dtype, "logits", 2)
+    dev = logits.get_device()
+    R, V = logits.shape
+    ld = V
+    if not logits.is_contiguous():
+        if V > 1 and logits.stride(1) != 1:
+            raise ValueError("logits must have unit column stride")
+        ld = _apart(R, logits.stride(0), V, "logits")
+    if not _is_whole(u, b.f32, (R,), dev):
+        _need_whole(u, b.f32, "u", (R,), dev)
+    for t, dtype, name in ((temperature, b.f32, "temperature"), (top_k, b.i32, "top_k"), (top_p, b.f32, "top_p"),
+                           (min_p, b.f32, "min_p")):
+        if t is not None and not _is_whole(t, dtype, (R,), dev):
+            _need_whole(t, dtype, name, (R,), dev)
+    made = out is None
+    if not made and not _is_whole(out, b.i32, (R,), dev):
+        _need_whole(out, b.i32, "out", (R,), dev)
+    with _on(b, dev, stream):
+        if made:
+            out = b.empty((R,), dtype=b.i32, device=logits.device)
+        logs = b.empty((R,), dtype=b.f32, device=logits.device) if logprob else None
+        st = b.sample(logits.data_ptr(), b.logits[logits.dtype], R, V, ld, u.data_ptr(),
+                      None if temperature is None else temperature.data_ptr(),
+                      None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
+                      None if min_p is None else min_p.data_ptr(), out.data_ptr(), logs.data_ptr() if logprob else None,
+                      b.raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        b.bq._check(st, "bq_sample")
+    if stream is not None:
+        _share(logits.device, out if made else None, logs)
+    return out, logs
+
+
+def bq_kv4_accept(tokens, targets, tree, codes, params, block_table, seq_lens, cu_q=None, max_q=None, stream=None):
+    """The longest branch of each sequence's tree that the chosen tokens confirm, whose cache lines move up behind the
+    accepted ones -> (path int32 (B, max_q), accepted int32 (B,), next int32 (B,), lens int32 (B,)).  tokens are the
+    drafted tokens int32 (T,), targets what was chosen from their logits; a node is confirmed when its token is the one
+    chosen at its parent, and its ancestors are (a root always is).  path holds the branch's nodes, -1 behind the last;
+    next is what was chosen at its end (-1 without one), lens the sequences' lengths then.  codes and params are a pool
+    (5 and 6 dims) or those of all layers (6 and 7 dims, layers first); the drafted places' pages belong to one
+    sequence each."""
+    b = _bound or _load()
+    i32 = b.i32
+    _need(tokens, i32, "tokens", 1)
+    dev = tokens.get_device()
+    T = tokens.shape[0]
+    if not isinstance(codes, b.torch.Tensor) or codes.dim() not in (5, 6):
+        raise ValueError("codes must have 5 dims, or 6 with the layers first")
+    layers = codes.shape[0] if codes.dim() == 6 else 1
+    if codes.dim() == 6:
+        _need(codes, b.u8, "codes", 6, dev)
+        _need(params, b.f16, "params", 7, dev)
+        if params.shape[0] != layers or not codes.is_contiguous() or not params.is_contiguous():
+            raise ValueError("codes and params must be contiguous and of the same layers")
+        one = (codes[0], params[0]) if layers else (codes.flatten(0, 1), params.flatten(0, 1))
+    else:
+        one = codes, params
+    D = 2 * codes.shape[-1]
+    pages, heads, page, group = _pool(b, *one, D, dev)
+    if not _is_whole(tokens, i32, (T,), dev):
+        _need_whole(tokens, i32, "tokens", (T,), dev)
+    if not _is_whole(targets, i32, (T,), dev):
+        _need_whole(targets, i32, "targets", (T,), dev)
+    block_table, B, width, ld_table = _table(b, block_table, dev, stream)
+    if not _is_whole(seq_lens, i32, (B,), dev):
+        _need_whole(seq_lens, i32, "seq_lens", (B,), dev)
+    words, max_q = _nodes(b, T, B, tree, cu_q, max_q, dev)
+    with _on(b, dev, stream):
+        path = b.empty((B, max_q), dtype=i32, device=tokens.device)
+        rest = b.empty((3, B), dtype=i32, device=tokens.device)
+        accepted, last, lens = rest[0], rest[1], rest[2]
+        st = b.accept(tokens.data_ptr(), targets.data_ptr(), tree.data_ptr(), words, T,
+                      None if cu_q is None else cu_q.data_ptr(), B, max_q, block_table.data_ptr(), ld_table,
+                      seq_lens.data_ptr(), width * page, codes.data_ptr(), params.data_ptr(), layers, pages, heads, page, D,
+                      group, path.data_ptr(), accepted.data_ptr(), last.data_ptr(), lens.data_ptr(),
+                      b.raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        b.bq._check(st, "bq_kv4_accept")
+    if stream is not None:
+        _share(tokens.device, path, rest)
+    return path, accepted, last, lens
