@@ -36,6 +36,7 @@ constexpr int FRAC = 44;                     // bits of a weight below the large
 constexpr float Y_MOST = FRAC + 2.0f;        // from here on a weight is 0
 constexpr int BINS = 2048, EACH = BINS / THREADS;
 constexpr int LIST = 2048;                   // gathered tokens
+constexpr int QUEUE = 32 * 9;                // of a warp: a step of 8 elements a lane, and less than 32 before it
 constexpr int MOST_BLOCKS = 8;
 
 // Keys of fp32 values: unsigned integers of the same order.
@@ -53,15 +54,26 @@ struct Cut {
   int last;
 };
 __device__ __forceinline__ bool kept(const Cut& c, float x, int index) {
-  return x > c.x || (x == c.x && index <= c.last);
+  return x >= c.x && (x > c.x || index <= c.last);
 }
+constexpr uint32_t KEY_LOWEST = 0x007fffffu;   // of -inf
 constexpr int NONE = -16;                    // below every index, also those before a row that starts off a boundary
 __device__ __forceinline__ Cut strictest(const Cut& a, const Cut& b) {
   if (a.x != b.x) return a.x > b.x ? a : b;
   return a.last < b.last ? a : b;
 }
 
-// Entries of 2**-(j / 32): 60 bits after the point, and as fp32.
+// 2**-(j / 32), 60 bits after the point
+__constant__ uint64_t ROOTS[32] = {
+    0x1000000000000000ull, 0xfa83b2db722a034ull, 0xf5257d152486cc3ull, 0xefe4b99bdcdaf5dull,
+    0xeac0c6e7dd24393ull, 0xe5b906e77c8348bull, 0xe0ccdeec2a94e11ull, 0xdbfbb797daf2375ull,
+    0xd744fccad69d6afull, 0xd2a81d91f12ae46ull, 0xce248c151f8480eull, 0xc9b9bd866e2f27aull,
+    0xc5672a115506daeull, 0xc12c4cca6670945ull, 0xbd08a39f580c36cull, 0xb8fbaf4762fb9efull,
+    0xb504f333f9de648ull, 0xb123f581d2ac259ull, 0xad583eea42a14acull, 0xa9a15ab4ea7c0f0ull,
+    0xa5fed6a9b15138full, 0xa27043030c49682ull, 0x9ef5326091a111bull, 0x9b8d39b9d54e554ull,
+    0x9837f0518db8a97ull, 0x94f4efa8fef7096ull, 0x91c3d373ab11c33ull, 0x8ea4398b45cd53cull,
+    0x8b95c1e3ea8bd6eull, 0x88980e8092da852ull, 0x85aac367cc487b1ull, 0x82cd8698ac2ba1dull};
+// The same in shared memory, and as fp32.
 struct Table {
   uint64_t fixed[32];
   float value[32];
@@ -101,10 +113,10 @@ __device__ __forceinline__ uint64_t weight(float x, const Scale& s, const Table&
 }
 
 // Shared memory of a block
-struct Shared {
+struct __align__(16) Shared {
   Table table;
   uint64_t part[2][WARPS];         // a warp's share of a sum, two in turn
-  uint64_t own[WARPS];             // the same within the block
+  uint64_t own[2][WARPS];          // the same within the block
   uint32_t hist[BINS];
   float list_x[LIST];              // gathered tokens: the block's own, then the row's behind them
   int32_t list_i[LIST];
@@ -116,7 +128,12 @@ struct Shared {
     int32_t all_i[LIST];
     uint32_t mass_hi[BINS];
   };
-  int n;                           // of the block's own
+  uint64_t all_w[LIST];
+  uint16_t tie[LIST];              // entries of the list
+  float queue[WARPS][QUEUE];       // tokens of a warp whose weights are to be summed
+  int n[2];                        // gathered by the block, two lists in turn
+  float c_hi, c_lo;
+  double reach;                    // temperature times ln of min_p
   int found;
   uint64_t reached;
   uint32_t scan[WARPS];
@@ -179,11 +196,15 @@ struct Row {
     first = min(warp * per, steps);
     last = min(first + per, steps);
   }
-  // Elements of step s: index of the first, values (-inf where there is none)
-  __device__ __forceinline__ int load(int s, float (&v)[E]) const {
+  // The 16 bytes of step s, where they are all of the row
+  __device__ __forceinline__ bool whole(int s) const { return s * E >= shift && s * E - shift + E <= V; }
+  __device__ __forceinline__ uint4 fetch(int s) const {
+    return s < last && whole(s) ? __ldg(base + s) : make_uint4(0, 0, 0, 0);
+  }
+  // Elements of step s, which has been fetched: index of the first, values (-inf where there is none)
+  __device__ __forceinline__ int take(int s, const uint4& w, float (&v)[E]) const {
     const int i = s * E - shift;
-    if (i >= 0 && i + E <= V) {
-      const uint4 w = __ldg(base + s);
+    if (whole(s)) {
       const T* t = reinterpret_cast<const T*>(&w);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = to_float(t[e]);
@@ -193,14 +214,54 @@ struct Row {
     }
     return i;
   }
+  // f(step, its 16 bytes) for this lane's steps: two steps are fetched ahead, for the latency's sake
+  template <class F>
+  __device__ __forceinline__ void steps(F f) const {
+    uint4 w0 = fetch(first + lane), w1 = fetch(first + lane + 32);
+    for (int s = first + lane; s < last; s += 32) {
+      const uint4 w2 = fetch(s + 64);
+      f(s, w0);
+      w0 = w1;
+      w1 = w2;
+    }
+  }
+  // The largest value of this thread's elements
+  __device__ __forceinline__ float largest() const {
+    float top = -INFINITY;
+    if constexpr (E == 8) {
+      // two at a time: NaN gives way to the other value
+      uint32_t t = std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+      steps([&](int s, const uint4& w) {
+        if (whole(s)) {
+          t = max2(max2(t, w.x), max2(max2(w.y, w.z), w.w));
+        } else {
+          float v[E];
+          take(s, w, v);
+#pragma unroll
+          for (int e = 0; e < E; ++e) top = fmaxf(top, v[e]);
+        }
+      });
+      const T* h = reinterpret_cast<const T*>(&t);
+      return fmaxf(top, fmaxf(to_float(h[0]), to_float(h[1])));
+    } else {
+      each([&](float v, int) { top = fmaxf(top, v); });
+      return top;
+    }
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (std::is_same<T, __half>::value) asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
   template <class F>
   __device__ __forceinline__ void each(F f) const {
-    for (int s = first + lane; s < last; s += 32) {
+    steps([&](int s, const uint4& w) {
       float v[E];
-      const int i = load(s, v);
+      const int i = take(s, w, v);
 #pragma unroll
       for (int e = 0; e < E; ++e) f(v[e], i + e);
-    }
+    });
   }
 };
 
@@ -212,10 +273,12 @@ struct Sampler {
   Shared& sh;
   const Row<T>& row;
   const int tid, warp, lane, blocks, rank;
-  int phase = 0;
+  int phase = 0, own_phase = 0, turn = 0;
   Scale s;
-  float bins;               // steps of y
+  float bins, slope;        // steps of y for one; what a step takes of 4096
   Cut cut;                  // what is kept so far
+  Cut known{INFINITY, NONE};
+  uint64_t share = 0;       // weight of this warp's tokens that `known` keeps
 
   __device__ Sampler(Shared& sh_, const Row<T>& row_, int blocks_, int rank_)
       : sh(sh_), row(row_), tid(threadIdx.x), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), blocks(blocks_), rank(rank_) {}
@@ -231,6 +294,12 @@ struct Sampler {
   __device__ __forceinline__ int bin_of(float y) const {
     constexpr float WHOLE = 8388608.0f;
     return min(__float_as_int(fmaf(y, bins, WHOLE)) - __float_as_int(WHOLE), BINS - 1);
+  }
+  // The weight of a token in bin b as a part of 4096 of the bin's largest, 2**-((b - 1/2) / bins): a bin is at most 1.6 %
+  // wide, and a straight line is good to 2**-13 over it.  (2**19 of them fit 32 bits.)
+  __device__ __forceinline__ uint32_t part_of(float y, int b) const {
+    const float f = __fadd_rn(fmaf(y, bins, -(float)b), 0.5f);
+    return (uint32_t)__float2int_rn(fmaf(f, slope, 4096.0f));
   }
 
   // Every warp's share of a sum, exchanged: f(share of warp i of the row) for this lane's i.  One barrier; the next
@@ -250,13 +319,66 @@ struct Sampler {
     exchange(warp_sum(v), [&](int, uint64_t w) { t += w; });
     return warp_sum(t);
   }
-  // The sum over the block alone, for numbers that every block has.
-  __device__ uint64_t block_sum(uint64_t v) {
-    v = warp_sum(v);
+  // The weights of this warp's tokens that `in` names, as each lane's share.  A token's weight is some 30 instructions:
+  // where few are named, a lane with one would have the others wait, so that they wait in a queue until every lane has
+  // one (FEW).
+  template <bool FEW, class F>
+  __device__ __forceinline__ uint64_t weigh(F in) {
+    constexpr int E = Row<T>::E;
+    uint64_t sum = 0;
+    if constexpr (!FEW) {
+      row.each([&](float x, int i) {
+        if (in(x, i)) sum += w_of(x);
+      });
+    } else {
+      int n = 0;
+      float* const q = sh.queue[warp];
+      uint4 w0 = row.fetch(row.first + lane), w1 = row.fetch(row.first + lane + 32);
+      for (int s0 = row.first; s0 < row.last; s0 += 32) {
+        const uint4 w2 = row.fetch(s0 + lane + 64);
+        float v[E];
+        int i = 0;
+        uint32_t named = 0;
+        if (s0 + lane < row.last) {
+          i = row.take(s0 + lane, w0, v);
+#pragma unroll
+          for (int e = 0; e < E; ++e) named |= in(v[e], i + e) ? 1u << e : 0;
+        }
+        // places by lane: an inclusive sum of the lanes' numbers
+        const int mine = __popc(named);
+        int at = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += up;
+        }
+        const int all = __shfl_sync(0xffffffffu, at, 31);
+        at += n - mine;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (named >> e & 1) q[at++] = v[e];
+        n += all;
+        __syncwarp();
+        while (n >= 32) {
+          n -= 32;
+          sum += w_of(q[n + lane]);
+        }
+        __syncwarp();
+        w0 = w1;
+        w1 = w2;
+      }
+      if (lane < n) sum += w_of(q[lane]);
+      __syncwarp();
+    }
+    return sum;
+  }
+  // A round of exchanges within the block: every warp's value, lane i has warp i's.  One barrier.
+  __device__ __forceinline__ uint64_t within(uint64_t v) {
+    if (lane == 0) sh.own[own_phase][warp] = v;
     __syncthreads();
-    if (lane == 0) sh.own[warp] = v;
-    __syncthreads();
-    return warp_sum(lane < WARPS ? sh.own[lane] : 0);
+    const uint64_t r = sh.own[own_phase][lane % WARPS];
+    own_phase ^= 1;
+    return r;
   }
 
   // The index of the m-th (from 1) token with logit x, or V
@@ -275,7 +397,7 @@ struct Sampler {
         int i = 0;
         uint32_t c = 0;
         if (s0 + lane < row.last) {
-          i = row.load(s0 + lane, v);
+          i = row.take(s0 + lane, row.fetch(s0 + lane), v);
 #pragma unroll
           for (int e = 0; e < Row<T>::E; ++e) c += v[e] == x;
         }
@@ -305,22 +427,49 @@ struct Sampler {
     return __reduce_min_sync(0xffffffffu, at);
   }
 
+  // This thread's four counts, summed over the cluster
+  __device__ __forceinline__ uint4 counts_of(const uint32_t* hist) const {
+    uint4 n = *reinterpret_cast<const uint4*>(hist + 4 * tid);
+    if (blocks == 1) return n;
+    uint4 v[MOST_BLOCKS - 1];                // (all loads first: one takes about a microsecond)
+#pragma unroll
+    for (int b = 1; b < MOST_BLOCKS; ++b) {
+      v[b - 1] = make_uint4(0, 0, 0, 0);
+      if (b < blocks)
+        asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[b - 1].x), "=r"(v[b - 1].y), "=r"(v[b - 1].z), "=r"(v[b - 1].w)
+                     : "r"(remote(hist + 4 * tid, (rank + b) % blocks)));
+    }
+#pragma unroll
+    for (int b = 0; b < MOST_BLOCKS - 1; ++b) {
+      n.x += v[b].x;
+      n.y += v[b].y;
+      n.z += v[b].z;
+      n.w += v[b].w;
+    }
+    return n;
+  }
+
   // The first bin whose tokens, with those before it, may reach `need`, and the first with which they surely do (the last
-  // bin where none does), by the cluster's counts; returns the tokens from the one to the other.  A token of bin b is
-  // worth low(b) to high(b).
+  // bin where none does), by the cluster's counts; returns the counts from the one to the other, and those before them.
+  // A count of bin b is worth low(b) to high(b).
   template <class L, class H>
-  __device__ uint32_t find(float need, L low, H high, int& b0, int& b1) {
-    sync();
+  __device__ uint32_t find(float need, L low, H high, int& b0, int& b1, uint32_t& before) {
     uint32_t n[EACH], count = 0;
-    float lo = 0.0f, hi = 0.0f;
+    float lo = 0.0f, hi = 0.0f, vl[EACH], vh[EACH];
+    static_assert(EACH == 4, "one 16-byte load of counts");
+    const uint4 c = counts_of(sh.hist);
+    n[0] = c.x;
+    n[1] = c.y;
+    n[2] = c.z;
+    n[3] = c.w;
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
-      const uint32_t* p = &sh.hist[tid * EACH + i];
-      n[i] = 0;
-      for (int b = 0; b < blocks; ++b) n[i] += blocks == 1 ? *p : ld_cluster_u32(remote(p, b));
       count += n[i];
-      lo += (float)n[i] * low(tid * EACH + i);
-      hi += (float)n[i] * high(tid * EACH + i);
+      vl[i] = (float)n[i] * low(tid * EACH + i);
+      vh[i] = (float)n[i] * high(tid * EACH + i);
+      lo += vl[i];
+      hi += vh[i];
     }
     if (tid == 0) sh.edge[0] = sh.edge[1] = BINS - 1;
     uint32_t ic = count;
@@ -343,20 +492,34 @@ struct Sampler {
     __syncthreads();
     uint32_t bc = ic - count;
     float bl = il - lo, bh = ih - hi;
-    for (int w = 0; w < warp; ++w) {
-      bc += sh.scan[w];
-      bl += sh.scan_lo[w];
-      bh += sh.scan_hi[w];
-    }
-    // (sums of 2048 fp32 terms are off by less than 2**-12 of themselves)
-    constexpr float LESS = 1.0f - 1.0f / 4096, MORE = 1.0f + 1.0f / 4096;
-    float l = bl, h = bh;
 #pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-      l += (float)n[i] * low(tid * EACH + i);
-      h += (float)n[i] * high(tid * EACH + i);
-      if (n[i] && h * MORE >= need) atomicMin(&sh.edge[0], tid * EACH + i);
-      if (n[i] && l * LESS >= need) atomicMin(&sh.edge[1], tid * EACH + i);
+    for (int w = 0; w < WARPS; ++w)
+      if (w < warp) {
+        bc += sh.scan[w];
+        bl += sh.scan_lo[w];
+        bh += sh.scan_hi[w];
+      }
+    // (a sum of 4 terms, 5 steps of a scan and 16 terms in fp32 is off by less than 2**-18 of itself)
+    constexpr float LESS = 1.0f - 1.0f / 262144, MORE = 1.0f + 1.0f / 262144;
+    float l = bl, h = bh;
+    int e0 = BINS - 1, e1 = BINS - 1;
+#pragma unroll
+    for (int i = EACH - 1; i >= 0; --i) {      // (from behind, so that the first one stays)
+      l = bl;
+      h = bh;
+#pragma unroll
+      for (int j = 0; j <= i; ++j) {
+        l += vl[j];
+        h += vh[j];
+      }
+      if (n[i] && h * MORE >= need) e0 = tid * EACH + i;
+      if (n[i] && l * LESS >= need) e1 = tid * EACH + i;
+    }
+    e0 = __reduce_min_sync(0xffffffffu, e0);
+    e1 = __reduce_min_sync(0xffffffffu, e1);
+    if (lane == 0) {
+      atomicMin(&sh.edge[0], e0);
+      atomicMin(&sh.edge[1], e1);
     }
     __syncthreads();
     b0 = sh.edge[0];
@@ -368,13 +531,17 @@ struct Sampler {
       if (tid * EACH + i == b1) sh.scan[1] = bc;
     }
     __syncthreads();
+    before = sh.scan[0];
     return sh.scan[1] - sh.scan[0];
   }
 
+  // Counts start at 0 again (the other blocks are done with them: a barrier of the cluster has passed since they read),
+  // and a new list, while the last one may still be read.
   __device__ void clear() {
-    sync();                                  // (the others are done with the last counts)
-    for (int i = tid; i < BINS; i += THREADS) sh.hist[i] = sh.mass_lo[i] = sh.mass_hi[i] = 0;
-    if (tid == 0) sh.n = 0;
+    __syncthreads();
+    for (int i = tid; i < BINS; i += THREADS) sh.hist[i] = 0;
+    turn ^= 1;
+    if (tid == 0) sh.n[turn] = 0;
     __syncthreads();
   }
 
@@ -383,44 +550,34 @@ struct Sampler {
   template <bool MASS>
   __device__ Cut descend(uint64_t need) {
     int b0, b1;
-    const float step = 1.0f / bins;          // (bins is 0 where all are equal: then there is one bin, of weight 1)
-    auto bound = [&](float y) { return bins > 0.0f ? exp2f(FRAC - fmaxf(y, 0.0f) * step) : exp2f(FRAC); };
-    uint32_t n = find((float)need, [&](int b) { return MASS ? bound(b + 0.51f) : 1.0f; },
-                      [&](int b) { return MASS ? bound(b - 0.51f) : 1.0f; }, b0, b1);
-    // what lies between the edges, and above them
-    auto inside = [&](float x, int i, bool& over) {
-      over = false;
-      if (!kept(cut, x, i)) return false;
-      const float y = y_of(x);
-      if (!(y < Y_MOST)) return false;
-      const int b = bin_of(y);
-      over = b < b0;
-      return b >= b0 && b <= b1;
-    };
-    if (n <= LIST) return search<MASS>(need, inside);
+    uint32_t before, n;
+    if constexpr (MASS) {
+      // parts of 4096 of a bin's largest weight, each off by at most 2**-12
+      const float step = 1.0f / bins;        // (bins is 0 where all are equal: then there is one bin, of weight 1)
+      auto largest = [&](int b) { return exp2f(FRAC - 12 - (bins > 0.0f ? (b - 0.5f) * step : 0.0f)); };
+      n = find((float)need, [&](int b) { return largest(b) * (1.0f - 1.0f / 4096); },
+               [&](int b) { return largest(b) * (1.0f + 1.0f / 4096); }, b0, b1, before);
+      n = n / 4096 + n / 131072 + 2;         // not fewer than there are: a part is 4032 or more
+    } else {
+      n = find((float)need, [](int) { return 1.0f; }, [](int) { return 1.0f; }, b0, b1, before);
+    }
+    // the bins from edge to edge as a range of keys
+    uint32_t k0 = key_below(b1 + 1) + 1, k1 = key_below(b0);
+    if (n <= LIST) return search<MASS>(need, before, value_of(k0), value_of(k1));
     uint64_t above = 0;
-    uint32_t lowest = 0xffffffffu, highest = 0;
     row.each([&](float x, int i) {
-      bool over;
-      if (inside(x, i, over)) {
-        const uint32_t k = key_of(x + 0.0f);
-        lowest = min(lowest, k);
-        highest = max(highest, k);
-      }
-      if (over) above += MASS ? w_of(x) : 1;
+      if (x > value_of(k1) && kept(cut, x, i)) above += MASS ? w_of(x) : 1;
     });
-    above = row_sum(above);
-    lowest = __reduce_min_sync(0xffffffffu, lowest);
-    highest = __reduce_max_sync(0xffffffffu, highest);
-    exchange((uint64_t)lowest << 32 | (0xffffffffu - highest), [&](int, uint64_t w) {
-      lowest = min(lowest, (uint32_t)(w >> 32));
-      highest = max(highest, 0xffffffffu - (uint32_t)w);
-    });
-    uint32_t k0 = __reduce_min_sync(0xffffffffu, lowest), k1 = __reduce_max_sync(0xffffffffu, highest);
+    above = row_sum(above);                  // (MASS false: `before`)
     // by keys: exact sums of 2048 ranges of them, of which one holds the last kept token; at most three times
     for (;;) {
       const int bits = 32 - __clz((k1 - k0) | 1), shift = bits > 11 ? bits - 11 : 0;
+      sync();                                // (the others are done with the last sums)
       clear();
+      if (MASS) {
+        for (int i = tid; i < BINS; i += THREADS) sh.mass_lo[i] = sh.mass_hi[i] = 0;
+        __syncthreads();
+      }
       row.each([&](float x, int i) {
         if (!kept(cut, x, i)) return;
         const uint32_t k = key_of(x + 0.0f);
@@ -439,15 +596,24 @@ struct Sampler {
       const uint32_t width = (1u << shift) - 1;
       k0 = width < top_key - k0 ? top_key - width : k0;
       k1 = top_key;
-      if (n <= LIST)
-        return search<MASS>(need, [&](float x, int i, bool& over) {
-          over = false;
-          if (!kept(cut, x, i)) return false;
-          const uint32_t k = key_of(x + 0.0f);
-          over = k > k1;
-          return k >= k0 && k <= k1;
-        });
+      if (n <= LIST) return search<MASS>(need, above, value_of(k0), value_of(k1));
     }
+  }
+
+  // The highest key of a logit that is not in a bin below b: bins do not fall as logits fall, and the lanes try 32 keys at
+  // a time.
+  __device__ uint32_t key_below(int b) const {
+    uint32_t lo = KEY_LOWEST, hi = key_of(s.top);
+    while (lo < hi) {
+      const uint32_t span = hi - lo;
+      auto tried = [&](int j) { return lo + (uint32_t)(((uint64_t)span * (j + 1) + 31) / 32); };
+      const float y = y_of(value_of(tried(lane)));
+      const int n = __popc(__ballot_sync(0xffffffffu, !(y < Y_MOST) || bin_of(y) >= b));
+      const uint32_t next = n > 0 ? tried(n - 1) : lo;
+      if (n < 32) hi = tried(n) - 1;
+      lo = next;
+    }
+    return lo;
   }
 
   // The bin whose tokens reach `need`, by exact sums; what lies above it is added to `above`, n is its number of tokens.
@@ -475,11 +641,9 @@ struct Sampler {
       const uint64_t up = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += up;
     }
-    __syncthreads();
-    if (lane == 31) sh.own[warp] = inc;
-    __syncthreads();
-    uint64_t before = inc - sum;
-    for (int w = 0; w < warp; ++w) before += sh.own[w];
+    const uint64_t shares = within(__shfl_sync(0xffffffffu, inc, 31));
+    const uint64_t before_warp = warp_sum(lane < warp ? shares : 0);
+    uint64_t before = before_warp + inc - sum;
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
       if (before < need && need <= before + v[i]) {
@@ -503,110 +667,143 @@ struct Sampler {
       const uint64_t w = w_of(x);
       m = w ? (need + w - 1) / w : n;
     }
-    // (a cut at this very logit keeps fewer of them already)
-    return Cut{x, m >= n ? (cut.x == x ? cut.last : row.V) : nth(x, m)};
+    if (m >= n) {
+      sync();                                // (the others may still read this block's sums)
+      return Cut{x, cut.x == x ? cut.last : row.V};      // (a cut at this very logit keeps just these)
+    }
+    return Cut{x, nth(x, m)};
   }
 
-  // The cut where its token is among at most LIST ones: `inside` tells which, and which others lie above them.
-  template <bool MASS, class F>
-  __device__ Cut search(uint64_t need, F inside) {
-    uint64_t above = 0;
-    row.each([&](float x, int i) {
-      bool over;
-      if (inside(x, i, over)) {
-        const int at = atomicAdd(&sh.n, 1);
-        if (at < LIST) {
-          sh.list_x[at] = x + 0.0f;
-          sh.list_i[at] = i;
+  // The cut where its token is among the at most LIST ones with logits from x0 to x1, `before` tokens lying above x1.
+  // The warps' weights of what it keeps come out with it.
+  template <bool MASS>
+  __device__ Cut search(uint64_t need, uint64_t before, float x0, float x1) {
+    int* const mine = &sh.n[turn];
+    const float least = fmaxf(x0, cut.x);
+    auto gather = [&](float x, int i) {
+      if (x < least || !(x > cut.x || kept(cut, x, i))) return false;
+      if (x > x1) return true;
+      const int at = atomicAdd(mine, 1);
+      if (at < LIST) {
+        sh.list_x[at] = x + 0.0f;
+        sh.list_i[at] = i;
+      }
+      return false;
+    };
+    share = warp_sum(weigh<true>(gather));
+    uint64_t over = 0;
+    exchange(share, [&](int, uint64_t w) { over += w; });
+    need -= MASS ? warp_sum(over) : before;
+    // every block takes the whole list
+    const int have = lane < blocks ? (blocks == 1 ? *mine : (int)ld_cluster_u32(remote(mine, lane))) : 0;
+    int upto = have;
+#pragma unroll
+    for (int o = 1; o < MOST_BLOCKS; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += up;
+    }
+    const int n = min(__shfl_sync(0xffffffffu, upto, MOST_BLOCKS - 1), LIST);
+    for (int i0 = warp * 32; i0 < n; i0 += THREADS) {
+      const int i = i0 + lane;
+      int block = 0, from = 0;               // whose list entry i is in, and what comes before that
+#pragma unroll
+      for (int b = 0; b < MOST_BLOCKS - 1; ++b) {
+        const int end = __shfl_sync(0xffffffffu, upto, b);
+        if (i >= end) {
+          block = b + 1;
+          from = end;
         }
       }
-      if (over) above += MASS ? w_of(x) : 1;
-    });
-    need -= row_sum(above);
-    // every block takes the whole list
-    sync();
-    int n = 0;
-    for (int b = 0; b < blocks; ++b) {
-      const int have = blocks == 1 ? sh.n : (int)ld_cluster_u32(remote(&sh.n, b));
-      for (int i = tid; i < have && n + i < LIST; i += THREADS) {
-        sh.all_x[n + i] = blocks == 1 ? sh.list_x[i] : __uint_as_float(ld_cluster_u32(remote(&sh.list_x[i], b)));
-        sh.all_i[n + i] = blocks == 1 ? sh.list_i[i] : (int)ld_cluster_u32(remote(&sh.list_i[i], b));
+      if (i < n && i - from < LIST) {
+        float x;
+        int at;
+        if (blocks == 1) {
+          x = sh.list_x[i];
+          at = sh.list_i[i];
+        } else {
+          x = __uint_as_float(ld_cluster_u32(remote(&sh.list_x[i - from], block)));
+          at = (int)ld_cluster_u32(remote(&sh.list_i[i - from], block));
+        }
+        sh.all_x[i] = x;
+        sh.all_i[i] = at;
+        sh.all_w[i] = w_of(x);
       }
-      n = min(n + have, LIST);
     }
     __syncthreads();
-    constexpr int PER = LIST / THREADS;
-    uint32_t key[PER], lo = 0xffffffffu, hi = 0;
-    uint64_t w[PER];
-    int index[PER];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int i = tid + j * THREADS;
-      const float x = i < n ? sh.all_x[i] : -INFINITY;
-      index[j] = i < n ? sh.all_i[i] : -1;
-      key[j] = i < n ? key_of(x) >> KEY_SHIFT : 0;
-      w[j] = i < n ? (MASS ? w_of(x) : 1) : 0;
-      if (i < n) {
-        lo = min(lo, key[j]);
-        hi = max(hi, key[j]);
-      }
+    auto key = [&](int i) { return key_of(sh.all_x[i]) >> KEY_SHIFT; };
+    uint32_t lo = 0xffffffffu, hi = 0;
+    for (int i = lane; i < n; i += 32) {
+      lo = min(lo, key(i));
+      hi = max(hi, key(i));
     }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) sh.own[warp] = (uint64_t)lo << 32 | hi;
-    __syncthreads();
-    {
-      const uint64_t v = lane < WARPS ? sh.own[lane] : 0xffffffff00000000ull;
-      lo = __reduce_min_sync(0xffffffffu, (uint32_t)(v >> 32));
-      hi = __reduce_max_sync(0xffffffffu, (uint32_t)v);
-    }
-    // the lowest key with less than `need` above it
+    // the lowest key with less than `need` above it: the warps try 16 at a time
     while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo) / 2;
+      const uint32_t mid = lo + (uint32_t)((uint64_t)(hi - lo) * (warp + 1) / (WARPS + 1));
       uint64_t t = 0;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) t += key[j] > mid ? w[j] : 0;
-      if (block_sum(t) < need) hi = mid;
-      else lo = mid + 1;
+      for (int i = lane; i < n; i += 32) t += key(i) > mid ? (MASS ? sh.all_w[i] : 1) : 0;
+      const uint64_t sums = within(warp_sum(t));
+      const uint32_t less = __ballot_sync(0xffffffffu, lane < WARPS && sums < need);
+      const int w = less ? __ffs(less) - 1 : WARPS;        // the first that leaves less
+      const uint32_t was = lo;
+      auto tried = [&](int j) { return was + (uint32_t)((uint64_t)(hi - was) * (j + 1) / (WARPS + 1)); };
+      if (w > 0) lo = tried(w - 1) + 1;
+      if (w < WARPS) hi = tried(w);
     }
-    uint64_t t = 0, one = 0;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      t += key[j] > lo ? w[j] : 0;
-      one += index[j] >= 0 && key[j] == lo;
+    // its tokens, and what lies above them
+    uint64_t above = 0;
+    int ties = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t k = i < n ? key(i) : 0;
+      above += k > lo ? (MASS ? sh.all_w[i] : 1) : 0;
+      const bool is = i < n && k == lo;
+      const uint32_t vote = __ballot_sync(0xffffffffu, is);
+      // (every warp writes the same)
+      if (is) sh.tie[ties + __popc(vote & ((1u << lane) - 1))] = i;
+      ties += __popc(vote);
     }
-    const uint64_t left = need - block_sum(t);
-    const uint64_t ties = block_sum(one);
-    // of its tokens the first m, by index
-#pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (index[j] >= 0 && key[j] == lo) {
-        sh.found = tid + j * THREADS;        // (any of them: they are equal)
-      }
     __syncthreads();
-    const float x = sh.all_x[sh.found];
-    uint64_t m = left;
+    above = warp_sum(above);
+    const float x = sh.all_x[sh.tie[0]];
+    // of them the first m, by index
+    uint64_t m = need - above;
     if (MASS) {
       const uint64_t each = w_of(x);
-      m = each ? (left + each - 1) / each : ties;
+      m = each ? (m + each - 1) / each : ties;
     }
-    if (m >= ties) return Cut{x, cut.x == x ? cut.last : row.V};
     int i0 = 0, i1 = row.V - 1;
+    if (m >= (uint64_t)ties) i0 = i1 = cut.x == x ? cut.last : row.V;
     while (i0 < i1) {
-      const int mid = (i0 + i1) / 2;
-      uint64_t c = 0;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) c += index[j] >= 0 && key[j] == lo && index[j] <= mid;
-      if (block_sum(c) >= m) i1 = mid;
-      else i0 = mid + 1;
+      const int mid = i0 + (int)((int64_t)(i1 - i0) * (warp + 1) / (WARPS + 1));
+      uint32_t c = 0;
+      for (int i = lane; i < ties; i += 32) c += sh.all_i[sh.tie[i]] <= mid;
+      const uint64_t sums = within(__reduce_add_sync(0xffffffffu, c));
+      const uint32_t enough = __ballot_sync(0xffffffffu, lane < WARPS && sums >= m);
+      const int w = enough ? __ffs(enough) - 1 : WARPS;
+      const int was = i0;
+      auto tried = [&](int j) { return was + (int)((int64_t)(i1 - was) * (j + 1) / (WARPS + 1)); };
+      if (w > 0) i0 = tried(w - 1) + 1;
+      if (w < WARPS) i1 = tried(w);
     }
-    return Cut{x, i0};
+    known = Cut{x, i0};
+    // what the list adds to this warp's weights
+    const int from = row.first * Row<T>::E - row.shift, to = row.last * Row<T>::E - row.shift;
+    uint64_t more = 0;
+    for (int i = lane; i < n; i += 32) {
+      const int at = sh.all_i[i];
+      if (at >= from && at < to && kept(known, sh.all_x[i], at)) more += sh.all_w[i];
+    }
+    share += warp_sum(more);
+    return known;
   }
 };
 
 template <class T>
 __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, int blocks) {
-  __shared__ Shared sh;
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blocks == 1 ? 0 : (int)cluster_ctarank();
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -615,20 +812,34 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   const int V = (int)a.V;
   const Row<T> row(static_cast<const T*>(a.logits) + r * a.ld, V, rank * WARPS + warp, blocks * WARPS, lane);
   if (tid < 32) {
-    const double v = exp2(-tid / 32.0);
-    sh.table.fixed[tid] = (uint64_t)(v * 1152921504606846976.0);     // 2**60
-    sh.table.value[tid] = (float)v;
+    sh.table.fixed[tid] = ROOTS[tid];
+    sh.table.value[tid] = (float)ROOTS[tid] * (1.0f / 1152921504606846976.0f);     // 2**60
   }
   for (int i = tid; i < BINS; i += THREADS) sh.hist[i] = 0;
-  if (tid == 0) sh.n = 0;
+  const float heat = a.temperature ? a.temperature[r] : 1.0f;
+  const int k = a.top_k ? a.top_k[r] : 0;
+  const float share = a.top_p ? a.top_p[r] : 1.0f, m = a.min_p ? a.min_p[r] : 0.0f, u = a.u[r];
+  // (64-bit arithmetic is slow here: one thread's part for the block)
+  if (tid == THREADS - 1) {
+    sh.n[0] = sh.n[1] = 0;
+    const double c = fmin(1.4426950408889634 / (double)heat, 1e30);
+    sh.c_hi = (float)c;
+    sh.c_lo = (float)(c - (double)sh.c_hi);
+    sh.reach = m > 0.0f && m <= 1.0f ? (double)heat * log((double)m) : 0.0;
+  }
 
   Sampler<T> p(sh, row, blocks, rank);
-  // ---- the largest and the smallest logit ----
+  // ---- the largest logit, and the smallest where steps of y will be counted ----
   float top = -INFINITY, least = INFINITY;
-  row.each([&](float x, int) {
-    top = fmaxf(top, x);
-    least = fminf(least, x > -INFINITY ? x : INFINITY);
-  });
+  const bool counts = (k > 0 && k < V) || (share > 0.0f && share < 1.0f);
+  if (counts) {
+    row.each([&](float x, int) {
+      top = fmaxf(top, x);
+      least = fminf(least, x > -INFINITY ? x : INFINITY);
+    });
+  } else {
+    top = row.largest();
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -644,7 +855,6 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
     least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
   }
   top += 0.0f;                               // (-0 is 0)
-  const float heat = a.temperature ? a.temperature[r] : 1.0f;
   if (top == -INFINITY || !(heat > 0.0f) || top == INFINITY) {
     // nothing to take, or the largest
     const int at = top == -INFINITY ? -1 : p.nth(top, 1);
@@ -655,18 +865,16 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
     p.sync();
     return;
   }
-  const double c = fmin(1.4426950408889634 / (double)heat, 1e30);
   p.s.top = top;
-  p.s.c_hi = (float)c;
-  p.s.c_lo = (float)(c - (double)p.s.c_hi);
+  p.s.c_hi = sh.c_hi;
+  p.s.c_lo = sh.c_lo;
   p.cut = Cut{-INFINITY, NONE};
-  const float range = fminf(p.y_of(least), Y_MOST);
+  const float range = counts ? fminf(p.y_of(least), Y_MOST) : 0.0f;
   p.bins = range > 1e-30f ? (BINS - 1) / range : 0.0f;
+  p.slope = range > 1e-30f ? -4096 * 0.69314718f / p.bins : 0.0f;
 
-  const int k = a.top_k ? a.top_k[r] : 0;
   if (k > 0 && k < V) {
     uint64_t n = 0;
-    __syncthreads();
     row.each([&](float x, int) {
       const float y = p.y_of(x);
       if (y < Y_MOST) {
@@ -676,39 +884,34 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
     });
     n = p.row_sum(n);
     if (n > (uint64_t)k) p.cut = p.template descend<false>(k);
-    p.clear();
+    if (counts) p.clear();
   }
-  const float share = a.top_p ? a.top_p[r] : 1.0f;
   if (share <= 0.0f) {
     p.cut = Cut{top, p.nth(top, 1)};
   } else if (share < 1.0f) {
-    uint64_t w = 0;
-    __syncthreads();
-    row.each([&](float x, int i) {
-      if (!kept(p.cut, x, i)) return;
+    uint64_t w = p.row_sum(p.template weigh<false>([&](float x, int i) {
+      if (!kept(p.cut, x, i)) return false;
       const float y = p.y_of(x);
-      if (!(y < Y_MOST)) return;
-      atomicAdd(&sh.hist[p.bin_of(y)], 1);
-      w += p.w_of(x);
-    });
-    w = p.row_sum(w);
+      if (!(y < Y_MOST)) return false;
+      const int b = p.bin_of(y);
+      atomicAdd(&sh.hist[b], p.part_of(y, b));
+      return true;
+    }));
     p.cut = strictest(p.cut, p.template descend<true>(times(share, w, true)));
   }
-  const float m = a.min_p ? a.min_p[r] : 0.0f;
   if (m > 1.0f) {
     p.cut = strictest(p.cut, Cut{top, p.nth(top, 1)});
   } else if (m > 0.0f) {
     // w >= m where x >= max + t ln m
-    const float x = __double2float_ru((double)top + (double)heat * log((double)m));
+    const float x = __double2float_ru((double)top + sh.reach);
     p.cut = strictest(p.cut, Cut{fminf(x, top), x > -INFINITY ? V : NONE});
   }
 
   // ---- kept weights by warp, and the one that u falls on ----
-  uint64_t mine = 0;
-  row.each([&](float x, int i) {
-    if (kept(p.cut, x, i)) mine += p.w_of(x);
-  });
-  mine = warp_sum(mine);
+  auto in = [&](float x, int i) { return kept(p.cut, x, i); };
+  uint64_t mine = p.share;
+  if (p.cut.x != p.known.x || p.cut.last != p.known.last)
+    mine = warp_sum(p.cut.x > -INFINITY ? p.template weigh<true>(in) : p.template weigh<false>(in));
   uint64_t before = 0, total = 0;
   p.exchange(mine, [&](int i, uint64_t w) {
     before += i < rank * WARPS + warp ? w : 0;
@@ -716,7 +919,6 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   });
   before = warp_sum(before);
   total = warp_sum(total);
-  const float u = a.u[r];
   uint64_t at = !(u > 0.0f) ? 0 : (u < 1.0f ? times(u, total, false) : total - 1);
   if (at >= before && at < before + mine) {
     at -= before;
@@ -726,7 +928,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
       int i = 0;
       uint64_t w = 0;
       if (s0 + lane < row.last) {
-        i = row.load(s0 + lane, v);
+        i = row.take(s0 + lane, row.fetch(s0 + lane), v);
 #pragma unroll
         for (int e = 0; e < E; ++e) w += kept(p.cut, v[e], i + e) ? p.w_of(v[e]) : 0;
       }
@@ -771,9 +973,12 @@ inline int row_blocks(int64_t R, int64_t V) {
 template <class T>
 cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
   const int blocks = row_blocks(a.R, a.V);
+  cudaError_t e = set_smem_once(sample_kernel<T>, (int)sizeof(Shared));
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.R * blocks));
   cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
