@@ -1,0 +1,828 @@
+// Attention of a tree of drafted tokens over the 4-bit cache (bq_attn_kv4_tree)
+// for many query rows, on tcgen05.
+//
+// The rows of a kv head are its query heads times the sequence's nodes.  Up to
+// 128 of them are the rows of S = Q K^T, whose accumulator lies in tensor
+// memory with a row a lane, so that a thread has a row's scores and needs no
+// other's for their maximum and sum.  The weights go back to tensor memory as
+// the A operand of O += P V, in the place of the scores.  Keys and values are turned from
+// codes into fp16 once for a block's rows (2 instructions a code pair and one
+// for its step and low), in the layout that the tensor cores read: both have a row a
+// key, which is K-major for the first product and MN-major for the second.
+// The pairs of a word come out as dims (0, 4), (1, 5), (2, 6), (3, 7); queries are stored in
+// that order, and outputs are put back.
+//
+// Two slots of S, P and O keep the tensor cores busy while a slot's softmax runs.  A
+// unit of more than 128 rows has 128 rows in each, over the same keys; a smaller
+// one has the same rows in both, one over its even and one over its odd tiles of 128
+// keys, joined at the end.
+//
+// A block is 17 warps: four of softmax for each slot, four that fetch and convert
+// keys and four values (a tile ahead in registers, two tiles in shared memory), one that
+// issues the products.
+//
+// The tiles of all units are dealt out to the blocks in equal contiguous ranges; a
+// unit that falls into several is joined by a second kernel.
+#include "attn_kv4.cuh"
+#include "draft_internal.h"
+#include "gemm_common.cuh"
+
+namespace bq {
+
+namespace {
+
+constexpr int KT = 128;                     // keys of a tile
+constexpr int SLOT_ROWS = 128;
+constexpr int SOFT_WARPS = 8, LOAD_WARPS = 4;     // of both slots; of keys, and of values
+constexpr int MMA_WARP = SOFT_WARPS + 2 * LOAD_WARPS, TREE_THREADS = 32 * (MMA_WARP + 1);
+constexpr int STAGES = 2;                   // tiles of keys, and of values, in shared memory
+constexpr int HALF_B = KT * 128;            // 64 dims of a tile
+constexpr uint64_t DRAIN_NS = 2000000000ull;
+
+template <int D>
+struct TreeCfg {
+  static constexpr int TILE_B = D / 64 * HALF_B;
+  static constexpr int OFF_K = 2 * TILE_B;                     // behind two tiles of queries
+  static constexpr int OFF_V = OFF_K + STAGES * TILE_B;
+  static constexpr int OFF_X = OFF_V + STAGES * TILE_B;        // maxima and sums of a row, by slot
+  static constexpr int OFF_SEEN = OFF_X + 2 * SLOT_ROWS * 8;   // drafted places that some node sees: 32 words a warp
+  static constexpr int OFF_BAR = OFF_SEEN + LOAD_WARPS * 128;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static constexpr int O_COL = 0, S_COL = 2 * D;               // tensor memory: O, then S (P in its place)
+  static constexpr int COLS = 512;
+};
+
+struct TreeParams {
+  AttnParams a;
+  int rows;                 // of a block: 128 or 256
+  uint64_t timeout_ns;
+};
+
+// A block's share of a unit
+struct Unit {
+  Seq s;
+  int64_t b, u0;            // sequence; the unit's first tile among all
+  int head, row0, rows;
+  int first, last, tiles;   // tiles [first, last) of the unit's
+  bool wide;                // rows in both slots
+};
+
+__device__ __forceinline__ int seq_tiles(const Seq& s) { return (s.tiles + KT / TILE - 1) / (KT / TILE); }
+__device__ __forceinline__ int64_t tree_cost(const AttnParams& a, const Seq& s) {
+  return (int64_t)seq_tiles(s) * s.qtiles * a.heads;
+}
+
+// The units of a block's range of tiles, one after the other; every role walks them by itself.
+struct Walk {
+  int64_t at, stop, base, b;
+  Seq s;
+  __device__ __forceinline__ bool next(const TreeParams& p, Unit& u) {
+    const AttnParams& a = p.a;
+    if (at >= stop) return false;
+    while (at >= base + tree_cost(a, s)) {
+      base += tree_cost(a, s);
+      s = load_seq(a, ++b, p.rows);
+    }
+    const int tiles = seq_tiles(s);
+    const int unit = (int)((at - base) / tiles);
+    const int qt = unit / a.heads;
+    u.s = s;
+    u.b = b;
+    u.u0 = base + (int64_t)unit * tiles;
+    u.head = unit - qt * a.heads;
+    u.row0 = qt * p.rows;
+    u.rows = min(p.rows, s.n * a.rep - u.row0);
+    u.tiles = tiles;
+    u.first = (int)(at - u.u0);
+    u.last = (int)min((int64_t)tiles, stop - u.u0);
+    u.wide = u.rows > SLOT_ROWS;
+    at = u.u0 + u.last;
+    return true;
+  }
+};
+
+// 16 columns of 32 lanes from registers
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait_tied16(const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+               "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+               "r"(r[15])
+               : "memory");
+}
+
+// Shared-memory descriptor of an MN-major operand in the 128-byte swizzle layout: rows of 64 elements along MN, one a k;
+// eight of them are 1024 bytes, the next 64 elements of MN are HALF_B further.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3ffffu) >> 4);
+  d |= (uint64_t)(HALF_B >> 4) << 16;                  // leading byte offset: the next 64 of MN
+  d |= (uint64_t)(1024 >> 4) << 32;                    // stride byte offset: the next eight k
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t IDESC_B_MN = 1u << 16;              // B is MN-major
+
+// Four words of codes (32 dims of a key) as fp16 values, into a tile's swizzled row.  Each value is fp16_rne(low + step * code), as
+// bq_qk_norm_rope_kv4 hands it out; where 15 steps pass fp16's range it is held to the largest.
+__device__ __forceinline__ void store_values(uint8_t* row, int key, int piece, const uint4& codes, uint32_t par) {
+  const uint32_t step = prmt(par, par, 0x1010), low = prmt(par, par, 0x3232);
+  const float2 f = unpack_h2(par);
+  const bool large = fabsf(fmaf(15.0f, f.x, f.y)) > 65504.0f;
+  uint8_t* const half = row + (piece >> 1) * HALF_B + key * 128;
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t h[4];
+    const uint32_t y = w[j] >> 8;
+    h[0] = hsub2_u32((w[j] & CODE_LO) | H2_MAGIC, H2_MAGIC);
+    h[1] = hfma2_u32((w[j] & CODE_HI) | H2_MAGIC, H2_INV16, 0xd400d400u);        // (1024 + 16 u) / 16 - 64
+    h[2] = hsub2_u32((y & CODE_LO) | H2_MAGIC, H2_MAGIC);
+    h[3] = hfma2_u32((y & CODE_HI) | H2_MAGIC, H2_INV16, 0xd400d400u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = hfma2_u32(h[i], step, low);
+    if (large) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(0x7bff7bffu));
+        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(0xfbfffbffu));
+      }
+    }
+    *reinterpret_cast<uint4*>(half + ((((piece & 1) * 4 + j) ^ (key & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+}
+
+template <int D, int NG>
+__global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreeParams p) {
+  using C = TreeCfg<D>;
+  constexpr int R = D / 2, PIECES = R / 16;             // bytes and 16-byte pieces of a code row
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ int64_t scan[MMA_WARP + 4];
+  __shared__ Seq first_seq;
+  __shared__ uint32_t tmem_slot;
+  const AttnParams& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* const k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* const k_empty = k_full + STAGES;
+  uint64_t* const v_full = k_empty + STAGES;
+  uint64_t* const v_empty = v_full + STAGES;
+  uint64_t* const s_full = v_empty + STAGES;            // of a slot: scores are there
+  uint64_t* const p_full = s_full + 2;                  // weights are there
+  uint64_t* const o_done = p_full + 2;                  // the unit's last product is done
+  uint64_t* const q_full = o_done + 2;                  // queries are there, and what the last unit left is read
+  uint64_t* const x_full = q_full + 1;                  // maxima and sums of both slots are there
+  uint64_t* const drained = x_full + 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&k_full[i], LOAD_WARPS);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], LOAD_WARPS);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], SOFT_WARPS / 2);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(q_full, SOFT_WARPS);
+    mbar_init(x_full, SOFT_WARPS);
+    mbar_init(drained, 1);
+    mbar_fence_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(&tmem_slot, C::COLS);
+    tmem_relinquish();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- which tiles are ours: equal shares, not less than `least` tiles each ----
+  Walk walk;
+  int64_t each, extra;
+  {
+    const int64_t per = (a.B + TREE_THREADS - 1) / TREE_THREADS;
+    const int64_t b0 = min((int64_t)tid * per, a.B), b1 = min(b0 + per, a.B);
+    int64_t mine = 0;
+    for (int64_t i = b0; i < b1; ++i) mine += tree_cost(a, load_seq(a, i, p.rows));
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) scan[warp] = inc;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w <= MMA_WARP; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    inc += before;
+    constexpr int64_t LEAST = 4;
+    const int64_t blocks = max((int64_t)1, min((int64_t)gridDim.x, total / LEAST));
+    each = total / blocks;
+    extra = total % blocks;
+    walk.at = blockIdx.x < blocks ? each * blockIdx.x + min((int64_t)blockIdx.x, extra) : total;
+    walk.stop = blockIdx.x < blocks ? walk.at + each + (blockIdx.x < extra ? 1 : 0) : total;
+    if (walk.at < walk.stop && walk.at >= inc - mine && walk.at < inc) {
+      int64_t sum = inc - mine, i = b0;
+      Seq s;
+      for (;; ++i) {
+        s = load_seq(a, i, p.rows);
+        if (walk.at < sum + tree_cost(a, s)) break;
+        sum += tree_cost(a, s);
+      }
+      first_seq = s;
+      scan[MMA_WARP + 1] = i;
+      scan[MMA_WARP + 2] = sum;
+    }
+    if (tid == 0 && !a.by_unit) a.meta[blockIdx.x] = Meta{};
+    __syncthreads();
+    walk.b = scan[MMA_WARP + 1];
+    walk.base = scan[MMA_WARP + 2];
+    walk.s = first_seq;
+  }
+  const int64_t at0 = walk.at;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  Unit u;
+  bool ok = true;
+
+  if (warp >= SOFT_WARPS && warp < MMA_WARP) {
+    // ------------------------------------------------------------ codes -> fp16 tiles
+    const bool values = warp >= SOFT_WARPS + LOAD_WARPS;
+    const int w = (warp - SOFT_WARPS) & (LOAD_WARPS - 1);
+    constexpr int KEYS = 32 / PIECES;                   // of a warp's step
+    constexpr int STEPS = KT / (LOAD_WARPS * KEYS);
+    const int piece = lane / KEYS, key_lane = lane % KEYS;
+    const int P = 1 << a.page_log2;
+    uint64_t* const full = values ? v_full : k_full;
+    uint64_t* const empty = values ? v_empty : k_empty;
+    uint8_t* const ring = smem + (values ? C::OFF_V : C::OFF_K);
+    const int par_at = piece * 32 / (D / NG) * 4;       // of a key's params
+    uint32_t* const seen = reinterpret_cast<uint32_t*>(smem + C::OFF_SEEN) + 32 * w;
+    int n = 0;                                          // tiles so far
+    while (ok && walk.next(p, u)) {
+      const int32_t* const trow = a.table + u.b * a.ld_table;
+      const int len = u.s.len, base = len - u.s.n;
+      const int first_seen = a.window > 0 ? (int)max((int64_t)0, (int64_t)base + 1 - a.window) : 0;
+      auto key_of_step = [&](int t, int i) {
+        return u.s.begin + t * KT + (i * LOAD_WARPS + w) * KEYS + key_lane;
+      };
+      int page[STEPS];
+      uint4 codes[STEPS];
+      uint32_t par[STEPS];
+      auto fetch_pages = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const int key = key_of_step(t, i);
+          int v = 0;
+          if (t < u.last && key < len) {
+            v = trow[key >> a.page_log2];
+            if (v < 0 || v >= a.num_pages) {
+              record_error(a.status, BQ_ERR_INVALID_ARG);
+              v = 0;
+            }
+          }
+          page[i] = v;
+        }
+      };
+      auto fetch_codes = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const int key = key_of_step(t, i);
+          codes[i] = make_uint4(0, 0, 0, 0);
+          par[i] = 0;
+          if (t < u.last && key < len) {
+            const int64_t row = (((int64_t)page[i] * 2 + (values ? 1 : 0)) * a.heads + u.head) * P + (key & (P - 1));
+            codes[i] = *reinterpret_cast<const uint4*>(a.codes + row * R + piece * 16);
+            par[i] = *reinterpret_cast<const uint32_t*>(a.params + row * (4 * NG) + par_at);
+          }
+        }
+      };
+      fetch_pages(u.first);
+      fetch_codes(u.first);
+      fetch_pages(u.first + 1);
+      bool marked = !values;                            // the drafted places that are seen are known
+      for (int t = u.first; t < u.last; ++t, ++n) {
+        const int stage = n % STAGES;
+        uint4 now[STEPS];
+        uint32_t now_par[STEPS];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          now[i] = codes[i];
+          now_par[i] = par[i];
+        }
+        fetch_codes(t + 1);
+        fetch_pages(t + 2);
+        const int tile0 = u.s.begin + t * KT;
+        if (values && (tile0 + KT > base || tile0 < first_seen)) {
+          // values at places that no node sees are zeros: their weights are 0, but they may be NaN
+          if (!marked && tile0 + KT > base) {
+            marked = true;
+            seen[lane] = 0;
+            __syncwarp();
+            for (int i = lane; i < u.s.n * a.words; i += 32) {
+              const uint64_t v = __ldg(a.tree + (u.s.first + i / a.words) * a.words + i % a.words);
+              atomicOr(&seen[2 * (i % a.words)], (uint32_t)v);
+              atomicOr(&seen[2 * (i % a.words) + 1], (uint32_t)(v >> 32));
+            }
+            __syncwarp();
+          }
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i) {
+            const int key = key_of_step(t, i), j = key - base;
+            if (key >= len || key < first_seen || (j >= 0 && !((seen[j >> 5] >> (j & 31)) & 1))) {
+              now[i] = make_uint4(0, 0, 0, 0);
+              now_par[i] = 0;
+            }
+          }
+        }
+        if (!warp_wait(&empty[stage], ((n / STAGES) & 1) ^ 1, p.timeout_ns, a.status)) {
+          ok = false;
+          break;
+        }
+        uint8_t* const tile = ring + stage * C::TILE_B;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+          store_values(tile, (i * LOAD_WARPS + w) * KEYS + key_lane, piece, now[i], now_par[i]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[stage]);
+      }
+    }
+  } else if (warp == MMA_WARP) {
+    // ------------------------------------------------------------ products
+    const uint32_t sb = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+    constexpr uint32_t IDESC_S = idesc_f16_f32(SLOT_ROWS, KT), IDESC_O = idesc_f16_f32(SLOT_ROWS, D) | IDESC_B_MN;
+    int n = 0, units = 0;                               // tiles and units so far
+    int weights[2] = {0, 0};                            // tiles whose weights were waited for, by slot
+    while (ok && walk.next(p, u)) {
+      const int count = u.last - u.first;
+      if (!warp_wait(q_full, units & 1, p.timeout_ns, a.status)) break;
+      ++units;
+      tc_fence_after();
+      // slot s works on tiles i (wide), or 2 i + s, of the unit's share
+      const int turns = u.wide ? count : (count + 1) / 2;
+      auto tile_of = [&](int s, int i) { return u.wide ? i : 2 * i + s; };
+      auto scores = [&](int s, int i) {
+        const int t = n + tile_of(s, i), stage = t % STAGES;
+        if (!u.wide || s == 0) {
+          if (!warp_wait(&k_full[stage], (t / STAGES) & 1, p.timeout_ns, a.status)) return false;
+          tc_fence_after();
+        }
+        if (elect_one()) {
+          const uint32_t q = sb + (u.wide ? s * C::TILE_B : 0), k = sb + C::OFF_K + stage * C::TILE_B;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * HALF_B + (kk % 4) * 32;
+            tc_mma_f16(tmem + C::S_COL + s * KT, smem_desc_sw128(q + off), smem_desc_sw128(k + off), IDESC_S, kk > 0);
+          }
+          tc_commit(&s_full[s]);
+          if (!u.wide || s == 1) tc_commit(&k_empty[stage]);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int s = 0; s < 2 && ok; ++s)
+        if (tile_of(s, 0) < count) ok = scores(s, 0);
+      for (int i = 0; i < turns && ok; ++i)
+        for (int s = 0; s < 2 && ok; ++s) {
+          const int mine = tile_of(s, i);
+          if (mine >= count) continue;
+          const int t = n + mine, stage = t % STAGES;
+          if (!u.wide || s == 0) ok = warp_wait(&v_full[stage], (t / STAGES) & 1, p.timeout_ns, a.status);
+          ok = ok && warp_wait(&p_full[s], weights[s] & 1, p.timeout_ns, a.status);
+          if (!ok) break;
+          ++weights[s];
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t v = sb + C::OFF_V + stage * C::TILE_B;
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk)
+              tc_mma_f16_ts(tmem + C::O_COL + s * D, tmem + C::S_COL + s * KT + 8 * kk, smem_desc_sw128_mn(v + kk * 2048),
+                            IDESC_O, i > 0 || kk > 0);
+            if (!u.wide || s == 1) tc_commit(&v_empty[stage]);
+            if (tile_of(s, i + 1) >= count) tc_commit(&o_done[s]);
+          }
+          __syncwarp();
+          if (tile_of(s, i + 1) < count) ok = scores(s, i + 1);
+        }
+      n += count;
+    }
+    // whatever was issued is done before the tensor memory goes back
+    if (elect_one()) tc_commit(drained);
+    __syncwarp();
+    mbar_wait(drained, 0, DRAIN_NS, a.status);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax, and a unit's end
+    const int slot = warp / (SOFT_WARPS / 2), r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t s_at = lanes + C::S_COL + slot * KT;
+    float2* const shared_ml = reinterpret_cast<float2*>(smem + C::OFF_X);
+    const float scale = fabsf(a.scale) * LOG2E;
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+    int n = 0, ends[2] = {0, 0}, joins = 0;             // tiles of this slot, units that each slot had a part in, and joined ones
+    while (walk.next(p, u)) {
+      const int count = u.last - u.first;
+      const int turns = u.wide ? count : (count + 1 - slot) / 2;
+      // ---- queries ----
+      const int row = u.row0 + (u.wide ? slot * SLOT_ROWS : 0) + r;      // of the sequence's
+      const bool live = row < u.row0 + u.rows;
+      const int rr = live ? row : u.row0;
+      const int tok = rr / a.rep, hr = rr - tok * a.rep;
+      if (u.wide || slot == 0) {
+        const __half* qp = a.q + (u.s.first + tok) * a.ld_q + (int64_t)(u.head * a.rep + hr) * D;
+        uint8_t* const q = smem + (u.wide ? slot * C::TILE_B : 0) + r * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live) v = *reinterpret_cast<const uint4*>(qp + 8 * c);
+          // dims (0, 4), (1, 5), (2, 6), (3, 7)
+          const uint4 o = make_uint4(prmt(v.x, v.z, 0x5410) ^ flip, prmt(v.x, v.z, 0x7632) ^ flip,
+                                     prmt(v.y, v.w, 0x5410) ^ flip, prmt(v.y, v.w, 0x7632) ^ flip);
+          *reinterpret_cast<uint4*>(q + (c / 8) * HALF_B + (((c % 8) ^ (r & 7)) << 4)) = o;
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+
+      const int len = u.s.len, base = len - u.s.n;
+      const int64_t token = u.s.first + tok;
+      const int depth = live ? tree_depth(a, token) : 0;
+      const int lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)base + depth - a.window) : 0;
+      // every row sees the keys from all_begin to base
+      const int all_begin = a.window > 0 ? (int)max((int64_t)0, (int64_t)len - a.window) : 0;
+      const bool idle = !__any_sync(0xffffffffu, live);
+      float m = -INFINITY, l = 0.0f;
+      for (int i = 0; i < turns; ++i, ++n) {
+        if (!warp_wait(&s_full[slot], n & 1, p.timeout_ns, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (!idle) {
+          const int t = u.first + (u.wide ? i : 2 * i + slot), key0 = u.s.begin + t * KT;
+          const bool masked = key0 + KT > base || key0 < all_begin;
+          uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int k0 = key0 + 32 * c;
+              // keys before the draft, from lo on
+              uint32_t v = 0;
+              if (k0 < base) {
+                v = base - k0 >= 32 ? 0xffffffffu : (1u << (base - k0)) - 1;
+                if (lo > k0) v = lo - k0 >= 32 ? 0 : v & ~((1u << (lo - k0)) - 1);
+              }
+              // drafted ones: bits from k0 - base on
+              const int j = k0 - base;
+              if (j > -32 && j < u.s.n) {
+                const uint64_t* bits = a.tree + token * a.words;
+                uint64_t d;
+                if (j < 0) {
+                  d = __ldg(bits) << -j;
+                } else {
+                  d = __ldg(bits + (j >> 6)) >> (j & 63);
+                  if ((j & 63) > 32 && (j >> 6) + 1 < a.words) d |= __ldg(bits + (j >> 6) + 1) << (64 - (j & 63));
+                }
+                uint32_t x = (uint32_t)d;
+                if (len - k0 < 32) x &= len > k0 ? (1u << (len - k0)) - 1 : 0;
+                v |= x;
+              }
+              vis[c] = depth > 0 ? v : 0;
+            }
+          }
+          // ---- the row's largest score ----
+          float top = -INFINITY;
+          {
+            uint32_t x[32];
+#pragma unroll
+            for (int c = 0; c < KT / 32; ++c) {
+              tmem_ld_32x32b_x32(s_at + 32 * c, x);
+              tmem_ld_wait_tied(x);
+              if (masked) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  top = fmaxf(top, (vis[c] >> e) & 1 ? __uint_as_float(x[e]) : -INFINITY);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
+              }
+            }
+          }
+          top *= scale;
+          // the running maximum is renewed only when it would rise by more than 2**8
+          const bool renew = top > m + 8.0f;
+          if (__any_sync(0xffffffffu, renew)) {
+            const float f = renew ? ex2(m - top) : 1.0f;
+            if (renew) m = top;
+            l *= f;
+            if (i > 0) {
+              // (the last tile's product is done: its commit came before these scores')
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t x[32];
+                tmem_ld_32x32b_x32(lanes + C::O_COL + slot * D + 32 * c, x);
+                tmem_ld_wait_tied(x);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                tmem_st_32x32b_x32(lanes + C::O_COL + slot * D + 32 * c, x);
+                tmem_st_wait_tied(x);
+              }
+            }
+          }
+          // ---- weights ----
+          const float down = m == -INFINITY ? 0.0f : -m;
+          P2 sum = p2(0.0f, 0.0f);
+          const P2 c2 = p2(scale, scale), d2 = p2(down, down);
+#pragma unroll
+          for (int c = 0; c < KT / 32; ++c) {
+            uint32_t x[32], w[16];
+            tmem_ld_32x32b_x32(s_at + 32 * c, x);
+            tmem_ld_wait_tied(x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 y = f2(fma2(p2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, d2));
+              float e0 = ex2(y.x), e1 = ex2(y.y);
+              if (masked) {
+                if (!((vis[c] >> (2 * e)) & 1)) e0 = 0.0f;
+                if (!((vis[c] >> (2 * e + 1)) & 1)) e1 = 0.0f;
+              }
+              sum = add2(sum, p2(e0, e1));
+              w[e] = pack_h2(e0, e1);
+            }
+            // (the weights' columns lie before the scores still to be read)
+            tmem_st_32x32b_x16(s_at + 16 * c, w);
+            tmem_st_wait_tied16(w);
+          }
+          const float2 s2 = f2(sum);
+          l += s2.x + s2.y;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[slot]);
+      }
+      if (!ok) break;
+      // ---- the unit's end ----
+      const bool whole = u.first == 0 && u.last == u.tiles;
+      bool had[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        had[s] = u.wide || (count + 1 - s) / 2 > 0;
+        if (had[s] && (s == slot || !u.wide)) {
+          ok = ok && warp_wait(&o_done[s], ends[s] & 1, p.timeout_ns, a.status);
+        }
+        if (had[s]) ++ends[s];
+      }
+      if (!ok) break;
+      tc_fence_after();
+      float f[2] = {slot == 0 ? 1.0f : 0.0f, slot == 0 ? 0.0f : 1.0f};
+      if (!u.wide) {
+        // both slots have the same rows: each puts half of their dims together
+        shared_ml[slot * SLOT_ROWS + r] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x_full);
+        if (!warp_wait(x_full, joins++ & 1, p.timeout_ns, a.status)) {
+          ok = false;
+          break;
+        }
+        const float2 x0 = shared_ml[r], x1 = shared_ml[SLOT_ROWS + r];
+        m = fmaxf(x0.x, x1.x);
+        // (a slot that has seen no key has the maximum -inf; of two of those nothing is kept, but for NaN)
+        f[0] = had[0] ? (x0.x == -INFINITY ? (x0.y == x0.y && m != -INFINITY ? 0.0f : 1.0f) : ex2(x0.x - m)) : 0.0f;
+        f[1] = had[1] ? (x1.x == -INFINITY ? (x1.y == x1.y && m != -INFINITY ? 0.0f : 1.0f) : ex2(x1.x - m)) : 0.0f;
+        l = (had[0] ? f[0] * x0.y : 0.0f) + (had[1] ? f[1] * x1.y : 0.0f);
+      }
+      const bool none = depth == 0;                     // padding
+      if (none) l = 0.0f;
+      const float top = l == 0.0f || m == -INFINITY ? (l == l ? M_NONE : 0.0f) : m;
+      const int64_t orow = token * (a.heads * a.rep) + u.head * a.rep + hr;
+      const int64_t part = 2 * (int64_t)blockIdx.x + (u.u0 + u.first != at0 ? 1 : 0);
+      float* const pr = whole ? nullptr : a.parts + (part * p.rows + (row - u.row0)) * (D + 4);
+      const float inv = inverse(l);
+      if (!idle) {
+        const int c0 = u.wide ? 0 : slot * (D / 64), c1 = u.wide ? D / 32 : c0 + D / 64;
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
+          float v[32];
+          uint32_t x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (u.wide ? s != slot : !had[s]) continue;
+            tmem_ld_32x32b_x32(lanes + C::O_COL + s * D + 32 * c, x);
+            tmem_ld_wait_tied(x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(x[e]), f[s], v[e]);
+          }
+          if (live) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              // back in order: columns hold dims 0, 4, 1, 5, 2, 6, 3, 7
+              const float* q = v + 8 * g;
+              if (whole) {
+                uint4 h = make_uint4(pack_h2(q[0] * inv, q[2] * inv), pack_h2(q[4] * inv, q[6] * inv),
+                                     pack_h2(q[1] * inv, q[3] * inv), pack_h2(q[5] * inv, q[7] * inv));
+                if (l == 0.0f) h = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(a.out + orow * D + 32 * c + 8 * g) = h;
+              } else {
+                const bool zero = l == 0.0f;
+                float4* const d = reinterpret_cast<float4*>(pr + 32 * c + 8 * g);
+                d[0] = zero ? make_float4(0, 0, 0, 0) : make_float4(q[0], q[2], q[4], q[6]);
+                d[1] = zero ? make_float4(0, 0, 0, 0) : make_float4(q[1], q[3], q[5], q[7]);
+              }
+            }
+          }
+        }
+        if (live && (u.wide || slot == 0)) {
+          if (!whole) {
+            pr[D] = top;
+            pr[D + 1] = l;
+          } else if (a.lse) {
+            a.lse[orow] = log_sum(top, l);
+          }
+        }
+      }
+      if (u.first == 0 && tid == 0 && (!whole || a.by_unit)) {
+        Meta mm{};
+        if (!whole) {
+          const int64_t last = u.u0 + u.tiles - 1, big = (each + 1) * extra;
+          const int64_t owner = last < big ? last / (each + 1) : extra + (last - big) / each;
+          mm.parts = (int32_t)(owner - blockIdx.x + 1);
+          mm.block = (int32_t)blockIdx.x;
+          mm.slot = u.u0 != at0 ? 1 : 0;
+          mm.head = u.head;
+          mm.row0 = u.row0;
+          mm.rows = u.rows;
+          mm.first = u.s.first;
+        }
+        const int qt = u.row0 / p.rows;
+        a.meta[a.by_unit ? (u.b * a.qtiles + qt) * a.heads + u.head : (int64_t)blockIdx.x] = mm;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::COLS);
+  }
+}
+
+// Joins a unit that fell into several blocks' ranges: a warp takes 128 / D rows at a time, a lane four dims of one.
+template <int D>
+__global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p) {
+  constexpr int JS = D + 4, LANES = D / 4, ROWS = 256 / LANES;
+  const AttnParams& a = p.a;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (a.by_unit && a.cu_q) {
+    // units that do not exist (a sequence with fewer nodes) have no meta
+    const int qt = blockIdx.x / a.heads % a.qtiles;
+    if (qt >= load_seq(a, blockIdx.x / (a.heads * a.qtiles), p.rows).qtiles) return;
+  }
+  const Meta mm = a.meta[blockIdx.x];
+  const int n = mm.parts, d = (threadIdx.x % LANES) * 4;
+  if (n == 0) return;
+  for (int r = blockIdx.y * ROWS + threadIdx.x / LANES; r < mm.rows; r += gridDim.y * ROWS) {
+    auto part = [&](int i) {
+      return a.parts + ((2 * (int64_t)(mm.block + i) + (i == 0 ? mm.slot : 0)) * p.rows + r) * JS;
+    };
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f, mt = M_NONE;
+    for (int i = 0; i < n; i += 4) {
+      float4 x[4];
+      float2 ml[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float* q = part(min(i + u, n - 1));
+        x[u] = *reinterpret_cast<const float4*>(q + d);
+        ml[u] = *reinterpret_cast<const float2*>(q + D);
+        if (i + u >= n) ml[u] = make_float2(M_NONE, 0.0f);
+      }
+      const float top = fmaxf(fmaxf(mt, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+      const float f0 = ex2(mt - top);
+      mt = top;
+      v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
+      sum *= f0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (i + u >= n) break;
+        const float f = ex2(ml[u].x - top);
+        v.x = fmaf(f, x[u].x, v.x);
+        v.y = fmaf(f, x[u].y, v.y);
+        v.z = fmaf(f, x[u].z, v.z);
+        v.w = fmaf(f, x[u].w, v.w);
+        sum = fmaf(f, ml[u].y, sum);
+      }
+    }
+    const int tok = (mm.row0 + r) / a.rep, hr = mm.row0 + r - tok * a.rep;
+    const int64_t orow = (mm.first + tok) * (int64_t)(a.heads * a.rep) + mm.head * a.rep + hr;
+    const float inv = inverse(sum);
+    uint2 h = make_uint2(pack_h2(v.x * inv, v.y * inv), pack_h2(v.z * inv, v.w * inv));
+    if (sum == 0.0f) h = make_uint2(0, 0);
+    *reinterpret_cast<uint2*>(a.out + orow * D + d) = h;
+    if (a.lse && d == 0) a.lse[orow] = log_sum(mt, sum);
+  }
+}
+
+inline int block_rows(int64_t rep, int64_t max_q) { return rep * max_q > SLOT_ROWS ? 2 * SLOT_ROWS : SLOT_ROWS; }
+
+template <class K>
+cudaError_t launch_tree(K kern, dim3 grid, int threads, int smem, cudaStream_t stream, const TreeParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int D, int NG>
+cudaError_t launch_both(const TreeParams& p, cudaStream_t stream) {
+  using C = TreeCfg<D>;
+  auto kern = attn_tree_kernel<D, NG>;
+  cudaError_t e = set_smem_once(kern, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int grid = sm_count();
+  e = launch_tree(kern, dim3((unsigned)grid), TREE_THREADS, C::SMEM, stream, p);
+  if (e != cudaSuccess) return e;
+  const int64_t units = p.a.B * p.a.qtiles * p.a.heads;
+  return launch_tree(attn_tree_join_kernel<D>, dim3((unsigned)(p.a.by_unit ? units : grid), (unsigned)(p.rows / 16)), 256, 0,
+                     stream, p);
+}
+
+}  // namespace
+
+bool attn_tree_tc_applies(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_len) {
+  return D <= 128 && q_heads / kv_heads * max_q > 32 && max_len > 0;
+}
+
+size_t attn_tree_tc_workspace(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q) {
+  const size_t grid = (size_t)sm_count();
+  return meta_bytes(grid) + 2 * grid * block_rows(q_heads / kv_heads, max_q) * (D + 4) * sizeof(float);
+}
+
+cudaError_t launch_attn_tree_tc(const AttnKv4Args& a, const uint64_t* tree, int words, cudaStream_t stream) {
+  TreeParams t{};
+  AttnParams& p = t.a;
+  cudaError_t e = device_status_ptr(&p.status);
+  if (e != cudaSuccess) return e;
+  p.tree = tree;
+  p.words = words;
+  p.q = reinterpret_cast<const __half*>(a.q);
+  p.ld_q = a.ld_q;
+  p.T = a.T;
+  p.codes = a.pool.codes;
+  p.params = reinterpret_cast<const uint8_t*>(a.pool.params);
+  p.num_pages = a.pool.num_pages;
+  p.page_log2 = __builtin_ctz((unsigned)a.pool.page_size);
+  p.heads = a.pool.heads;
+  p.rep = a.q_heads / a.pool.heads;
+  p.table = a.table;
+  p.ld_table = a.ld_table;
+  p.lens = a.lens;
+  p.cu_q = a.cu_q;
+  p.B = a.B;
+  p.each = a.cu_q ? 0 : a.T / a.B;
+  p.max_q = a.max_q;
+  p.max_len = a.max_len;
+  p.window = a.window;
+  p.scale = a.scale;
+  p.out = reinterpret_cast<__half*>(a.out);
+  p.lse = a.lse;
+  t.rows = block_rows(p.rep, a.max_q);
+  t.timeout_ns = (uint64_t)wait_timeout_ns();
+  p.qtiles = (int)((a.max_q * p.rep + t.rows - 1) / t.rows);
+  const size_t grid = (size_t)sm_count();
+  p.meta = static_cast<Meta*>(a.workspace);
+  p.by_unit = a.B * p.qtiles * p.heads <= (int64_t)grid;
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + meta_bytes(grid));
+  const int D = a.pool.D, ng = D / a.pool.group;
+  if (D == 64) return ng == 1 ? launch_both<64, 1>(t, stream) : launch_both<64, 2>(t, stream);
+  if (ng == 1) return launch_both<128, 1>(t, stream);
+  return ng == 2 ? launch_both<128, 2>(t, stream) : launch_both<128, 4>(t, stream);
+}
+
+}  // namespace bq

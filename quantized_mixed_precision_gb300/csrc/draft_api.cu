@@ -39,7 +39,11 @@ size_t bq_attn_kv4_tree_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, 
                                   int64_t max_len) {
   if (B < 1 || kv_heads < 1 || q_heads < 1 || D < 1 || max_q < 1 || max_len < 0 || q_heads % kv_heads != 0) return 0;
   if (B > MAX_ROWS || q_heads > MAX_HEADS || D > 256 || max_q > 64 * MAX_WORDS || max_len > MAX_LEN) return 0;
-  return attn_tree_rows_workspace(q_heads, kv_heads, D, max_q, max_len);
+  // (the call takes the smaller of max_q and T: enough for either form)
+  const size_t rows = attn_tree_rows_workspace(q_heads, kv_heads, D, max_q, max_len);
+  const size_t tc = attn_tree_tc_applies(q_heads, kv_heads, D, max_q, max_len)
+                        ? attn_tree_tc_workspace(q_heads, kv_heads, D, max_q) : 0;
+  return rows > tc ? rows : tc;
 }
 
 bq_status bq_attn_kv4_tree(const uint16_t* q, int64_t ld_q, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D,
@@ -91,7 +95,10 @@ bq_status bq_attn_kv4_tree(const uint16_t* q, int64_t ld_q, int64_t T, int64_t q
   a.out = out;
   a.lse = lse;
   a.workspace = workspace;
-  return from_cuda(launch_attn_tree_rows(a, tree, (int)words, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (attn_tree_tc_applies(q_heads, kv_heads, D, max_q, max_len))
+    return from_cuda(launch_attn_tree_tc(a, tree, (int)words, s));
+  return from_cuda(launch_attn_tree_rows(a, tree, (int)words, s));
 }
 
 bq_status bq_sample(const void* logits, int ltype, int64_t R, int64_t V, int64_t ld, const float* u,
