@@ -17,9 +17,9 @@
 // one has the same rows in both, one over its even and one over its odd tiles of 128
 // keys, joined at the end.
 //
-// A block is 17 warps: four of softmax for each slot, four that fetch and convert
-// keys and four values (a tile ahead in registers, two tiles in shared memory), one that
-// issues the products.
+// A block is five warpgroups: one of softmax for each slot, one that fetches and
+// converts keys and one values (a tile ahead in registers, two tiles in shared
+// memory), one of which a warp issues the products.
 //
 // The tiles of all units are dealt out to the blocks in equal contiguous ranges; a
 // unit that falls into several is joined by a second kernel.
@@ -34,7 +34,9 @@ namespace {
 constexpr int KT = 128;                     // keys of a tile
 constexpr int SLOT_ROWS = 128;
 constexpr int SOFT_WARPS = 8, LOAD_WARPS = 4;     // of both slots; of keys, and of values
-constexpr int MMA_WARP = SOFT_WARPS + 2 * LOAD_WARPS, TREE_THREADS = 32 * (MMA_WARP + 1);
+constexpr int MMA_WARP = SOFT_WARPS + 2 * LOAD_WARPS, TREE_WARPS = MMA_WARP + 4, TREE_THREADS = 32 * TREE_WARPS;
+// Registers of a thread, by warpgroup: 96 at the launch (5 * 96 = 480), then 128, 128, 88, 88 and 48.
+constexpr int SOFT_REGS = 128, LOAD_REGS = 80, MMA_REGS = 64;
 constexpr int STAGES = 2;                   // tiles of keys, and of values, in shared memory
 constexpr int HALF_B = KT * 128;            // 64 dims of a tile
 constexpr uint64_t DRAIN_NS = 2000000000ull;
@@ -130,13 +132,16 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr) {
 }
 constexpr uint32_t IDESC_B_MN = 1u << 16;              // B is MN-major
 
-// Four words of codes (32 dims of a key) as fp16 values, into a tile's swizzled row.  Each value is fp16_rne(low + step * code), as
-// bq_qk_norm_rope_kv4 hands it out; where 15 steps pass fp16's range it is held to the largest.
-__device__ __forceinline__ void store_values(uint8_t* row, int key, int piece, const uint4& codes, uint32_t par) {
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Four words of codes (32 dims of a key) as fp16 values: each is fp16_rne(low + step * code), as bq_qk_norm_rope_kv4 hands
+// it out; where 15 steps pass fp16's range it is held to the largest.
+__device__ __forceinline__ void store_values(const uint32_t (&to)[4], uint32_t off, const uint4& codes, uint32_t par) {
   const uint32_t step = prmt(par, par, 0x1010), low = prmt(par, par, 0x3232);
   const float2 f = unpack_h2(par);
   const bool large = fabsf(fmaf(15.0f, f.x, f.y)) > 65504.0f;
-  uint8_t* const half = row + (piece >> 1) * HALF_B + key * 128;
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -155,8 +160,30 @@ __device__ __forceinline__ void store_values(uint8_t* row, int key, int piece, c
         asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(0xfbfffbffu));
       }
     }
-    *reinterpret_cast<uint4*>(half + ((((piece & 1) * 4 + j) ^ (key & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+    st_shared_v4(to[j] + off, h[0], h[1], h[2], h[3]);
   }
+}
+
+constexpr uint32_t IDESC_S = idesc_f16_f32(SLOT_ROWS, KT);
+
+// One tile's products, by one elected thread: S = Q K^T, and O (+)= P V.
+template <int D>
+__device__ __forceinline__ void issue_scores(uint32_t s_col, uint32_t q, uint32_t k) {
+  const uint64_t qd = smem_desc_sw128(q), kd = smem_desc_sw128(k);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    constexpr int HALF = HALF_B / 16;                  // in the descriptors' units
+    const uint32_t off = (kk / 4) * HALF + (kk % 4) * 2;
+    tc_mma_f16(s_col, qd + off, kd + off, IDESC_S, kk > 0);
+  }
+}
+template <int D>
+__device__ __forceinline__ void issue_values(uint32_t o_col, uint32_t p_col, uint32_t v, bool more) {
+  constexpr uint32_t IDESC_O = idesc_f16_f32(SLOT_ROWS, D) | IDESC_B_MN;
+  const uint64_t vd = smem_desc_sw128_mn(v);
+#pragma unroll
+  for (int kk = 0; kk < KT / 16; ++kk)
+    tc_mma_f16_ts(o_col, p_col + 8 * kk, vd + kk * (2048 / 16), IDESC_O, kk > 0 || more);
 }
 
 template <int D, int NG>
@@ -165,8 +192,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
   constexpr int R = D / 2, PIECES = R / 16;             // bytes and 16-byte pieces of a code row
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ int64_t scan[MMA_WARP + 4];
-  __shared__ Seq first_seq;
+  __shared__ int64_t scan[TREE_WARPS];
+  __shared__ Walk start;                                // where the block's range begins
+  __shared__ int64_t shares[2];                         // tiles of a block; the first so many blocks have one more
+  __shared__ int next_unit[2];                          // of the products' warp: tiles (0: no more units), wide or not
   __shared__ uint32_t tmem_slot;
   const AttnParams& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -206,8 +235,6 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- which tiles are ours: equal shares, not less than `least` tiles each ----
-  Walk walk;
-  int64_t each, extra;
   {
     const int64_t per = (a.B + TREE_THREADS - 1) / TREE_THREADS;
     const int64_t b0 = min((int64_t)tid * per, a.B), b1 = min(b0 + per, a.B);
@@ -224,42 +251,43 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
     __syncthreads();
     tc_fence_after();
     int64_t before = 0, total = 0;
-    for (int w = 0; w <= MMA_WARP; ++w) {
+    for (int w = 0; w < TREE_WARPS; ++w) {
       if (w < warp) before += scan[w];
       total += scan[w];
     }
     inc += before;
     constexpr int64_t LEAST = 4;
     const int64_t blocks = max((int64_t)1, min((int64_t)gridDim.x, total / LEAST));
-    each = total / blocks;
-    extra = total % blocks;
-    walk.at = blockIdx.x < blocks ? each * blockIdx.x + min((int64_t)blockIdx.x, extra) : total;
-    walk.stop = blockIdx.x < blocks ? walk.at + each + (blockIdx.x < extra ? 1 : 0) : total;
-    if (walk.at < walk.stop && walk.at >= inc - mine && walk.at < inc) {
-      int64_t sum = inc - mine, i = b0;
-      Seq s;
-      for (;; ++i) {
-        s = load_seq(a, i, p.rows);
-        if (walk.at < sum + tree_cost(a, s)) break;
-        sum += tree_cost(a, s);
+    const int64_t each = total / blocks, extra = total % blocks;
+    const bool some = blockIdx.x < blocks;
+    const int64_t at = some ? each * blockIdx.x + min((int64_t)blockIdx.x, extra) : total;
+    const int64_t stop = some ? at + each + (blockIdx.x < extra ? 1 : 0) : total;
+    if (at < stop ? at >= inc - mine && at < inc : tid == 0) {
+      Walk walk{at, stop, inc - mine, b0, Seq{}};
+      if (at < stop) {
+        for (;; ++walk.b) {
+          walk.s = load_seq(a, walk.b, p.rows);
+          if (at < walk.base + tree_cost(a, walk.s)) break;
+          walk.base += tree_cost(a, walk.s);
+        }
       }
-      first_seq = s;
-      scan[MMA_WARP + 1] = i;
-      scan[MMA_WARP + 2] = sum;
+      start = walk;
+      shares[0] = each;
+      shares[1] = extra;
     }
     if (tid == 0 && !a.by_unit) a.meta[blockIdx.x] = Meta{};
     __syncthreads();
-    walk.b = scan[MMA_WARP + 1];
-    walk.base = scan[MMA_WARP + 2];
-    walk.s = first_seq;
   }
-  const int64_t at0 = walk.at;
-  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-  Unit u;
-  bool ok = true;
+  // (all 512 columns are this block's: they begin at 0)
+  const uint32_t tmem = tmem_slot;
+  bool ok = tmem == 0;
+  if (!ok && tid == 0) record_error(a.status, BQ_DIAG_RANGE);
 
   if (warp >= SOFT_WARPS && warp < MMA_WARP) {
     // ------------------------------------------------------------ codes -> fp16 tiles
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LOAD_REGS));
+    Walk walk = start;
+    Unit u;
     const bool values = warp >= SOFT_WARPS + LOAD_WARPS;
     const int w = (warp - SOFT_WARPS) & (LOAD_WARPS - 1);
     constexpr int KEYS = 32 / PIECES;                   // of a warp's step
@@ -268,7 +296,12 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
     const int P = 1 << a.page_log2;
     uint64_t* const full = values ? v_full : k_full;
     uint64_t* const empty = values ? v_empty : k_empty;
-    uint8_t* const ring = smem + (values ? C::OFF_V : C::OFF_K);
+    // this lane's four places in a tile's first step: its piece's chunks of a key's row, swizzled
+    uint32_t to[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      to[j] = smem_u32(smem) + (values ? C::OFF_V : C::OFF_K) + (piece >> 1) * HALF_B + (w * KEYS + key_lane) * 128 +
+              ((((piece & 1) * 4 + j) ^ (key_lane & 7)) << 4);
     const int par_at = piece * 32 / (D / NG) * 4;       // of a key's params
     uint32_t* const seen = reinterpret_cast<uint32_t*>(smem + C::OFF_SEEN) + 32 * w;
     int n = 0;                                          // tiles so far
@@ -276,55 +309,47 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
       const int32_t* const trow = a.table + u.b * a.ld_table;
       const int len = u.s.len, base = len - u.s.n;
       const int first_seen = a.window > 0 ? (int)max((int64_t)0, (int64_t)base + 1 - a.window) : 0;
-      auto key_of_step = [&](int t, int i) {
-        return u.s.begin + t * KT + (i * LOAD_WARPS + w) * KEYS + key_lane;
-      };
+      // a step's keys lie in one page (a page's 16 keys are never split)
       int page[STEPS];
       uint4 codes[STEPS];
       uint32_t par[STEPS];
-      auto fetch_pages = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-          const int key = key_of_step(t, i);
-          int v = 0;
-          if (t < u.last && key < len) {
-            v = trow[key >> a.page_log2];
-            if (v < 0 || v >= a.num_pages) {
-              record_error(a.status, BQ_ERR_INVALID_ARG);
-              v = 0;
-            }
+      const int key_first = u.s.begin + w * KEYS;       // of this warp's first step
+      const int last_key = u.last * KT + u.s.begin < len ? u.last * KT + u.s.begin : len;    // keys from here on are not fetched
+      auto key_of_step = [&](int t, int i) { return key_first + t * KT + i * LOAD_WARPS * KEYS; };
+      auto fetch_page = [&](int t, int i) {
+        const int key = key_of_step(t, i);
+        page[i] = key < last_key ? trow[key >> a.page_log2] : 0;
+      };
+      const uint32_t unit_row = ((values ? a.heads : 0) + u.head) * P + key_lane, page_rows = 2u * a.heads * P;
+      const uint8_t* const unit_codes = a.codes + unit_row * (uint64_t)R + piece * 16;
+      const uint8_t* const unit_params = a.params + unit_row * (uint64_t)(4 * NG) + par_at;
+      const uint32_t page_codes = page_rows * R, page_params = page_rows * 4 * NG;      // (below 2**32)
+      auto fetch_codes = [&](int t, int i) {
+        const int key = key_of_step(t, i);
+        codes[i] = make_uint4(0, 0, 0, 0);
+        par[i] = 0;
+        if (key + key_lane < last_key) {
+          // (looked at a tile after its load, which nothing waits for till then)
+          uint32_t at = (uint32_t)page[i];
+          if (at >= (uint64_t)a.num_pages) {
+            record_error(a.status, BQ_ERR_INVALID_ARG);
+            at = 0;
           }
-          page[i] = v;
+          const uint32_t row = key & (P - 1);
+          codes[i] = *reinterpret_cast<const uint4*>(unit_codes + (uint64_t)at * page_codes + row * R);
+          par[i] = *reinterpret_cast<const uint32_t*>(unit_params + (uint64_t)at * page_params + row * (4 * NG));
         }
       };
-      auto fetch_codes = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-          const int key = key_of_step(t, i);
-          codes[i] = make_uint4(0, 0, 0, 0);
-          par[i] = 0;
-          if (t < u.last && key < len) {
-            const int64_t row = (((int64_t)page[i] * 2 + (values ? 1 : 0)) * a.heads + u.head) * P + (key & (P - 1));
-            codes[i] = *reinterpret_cast<const uint4*>(a.codes + row * R + piece * 16);
-            par[i] = *reinterpret_cast<const uint32_t*>(a.params + row * (4 * NG) + par_at);
-          }
-        }
-      };
-      fetch_pages(u.first);
-      fetch_codes(u.first);
-      fetch_pages(u.first + 1);
+      for (int i = 0; i < STEPS; ++i) fetch_page(u.first, i);
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        fetch_codes(u.first, i);
+        fetch_page(u.first + 1, i);
+      }
       bool marked = !values;                            // the drafted places that are seen are known
       for (int t = u.first; t < u.last; ++t, ++n) {
         const int stage = n % STAGES;
-        uint4 now[STEPS];
-        uint32_t now_par[STEPS];
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-          now[i] = codes[i];
-          now_par[i] = par[i];
-        }
-        fetch_codes(t + 1);
-        fetch_pages(t + 2);
         const int tile0 = u.s.begin + t * KT;
         if (values && (tile0 + KT > base || tile0 < first_seen)) {
           // values at places that no node sees are zeros: their weights are 0, but they may be NaN
@@ -341,10 +366,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
           }
 #pragma unroll
           for (int i = 0; i < STEPS; ++i) {
-            const int key = key_of_step(t, i), j = key - base;
+            const int key = key_of_step(t, i) + key_lane, j = key - base;
             if (key >= len || key < first_seen || (j >= 0 && !((seen[j >> 5] >> (j & 31)) & 1))) {
-              now[i] = make_uint4(0, 0, 0, 0);
-              now_par[i] = 0;
+              codes[i] = make_uint4(0, 0, 0, 0);
+              par[i] = 0;
             }
           }
         }
@@ -352,44 +377,45 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
           ok = false;
           break;
         }
-        uint8_t* const tile = ring + stage * C::TILE_B;
+        // (the next tile's codes go into the registers of those that are done with)
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-          store_values(tile, (i * LOAD_WARPS + w) * KEYS + key_lane, piece, now[i], now_par[i]);
+        for (int i = 0; i < STEPS; ++i) {
+          store_values(to, stage * C::TILE_B + i * LOAD_WARPS * KEYS * 128, codes[i], par[i]);
+          fetch_codes(t + 1, i);
+          fetch_page(t + 2, i);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[stage]);
       }
     }
-  } else if (warp == MMA_WARP) {
+  } else if (warp >= MMA_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(MMA_REGS));
+    if (warp == MMA_WARP) {
     // ------------------------------------------------------------ products
-    const uint32_t sb = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
-    constexpr uint32_t IDESC_S = idesc_f16_f32(SLOT_ROWS, KT), IDESC_O = idesc_f16_f32(SLOT_ROWS, D) | IDESC_B_MN;
+    const uint32_t sb = smem_u32(smem);
     int n = 0, units = 0;                               // tiles and units so far
     int weights[2] = {0, 0};                            // tiles whose weights were waited for, by slot
-    while (ok && walk.next(p, u)) {
-      const int count = u.last - u.first;
-      if (!warp_wait(q_full, units & 1, p.timeout_ns, a.status)) break;
+    for (;;) {
+      if (!ok || !warp_wait(q_full, units & 1, p.timeout_ns, a.status)) break;
       ++units;
       tc_fence_after();
+      const int count = next_unit[0];
+      const bool wide = next_unit[1];
+      if (count == 0) break;
       // slot s works on tiles i (wide), or 2 i + s, of the unit's share
-      const int turns = u.wide ? count : (count + 1) / 2;
-      auto tile_of = [&](int s, int i) { return u.wide ? i : 2 * i + s; };
+      const int turns = wide ? count : (count + 1) / 2;
+      auto tile_of = [&](int s, int i) { return wide ? i : 2 * i + s; };
       auto scores = [&](int s, int i) {
         const int t = n + tile_of(s, i), stage = t % STAGES;
-        if (!u.wide || s == 0) {
+        if (!wide || s == 0) {
           if (!warp_wait(&k_full[stage], (t / STAGES) & 1, p.timeout_ns, a.status)) return false;
           tc_fence_after();
         }
         if (elect_one()) {
-          const uint32_t q = sb + (u.wide ? s * C::TILE_B : 0), k = sb + C::OFF_K + stage * C::TILE_B;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * HALF_B + (kk % 4) * 32;
-            tc_mma_f16(tmem + C::S_COL + s * KT, smem_desc_sw128(q + off), smem_desc_sw128(k + off), IDESC_S, kk > 0);
-          }
+          issue_scores<D>(C::S_COL + s * KT, sb + (wide ? s * C::TILE_B : 0), sb + C::OFF_K + stage * C::TILE_B);
           tc_commit(&s_full[s]);
-          if (!u.wide || s == 1) tc_commit(&k_empty[stage]);
+          if (!wide || s == 1) tc_commit(&k_empty[stage]);
         }
         __syncwarp();
         return true;
@@ -401,18 +427,14 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
           const int mine = tile_of(s, i);
           if (mine >= count) continue;
           const int t = n + mine, stage = t % STAGES;
-          if (!u.wide || s == 0) ok = warp_wait(&v_full[stage], (t / STAGES) & 1, p.timeout_ns, a.status);
+          if (!wide || s == 0) ok = warp_wait(&v_full[stage], (t / STAGES) & 1, p.timeout_ns, a.status);
           ok = ok && warp_wait(&p_full[s], weights[s] & 1, p.timeout_ns, a.status);
           if (!ok) break;
           ++weights[s];
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t v = sb + C::OFF_V + stage * C::TILE_B;
-#pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
-              tc_mma_f16_ts(tmem + C::O_COL + s * D, tmem + C::S_COL + s * KT + 8 * kk, smem_desc_sw128_mn(v + kk * 2048),
-                            IDESC_O, i > 0 || kk > 0);
-            if (!u.wide || s == 1) tc_commit(&v_empty[stage]);
+            issue_values<D>(C::O_COL + s * D, C::S_COL + s * KT, sb + C::OFF_V + stage * C::TILE_B, i > 0);
+            if (!wide || s == 1) tc_commit(&v_empty[stage]);
             if (tile_of(s, i + 1) >= count) tc_commit(&o_done[s]);
           }
           __syncwarp();
@@ -425,16 +447,20 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
     __syncwarp();
     mbar_wait(drained, 0, DRAIN_NS, a.status);
     __syncwarp();
+    }
   } else {
     // ------------------------------------------------------------ softmax, and a unit's end
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFT_REGS));
+    Walk walk = start;
+    Unit u;
     const int slot = warp / (SOFT_WARPS / 2), r = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t s_at = lanes + C::S_COL + slot * KT;
     float2* const shared_ml = reinterpret_cast<float2*>(smem + C::OFF_X);
-    const float scale = fabsf(a.scale) * LOG2E;
+    const float scale = fmaxf(fabsf(a.scale) * LOG2E, 1e-37f);     // (not 0: a score that is not seen is -inf)
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     int n = 0, ends[2] = {0, 0}, joins = 0;             // tiles of this slot, units that each slot had a part in, and joined ones
-    while (walk.next(p, u)) {
+    while (ok && walk.next(p, u)) {
       const int count = u.last - u.first;
       const int turns = u.wide ? count : (count + 1 - slot) / 2;
       // ---- queries ----
@@ -443,18 +469,28 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
       const int rr = live ? row : u.row0;
       const int tok = rr / a.rep, hr = rr - tok * a.rep;
       if (u.wide || slot == 0) {
-        const __half* qp = a.q + (u.s.first + tok) * a.ld_q + (int64_t)(u.head * a.rep + hr) * D;
-        uint8_t* const q = smem + (u.wide ? slot * C::TILE_B : 0) + r * 128;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        // a warp's rows one after the other, a lane 8 dims of one
+        constexpr int CHUNKS = D / 8, AT_ONCE = 32 / CHUNKS;
+        const int64_t mine = (u.s.first + tok) * a.ld_q + (int64_t)(u.head * a.rep + hr) * D;
+        const uint32_t lives = __ballot_sync(0xffffffffu, live);
+        const int c = lane % CHUNKS;
+        uint8_t* const q = smem + (u.wide ? slot * C::TILE_B : 0) + (c / 8) * HALF_B;
+#pragma unroll 4
+        for (int i = 0; i < 32 / AT_ONCE; ++i) {
+          const int from = i * AT_ONCE + lane / CHUNKS, to = (warp & 3) * 32 + from;
+          const int64_t at = __shfl_sync(0xffffffffu, mine, from);
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (live) v = *reinterpret_cast<const uint4*>(qp + 8 * c);
+          if ((lives >> from) & 1) v = *reinterpret_cast<const uint4*>(a.q + at + 8 * c);
           // dims (0, 4), (1, 5), (2, 6), (3, 7)
           const uint4 o = make_uint4(prmt(v.x, v.z, 0x5410) ^ flip, prmt(v.x, v.z, 0x7632) ^ flip,
                                      prmt(v.y, v.w, 0x5410) ^ flip, prmt(v.y, v.w, 0x7632) ^ flip);
-          *reinterpret_cast<uint4*>(q + (c / 8) * HALF_B + (((c % 8) ^ (r & 7)) << 4)) = o;
+          *reinterpret_cast<uint4*>(q + to * 128 + (((c % 8) ^ (to & 7)) << 4)) = o;
         }
         fence_proxy_async_smem();
+      }
+      if (tid == 0) {
+        next_unit[0] = count;
+        next_unit[1] = u.wide;
       }
       tc_fence_before();
       __syncwarp();
@@ -477,51 +513,55 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
         if (!idle) {
           const int t = u.first + (u.wide ? i : 2 * i + slot), key0 = u.s.begin + t * KT;
           const bool masked = key0 + KT > base || key0 < all_begin;
-          uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int k0 = key0 + 32 * c;
-              // keys before the draft, from lo on
-              uint32_t v = 0;
-              if (k0 < base) {
-                v = base - k0 >= 32 ? 0xffffffffu : (1u << (base - k0)) - 1;
-                if (lo > k0) v = lo - k0 >= 32 ? 0 : v & ~((1u << (lo - k0)) - 1);
-              }
-              // drafted ones: bits from k0 - base on
-              const int j = k0 - base;
-              if (j > -32 && j < u.s.n) {
-                const uint64_t* bits = a.tree + token * a.words;
-                uint64_t d;
-                if (j < 0) {
-                  d = __ldg(bits) << -j;
-                } else {
-                  d = __ldg(bits + (j >> 6)) >> (j & 63);
-                  if ((j & 63) > 32 && (j >> 6) + 1 < a.words) d |= __ldg(bits + (j >> 6) + 1) << (64 - (j & 63));
-                }
-                uint32_t x = (uint32_t)d;
-                if (len - k0 < 32) x &= len > k0 ? (1u << (len - k0)) - 1 : 0;
-                v |= x;
-              }
-              vis[c] = depth > 0 ? v : 0;
+          // bit e: this row sees key 32 c + e of the tile
+          auto visible = [&](int c) -> uint32_t {
+            const int k0 = key0 + 32 * c, j = k0 - base;
+            uint32_t v = 0;
+            // keys before the draft, from lo on
+            if (j < 0) {
+              v = j <= -32 ? 0xffffffffu : (1u << -j) - 1;
+              if (lo > k0) v = lo - k0 >= 32 ? 0 : v & ~((1u << (lo - k0)) - 1);
             }
-          }
+            // drafted ones: bits from j on
+            if (j > -32 && j < u.s.n) {
+              const uint64_t* bits = a.tree + token * a.words;
+              uint64_t d;
+              if (j < 0) {
+                d = __ldg(bits) << -j;
+              } else {
+                d = __ldg(bits + (j >> 6)) >> (j & 63);
+                if ((j & 63) > 32 && (j >> 6) + 1 < a.words) d |= __ldg(bits + (j >> 6) + 1) << (64 - (j & 63));
+              }
+              uint32_t x = (uint32_t)d;
+              if (len - k0 < 32) x &= len > k0 ? (1u << (len - k0)) - 1 : 0;
+              v |= x;
+            }
+            return depth > 0 ? v : 0;
+          };
           // ---- the row's largest score ----
           float top = -INFINITY;
-          {
-            uint32_t x[32];
+          uint32_t x[2][16];
+          tmem_ld_32x32b_x16(s_at, x[0]);
+#pragma unroll 1
+          for (int c0 = 0; c0 < KT / 16; c0 += 4) {
 #pragma unroll
-            for (int c = 0; c < KT / 32; ++c) {
-              tmem_ld_32x32b_x32(s_at + 32 * c, x);
-              tmem_ld_wait_tied(x);
+            for (int h = 0; h < 4; ++h) {
+              const int c = c0 + h;
+              tmem_ld_wait_tied(x[h & 1]);
+              if (c + 1 < KT / 16) tmem_ld_32x32b_x16(s_at + 16 * (c + 1), x[(h + 1) & 1]);
               if (masked) {
+                const uint32_t v = visible(c >> 1) >> (16 * (h & 1));
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  top = fmaxf(top, (vis[c] >> e) & 1 ? __uint_as_float(x[e]) : -INFINITY);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
+                for (int e = 0; e < 16; ++e)
+                  if (!((v >> e) & 1)) x[h & 1][e] = 0xff800000u;
               }
+              float t2 = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                top = fmaxf(fmaxf(top, __uint_as_float(x[h & 1][e])), __uint_as_float(x[h & 1][e + 1]));
+                t2 = fmaxf(fmaxf(t2, __uint_as_float(x[h & 1][e + 2])), __uint_as_float(x[h & 1][e + 3]));
+              }
+              top = fmaxf(top, t2);
             }
           }
           top *= scale;
@@ -549,25 +589,34 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
           const float down = m == -INFINITY ? 0.0f : -m;
           P2 sum = p2(0.0f, 0.0f);
           const P2 c2 = p2(scale, scale), d2 = p2(down, down);
+          uint32_t w[2][16];
+          tmem_ld_32x32b_x16(s_at, x[0]);
+#pragma unroll 1
+          for (int c0 = 0; c0 < KT / 16; c0 += 4) {
 #pragma unroll
-          for (int c = 0; c < KT / 32; ++c) {
-            uint32_t x[32], w[16];
-            tmem_ld_32x32b_x32(s_at + 32 * c, x);
-            tmem_ld_wait_tied(x);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 y = f2(fma2(p2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, d2));
-              float e0 = ex2(y.x), e1 = ex2(y.y);
+            for (int h = 0; h < 4; ++h) {
+              const int c = c0 + h;
+              tmem_ld_wait_tied(x[h & 1]);
+              if (c + 1 < KT / 16) tmem_ld_32x32b_x16(s_at + 16 * (c + 1), x[(h + 1) & 1]);
               if (masked) {
-                if (!((vis[c] >> (2 * e)) & 1)) e0 = 0.0f;
-                if (!((vis[c] >> (2 * e + 1)) & 1)) e1 = 0.0f;
+                const uint32_t v = visible(c >> 1) >> (16 * (h & 1));
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (!((v >> e) & 1)) x[h & 1][e] = 0xff800000u;
               }
-              sum = add2(sum, p2(e0, e1));
-              w[e] = pack_h2(e0, e1);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t* const y2 = &x[h & 1][2 * e];
+                const float2 y = f2(fma2(p2(__uint_as_float(y2[0]), __uint_as_float(y2[1])), c2, d2));
+                const float e0 = ex2(y.x), e1 = ex2(y.y);
+                sum = add2(sum, p2(e0, e1));
+                w[h >> 1][8 * (h & 1) + e] = pack_h2(e0, e1);
+              }
+              // (the weights' columns lie before the scores still to be read)
+              if (h & 1) tmem_st_32x32b_x16(s_at + 16 * (c >> 1), w[h >> 1]);
             }
-            // (the weights' columns lie before the scores still to be read)
-            tmem_st_32x32b_x16(s_at + 16 * c, w);
-            tmem_st_wait_tied16(w);
+            tmem_st_wait_tied16(w[0]);
+            tmem_st_wait_tied16(w[1]);
           }
           const float2 s2 = f2(sum);
           l += s2.x + s2.y;
@@ -611,8 +660,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
       if (none) l = 0.0f;
       const float top = l == 0.0f || m == -INFINITY ? (l == l ? M_NONE : 0.0f) : m;
       const int64_t orow = token * (a.heads * a.rep) + u.head * a.rep + hr;
-      const int64_t part = 2 * (int64_t)blockIdx.x + (u.u0 + u.first != at0 ? 1 : 0);
-      float* const pr = whole ? nullptr : a.parts + (part * p.rows + (row - u.row0)) * (D + 4);
+      const int64_t part = 2 * (int64_t)blockIdx.x + (u.u0 + u.first != start.at ? 1 : 0);
+      // parts: [four dims][row][4], then the maxima and sums, so that a warp's stores are one stretch
+      float* const pr = a.parts + part * p.rows * (D + 4) + 4 * (row - u.row0);
       const float inv = inverse(l);
       if (!idle) {
         const int c0 = u.wide ? 0 : slot * (D / 64), c1 = u.wide ? D / 32 : c0 + D / 64;
@@ -642,17 +692,17 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
                 *reinterpret_cast<uint4*>(a.out + orow * D + 32 * c + 8 * g) = h;
               } else {
                 const bool zero = l == 0.0f;
-                float4* const d = reinterpret_cast<float4*>(pr + 32 * c + 8 * g);
-                d[0] = zero ? make_float4(0, 0, 0, 0) : make_float4(q[0], q[2], q[4], q[6]);
-                d[1] = zero ? make_float4(0, 0, 0, 0) : make_float4(q[1], q[3], q[5], q[7]);
+                float* const d = pr + (8 * c + 2 * g) * 4 * p.rows;
+                *reinterpret_cast<float4*>(d) = zero ? make_float4(0, 0, 0, 0) : make_float4(q[0], q[2], q[4], q[6]);
+                *reinterpret_cast<float4*>(d + 4 * p.rows) =
+                    zero ? make_float4(0, 0, 0, 0) : make_float4(q[1], q[3], q[5], q[7]);
               }
             }
           }
         }
         if (live && (u.wide || slot == 0)) {
           if (!whole) {
-            pr[D] = top;
-            pr[D + 1] = l;
+            *reinterpret_cast<float2*>(pr + D * p.rows - 2 * (row - u.row0)) = make_float2(top, l);
           } else if (a.lse) {
             a.lse[orow] = log_sum(top, l);
           }
@@ -661,11 +711,12 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
       if (u.first == 0 && tid == 0 && (!whole || a.by_unit)) {
         Meta mm{};
         if (!whole) {
+          const int64_t each = shares[0], extra = shares[1];
           const int64_t last = u.u0 + u.tiles - 1, big = (each + 1) * extra;
           const int64_t owner = last < big ? last / (each + 1) : extra + (last - big) / each;
           mm.parts = (int32_t)(owner - blockIdx.x + 1);
           mm.block = (int32_t)blockIdx.x;
-          mm.slot = u.u0 != at0 ? 1 : 0;
+          mm.slot = u.u0 != start.at ? 1 : 0;
           mm.head = u.head;
           mm.row0 = u.row0;
           mm.rows = u.rows;
@@ -674,6 +725,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
         const int qt = u.row0 / p.rows;
         a.meta[a.by_unit ? (u.b * a.qtiles + qt) * a.heads + u.head : (int64_t)blockIdx.x] = mm;
       }
+    }
+    if (ok) {
+      if (tid == 0) next_unit[0] = 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
     }
   }
 
@@ -685,10 +741,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
   }
 }
 
-// Joins a unit that fell into several blocks' ranges: a warp takes 128 / D rows at a time, a lane four dims of one.
+// Joins a unit that fell into several blocks' ranges: a lane has a row, a warp 8 of the dims.
 template <int D>
 __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p) {
-  constexpr int JS = D + 4, LANES = D / 4, ROWS = 256 / LANES;
   const AttnParams& a = p.a;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -698,48 +753,50 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p)
     if (qt >= load_seq(a, blockIdx.x / (a.heads * a.qtiles), p.rows).qtiles) return;
   }
   const Meta mm = a.meta[blockIdx.x];
-  const int n = mm.parts, d = (threadIdx.x % LANES) * 4;
-  if (n == 0) return;
-  for (int r = blockIdx.y * ROWS + threadIdx.x / LANES; r < mm.rows; r += gridDim.y * ROWS) {
-    auto part = [&](int i) {
-      return a.parts + ((2 * (int64_t)(mm.block + i) + (i == 0 ? mm.slot : 0)) * p.rows + r) * JS;
-    };
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float sum = 0.0f, mt = M_NONE;
-    for (int i = 0; i < n; i += 4) {
-      float4 x[4];
-      float2 ml[4];
+  const int n = mm.parts, r = (blockIdx.y / (D / 64)) * 32 + (threadIdx.x & 31);
+  const int d = ((blockIdx.y % (D / 64)) * 8 + (threadIdx.x >> 5)) * 8;
+  if (n == 0 || r >= mm.rows) return;
+  auto part = [&](int i) {
+    return a.parts + (2 * (int64_t)(mm.block + i) + (i == 0 ? mm.slot : 0)) * p.rows * (D + 4);
+  };
+  float v[8], sum = 0.0f, mt = M_NONE;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float* q = part(min(i + u, n - 1));
-        x[u] = *reinterpret_cast<const float4*>(q + d);
-        ml[u] = *reinterpret_cast<const float2*>(q + D);
-        if (i + u >= n) ml[u] = make_float2(M_NONE, 0.0f);
-      }
-      const float top = fmaxf(fmaxf(mt, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
-      const float f0 = ex2(mt - top);
-      mt = top;
-      v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
-      sum *= f0;
+  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+  for (int i = 0; i < n; i += 4) {
+    float4 x[4][2];
+    float2 ml[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (i + u >= n) break;
-        const float f = ex2(ml[u].x - top);
-        v.x = fmaf(f, x[u].x, v.x);
-        v.y = fmaf(f, x[u].y, v.y);
-        v.z = fmaf(f, x[u].z, v.z);
-        v.w = fmaf(f, x[u].w, v.w);
-        sum = fmaf(f, ml[u].y, sum);
-      }
+    for (int u = 0; u < 4; ++u) {
+      const float* q = part(min(i + u, n - 1));
+      x[u][0] = *reinterpret_cast<const float4*>(q + d * p.rows + 4 * r);
+      x[u][1] = *reinterpret_cast<const float4*>(q + (d + 4) * p.rows + 4 * r);
+      ml[u] = *reinterpret_cast<const float2*>(q + D * p.rows + 2 * r);
+      if (i + u >= n) ml[u] = make_float2(M_NONE, 0.0f);
     }
-    const int tok = (mm.row0 + r) / a.rep, hr = mm.row0 + r - tok * a.rep;
-    const int64_t orow = (mm.first + tok) * (int64_t)(a.heads * a.rep) + mm.head * a.rep + hr;
-    const float inv = inverse(sum);
-    uint2 h = make_uint2(pack_h2(v.x * inv, v.y * inv), pack_h2(v.z * inv, v.w * inv));
-    if (sum == 0.0f) h = make_uint2(0, 0);
-    *reinterpret_cast<uint2*>(a.out + orow * D + d) = h;
-    if (a.lse && d == 0) a.lse[orow] = log_sum(mt, sum);
+    const float top = fmaxf(fmaxf(mt, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+    const float f0 = ex2(mt - top);
+    mt = top;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= f0;
+    sum *= f0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (i + u >= n) break;
+      const float f = ex2(ml[u].x - top);
+      const float* y = reinterpret_cast<const float*>(x[u]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = fmaf(f, y[e], v[e]);
+      sum = fmaf(f, ml[u].y, sum);
+    }
   }
+  const int tok = (mm.row0 + r) / a.rep, hr = mm.row0 + r - tok * a.rep;
+  const int64_t orow = (mm.first + tok) * (int64_t)(a.heads * a.rep) + mm.head * a.rep + hr;
+  const float inv = inverse(sum);
+  uint4 h = make_uint4(pack_h2(v[0] * inv, v[1] * inv), pack_h2(v[2] * inv, v[3] * inv), pack_h2(v[4] * inv, v[5] * inv),
+                       pack_h2(v[6] * inv, v[7] * inv));
+  if (sum == 0.0f) h = make_uint4(0, 0, 0, 0);
+  *reinterpret_cast<uint4*>(a.out + orow * D + d) = h;
+  if (a.lse && d == 0) a.lse[orow] = log_sum(mt, sum);
 }
 
 inline int block_rows(int64_t rep, int64_t max_q) { return rep * max_q > SLOT_ROWS ? 2 * SLOT_ROWS : SLOT_ROWS; }
@@ -769,7 +826,7 @@ cudaError_t launch_both(const TreeParams& p, cudaStream_t stream) {
   e = launch_tree(kern, dim3((unsigned)grid), TREE_THREADS, C::SMEM, stream, p);
   if (e != cudaSuccess) return e;
   const int64_t units = p.a.B * p.a.qtiles * p.a.heads;
-  return launch_tree(attn_tree_join_kernel<D>, dim3((unsigned)(p.a.by_unit ? units : grid), (unsigned)(p.rows / 16)), 256, 0,
+  return launch_tree(attn_tree_join_kernel<D>, dim3((unsigned)(p.a.by_unit ? units : grid), (unsigned)(p.rows / 32 * (D / 64))), 256, 0,
                      stream, p);
 }
 
