@@ -35,8 +35,8 @@ constexpr int KT = 128;                     // keys of a tile
 constexpr int SLOT_ROWS = 128;
 constexpr int SOFT_WARPS = 8, LOAD_WARPS = 4;     // of both slots; of keys, and of values
 constexpr int MMA_WARP = SOFT_WARPS + 2 * LOAD_WARPS, TREE_WARPS = MMA_WARP + 4, TREE_THREADS = 32 * TREE_WARPS;
-// Registers of a thread, by warpgroup: 96 at the launch (5 * 96 = 480), then 128, 128, 88, 88 and 48.
-constexpr int SOFT_REGS = 128, LOAD_REGS = 80, MMA_REGS = 64;
+// Registers of a thread, by warpgroup: 96 at the launch (5 * 96 = 480), then 144, 144, 72, 72 and 48.
+constexpr int SOFT_REGS = 144, LOAD_REGS = 72, MMA_REGS = 48;
 constexpr int STAGES = 2;                   // tiles of keys, and of values, in shared memory
 constexpr int HALF_B = KT * 128;            // 64 dims of a tile
 constexpr uint64_t DRAIN_NS = 2000000000ull;
@@ -309,28 +309,29 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
       const int32_t* const trow = a.table + u.b * a.ld_table;
       const int len = u.s.len, base = len - u.s.n;
       const int first_seen = a.window > 0 ? (int)max((int64_t)0, (int64_t)base + 1 - a.window) : 0;
-      // a step's keys lie in one page (a page's 16 keys are never split)
-      int page[STEPS];
+      // The pages of 32 times 16 keys (four tiles) are a lane's each, and the next 32 are loaded with them: a load that
+      // waits its turn behind those of codes from memory takes as long as they do.  (A page's 16 keys are never split, so
+      // that a step's keys lie in one.)
+      const int last_key = min(u.last * KT + u.s.begin, len);      // keys from here on are not fetched
+      auto load_pages = [&](int t) {
+        const int key = u.s.begin + t * KT + lane * 16;
+        return key < last_key ? trow[key >> a.page_log2] : 0;
+      };
+      int pages = load_pages(u.first), next_pages = load_pages(u.first + 4);
+      const uint32_t unit_row = ((values ? a.heads : 0) + u.head) * P, page_rows = 2u * a.heads * P;
+      const uint8_t* const unit_codes = a.codes + (unit_row + key_lane) * (uint64_t)R + piece * 16;
+      const uint8_t* const unit_params = a.params + (unit_row + key_lane) * (uint64_t)(4 * NG) + par_at;
+      const uint32_t page_codes = page_rows * R, page_params = page_rows * 4 * NG;      // (below 2**32)
       uint4 codes[STEPS];
       uint32_t par[STEPS];
       const int key_first = u.s.begin + w * KEYS;       // of this warp's first step
-      const int last_key = u.last * KT + u.s.begin < len ? u.last * KT + u.s.begin : len;    // keys from here on are not fetched
       auto key_of_step = [&](int t, int i) { return key_first + t * KT + i * LOAD_WARPS * KEYS; };
-      auto fetch_page = [&](int t, int i) {
-        const int key = key_of_step(t, i);
-        page[i] = key < last_key ? trow[key >> a.page_log2] : 0;
-      };
-      const uint32_t unit_row = ((values ? a.heads : 0) + u.head) * P + key_lane, page_rows = 2u * a.heads * P;
-      const uint8_t* const unit_codes = a.codes + unit_row * (uint64_t)R + piece * 16;
-      const uint8_t* const unit_params = a.params + unit_row * (uint64_t)(4 * NG) + par_at;
-      const uint32_t page_codes = page_rows * R, page_params = page_rows * 4 * NG;      // (below 2**32)
       auto fetch_codes = [&](int t, int i) {
         const int key = key_of_step(t, i);
+        uint32_t at = __shfl_sync(0xffffffffu, pages, ((key - u.s.begin) / 16 - u.first * (KT / 16)) & 31);
         codes[i] = make_uint4(0, 0, 0, 0);
         par[i] = 0;
         if (key + key_lane < last_key) {
-          // (looked at a tile after its load, which nothing waits for till then)
-          uint32_t at = (uint32_t)page[i];
           if (at >= (uint64_t)a.num_pages) {
             record_error(a.status, BQ_ERR_INVALID_ARG);
             at = 0;
@@ -340,16 +341,29 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
           par[i] = *reinterpret_cast<const uint32_t*>(unit_params + (uint64_t)at * page_params + row * (4 * NG));
         }
       };
+      // brings this warp's quarter of a tile's codes and params to L2
+      auto prefetch = [&](int t, int from) {
+        constexpr int LINES = (KT / LOAD_WARPS) * R / 128;         // of codes: 32 keys' rows, in two blocks of 16
+        const int line = lane < LINES ? lane : 0;
+        const int key = u.s.begin + t * KT + w * (KT / LOAD_WARPS) + (lane < LINES ? line * 128 / R : (lane & 1) * 16);
+        const uint32_t at = __shfl_sync(0xffffffffu, from ? next_pages : pages,
+                                        ((key - u.s.begin) / 16 - u.first * (KT / 16)) & 31);
+        if (lane < LINES + 2 && key < last_key && at < (uint64_t)a.num_pages) {
+          const uint32_t row = key & (P - 1);
+          const uint8_t* const x = lane < LINES
+              ? a.codes + (uint64_t)at * page_codes + (uint64_t)(unit_row + row) * R + (line * 128) % R
+              : a.params + (uint64_t)at * page_params + (uint64_t)(unit_row + row) * (4 * NG);
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(x));
+        }
+      };
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i) fetch_page(u.first, i);
-#pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        fetch_codes(u.first, i);
-        fetch_page(u.first + 1, i);
-      }
+      for (int i = 0; i < STEPS; ++i) fetch_codes(u.first, i);
+      prefetch(u.first + 1, 0);
+      prefetch(u.first + 2, 0);
       bool marked = !values;                            // the drafted places that are seen are known
+#pragma unroll 1
       for (int t = u.first; t < u.last; ++t, ++n) {
-        const int stage = n % STAGES;
+        const int stage = n % STAGES, quarter = (t - u.first) & 3;
         const int tile0 = u.s.begin + t * KT;
         if (values && (tile0 + KT > base || tile0 < first_seen)) {
           // values at places that no node sees are zeros: their weights are 0, but they may be NaN
@@ -373,6 +387,12 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
             }
           }
         }
+        // two tiles ahead to L2, one to registers
+        prefetch(t + 3, quarter >= 1);
+        if (quarter == 3) {
+          pages = next_pages;
+          next_pages = load_pages(t + 5);
+        }
         if (!warp_wait(&empty[stage], ((n / STAGES) & 1) ^ 1, p.timeout_ns, a.status)) {
           ok = false;
           break;
@@ -382,7 +402,6 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
         for (int i = 0; i < STEPS; ++i) {
           store_values(to, stage * C::TILE_B + i * LOAD_WARPS * KEYS * 128, codes[i], par[i]);
           fetch_codes(t + 1, i);
-          fetch_page(t + 2, i);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -395,7 +414,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
     // ------------------------------------------------------------ products
     const uint32_t sb = smem_u32(smem);
     int n = 0, units = 0;                               // tiles and units so far
-    int weights[2] = {0, 0};                            // tiles whose weights were waited for, by slot
+    uint32_t turned = 0;                                // bit s: parity of the tiles whose weights were waited for in slot s
     for (;;) {
       if (!ok || !warp_wait(q_full, units & 1, p.timeout_ns, a.status)) break;
       ++units;
@@ -420,17 +439,20 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
         __syncwarp();
         return true;
       };
+#pragma unroll 1
       for (int s = 0; s < 2 && ok; ++s)
         if (tile_of(s, 0) < count) ok = scores(s, 0);
+#pragma unroll 1
       for (int i = 0; i < turns && ok; ++i)
+#pragma unroll 1
         for (int s = 0; s < 2 && ok; ++s) {
           const int mine = tile_of(s, i);
           if (mine >= count) continue;
           const int t = n + mine, stage = t % STAGES;
           if (!wide || s == 0) ok = warp_wait(&v_full[stage], (t / STAGES) & 1, p.timeout_ns, a.status);
-          ok = ok && warp_wait(&p_full[s], weights[s] & 1, p.timeout_ns, a.status);
+          ok = ok && warp_wait(&p_full[s], (turned >> s) & 1, p.timeout_ns, a.status);
           if (!ok) break;
-          ++weights[s];
+          turned ^= 1u << s;
           tc_fence_after();
           if (elect_one()) {
             issue_values<D>(C::O_COL + s * D, C::S_COL + s * KT, sb + C::OFF_V + stage * C::TILE_B, i > 0);
@@ -513,111 +535,102 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
         if (!idle) {
           const int t = u.first + (u.wide ? i : 2 * i + slot), key0 = u.s.begin + t * KT;
           const bool masked = key0 + KT > base || key0 < all_begin;
-          // bit e: this row sees key 32 c + e of the tile
-          auto visible = [&](int c) -> uint32_t {
-            const int k0 = key0 + 32 * c, j = k0 - base;
-            uint32_t v = 0;
-            // keys before the draft, from lo on
-            if (j < 0) {
-              v = j <= -32 ? 0xffffffffu : (1u << -j) - 1;
-              if (lo > k0) v = lo - k0 >= 32 ? 0 : v & ~((1u << (lo - k0)) - 1);
-            }
-            // drafted ones: bits from j on
-            if (j > -32 && j < u.s.n) {
-              const uint64_t* bits = a.tree + token * a.words;
-              uint64_t d;
-              if (j < 0) {
-                d = __ldg(bits) << -j;
-              } else {
-                d = __ldg(bits + (j >> 6)) >> (j & 63);
-                if ((j & 63) > 32 && (j >> 6) + 1 < a.words) d |= __ldg(bits + (j >> 6) + 1) << (64 - (j & 63));
-              }
-              uint32_t x = (uint32_t)d;
-              if (len - k0 < 32) x &= len > k0 ? (1u << (len - k0)) - 1 : 0;
-              v |= x;
-            }
-            return depth > 0 ? v : 0;
-          };
-          // ---- the row's largest score ----
-          float top = -INFINITY;
-          uint32_t x[2][16];
-          tmem_ld_32x32b_x16(s_at, x[0]);
+          if (masked) {
+            // scores that this row does not see become -inf, in their place
 #pragma unroll 1
-          for (int c0 = 0; c0 < KT / 16; c0 += 4) {
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const int c = c0 + h;
-              tmem_ld_wait_tied(x[h & 1]);
-              if (c + 1 < KT / 16) tmem_ld_32x32b_x16(s_at + 16 * (c + 1), x[(h + 1) & 1]);
-              if (masked) {
-                const uint32_t v = visible(c >> 1) >> (16 * (h & 1));
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (!((v >> e) & 1)) x[h & 1][e] = 0xff800000u;
+            for (int c = 0; c < KT / 16; ++c) {
+              const int k0 = key0 + 16 * c, j = k0 - base;
+              uint32_t v = 0;            // bit e: key k0 + e is seen
+              // keys before the draft, from lo on
+              if (j < 0) {
+                v = j <= -16 ? 0xffffu : (1u << -j) - 1;
+                if (lo > k0) v = lo - k0 >= 16 ? 0 : v & ~((1u << (lo - k0)) - 1);
               }
+              // drafted ones: bits from j on
+              if (j > -16 && j < u.s.n) {
+                const uint64_t* bits = a.tree + token * a.words;
+                uint64_t d;
+                if (j < 0) {
+                  d = __ldg(bits) << -j;
+                } else {
+                  d = __ldg(bits + (j >> 6)) >> (j & 63);
+                  if ((j & 63) > 48 && (j >> 6) + 1 < a.words) d |= __ldg(bits + (j >> 6) + 1) << (64 - (j & 63));
+                }
+                uint32_t x = (uint32_t)d;
+                if (len - k0 < 16) x &= len > k0 ? (1u << (len - k0)) - 1 : 0;
+                v |= x;
+              }
+              if (depth == 0) v = 0;
+              uint32_t x[16];
+              tmem_ld_32x32b_x16(s_at + 16 * c, x);
+              tmem_ld_wait_tied(x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (!((v >> e) & 1)) x[e] = 0xff800000u;
+              tmem_st_32x32b_x16(s_at + 16 * c, x);
+              tmem_st_wait_tied16(x);
+            }
+          }
+          // ---- weights by the running maximum, which is renewed only when it would rise by more than 2**8: the scores are
+          // still there then, and the weights are made again (always for a first tile) ----
+          uint32_t w[KT / 2];
+          P2 sum;
+          const P2 c2 = p2(scale, scale);
+          for (;;) {
+            const float down = m == -INFINITY ? 0.0f : -m;
+            const P2 d2 = p2(down, down);
+            float top = -INFINITY;
+            sum = p2(0.0f, 0.0f);
+            uint32_t x[2][16];
+            tmem_ld_32x32b_x16(s_at, x[0]);
+#pragma unroll
+            for (int c = 0; c < KT / 16; ++c) {
+              uint32_t(&y)[16] = x[c & 1];
+              tmem_ld_wait_tied(y);
+              if (c + 1 < KT / 16) tmem_ld_32x32b_x16(s_at + 16 * (c + 1), x[(c + 1) & 1]);
               float t2 = -INFINITY;
 #pragma unroll
               for (int e = 0; e < 16; e += 4) {
-                top = fmaxf(fmaxf(top, __uint_as_float(x[h & 1][e])), __uint_as_float(x[h & 1][e + 1]));
-                t2 = fmaxf(fmaxf(t2, __uint_as_float(x[h & 1][e + 2])), __uint_as_float(x[h & 1][e + 3]));
+                top = fmaxf(fmaxf(top, __uint_as_float(y[e])), __uint_as_float(y[e + 1]));
+                t2 = fmaxf(fmaxf(t2, __uint_as_float(y[e + 2])), __uint_as_float(y[e + 3]));
               }
               top = fmaxf(top, t2);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 z = f2(fma2(p2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), c2, d2));
+                const float e0 = ex2(z.x), e1 = ex2(z.y);
+                sum = add2(sum, p2(e0, e1));
+                w[8 * c + e] = pack_h2(e0, e1);
+              }
             }
-          }
-          top *= scale;
-          // the running maximum is renewed only when it would rise by more than 2**8
-          const bool renew = top > m + 8.0f;
-          if (__any_sync(0xffffffffu, renew)) {
+            top *= scale;
+            const bool renew = top > m + 8.0f;
+            if (!__any_sync(0xffffffffu, renew)) break;
             const float f = renew ? ex2(m - top) : 1.0f;
             if (renew) m = top;
             l *= f;
             if (i > 0) {
               // (the last tile's product is done: its commit came before these scores')
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t x[32];
-                tmem_ld_32x32b_x32(lanes + C::O_COL + slot * D + 32 * c, x);
-                tmem_ld_wait_tied(x);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                tmem_st_32x32b_x32(lanes + C::O_COL + slot * D + 32 * c, x);
-                tmem_st_wait_tied(x);
-              }
-            }
-          }
-          // ---- weights ----
-          const float down = m == -INFINITY ? 0.0f : -m;
-          P2 sum = p2(0.0f, 0.0f);
-          const P2 c2 = p2(scale, scale), d2 = p2(down, down);
-          uint32_t w[2][16];
-          tmem_ld_32x32b_x16(s_at, x[0]);
 #pragma unroll 1
-          for (int c0 = 0; c0 < KT / 16; c0 += 4) {
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(lanes + C::O_COL + slot * D + 16 * c, o);
+                tmem_ld_wait_tied(o);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const int c = c0 + h;
-              tmem_ld_wait_tied(x[h & 1]);
-              if (c + 1 < KT / 16) tmem_ld_32x32b_x16(s_at + 16 * (c + 1), x[(h + 1) & 1]);
-              if (masked) {
-                const uint32_t v = visible(c >> 1) >> (16 * (h & 1));
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (!((v >> e) & 1)) x[h & 1][e] = 0xff800000u;
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st_32x32b_x16(lanes + C::O_COL + slot * D + 16 * c, o);
+                tmem_st_wait_tied16(o);
               }
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const uint32_t* const y2 = &x[h & 1][2 * e];
-                const float2 y = f2(fma2(p2(__uint_as_float(y2[0]), __uint_as_float(y2[1])), c2, d2));
-                const float e0 = ex2(y.x), e1 = ex2(y.y);
-                sum = add2(sum, p2(e0, e1));
-                w[h >> 1][8 * (h & 1) + e] = pack_h2(e0, e1);
-              }
-              // (the weights' columns lie before the scores still to be read)
-              if (h & 1) tmem_st_32x32b_x16(s_at + 16 * (c >> 1), w[h >> 1]);
             }
-            tmem_st_wait_tied16(w[0]);
-            tmem_st_wait_tied16(w[1]);
           }
+          // (in the place of the scores)
+#pragma unroll
+          for (int c = 0; c < KT / 64; ++c) {
+            uint32_t(&y)[32] = *reinterpret_cast<uint32_t(*)[32]>(&w[32 * c]);
+            tmem_st_32x32b_x32(s_at + 32 * c, y);
+          }
+#pragma unroll
+          for (int c = 0; c < KT / 64; ++c) tmem_st_wait_tied(*reinterpret_cast<uint32_t(*)[32]>(&w[32 * c]));
           const float2 s2 = f2(sum);
           l += s2.x + s2.y;
         }
