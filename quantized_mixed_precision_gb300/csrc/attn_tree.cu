@@ -86,7 +86,7 @@ struct Walk {
       s = load_seq(a, ++b, p.rows);
     }
     const int tiles = seq_tiles(s);
-    const int unit = (int)((at - base) / tiles);
+    const int unit = (at - base) >> 32 ? (int)((at - base) / tiles) : (int)((uint32_t)(at - base) / (uint32_t)tiles);
     const int qt = unit / a.heads;
     u.s = s;
     u.b = b;
@@ -132,8 +132,10 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr) {
 }
 constexpr uint32_t IDESC_B_MN = 1u << 16;              // B is MN-major
 
+// (No memory clobber: what is stored is read by the tensor cores alone, behind a fence, and a step's loads and arithmetic may
+// move past the stores of the one before.)
 __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w));
 }
 
 // Four words of codes (32 dims of a key) as fp16 values: each is fp16_rne(low + step * code), as bq_qk_norm_rope_kv4 hands
@@ -251,14 +253,16 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
     __syncthreads();
     tc_fence_after();
     int64_t before = 0, total = 0;
+#pragma unroll
     for (int w = 0; w < TREE_WARPS; ++w) {
-      if (w < warp) before += scan[w];
-      total += scan[w];
+      const int64_t v = scan[w];
+      if (w < warp) before += v;
+      total += v;
     }
     inc += before;
     constexpr int64_t LEAST = 4;
     const int64_t blocks = max((int64_t)1, min((int64_t)gridDim.x, total / LEAST));
-    const int64_t each = total / blocks, extra = total % blocks;
+    const int64_t each = total >> 32 ? total / blocks : (uint32_t)total / (uint32_t)blocks, extra = total - each * blocks;
     const bool some = blockIdx.x < blocks;
     const int64_t at = some ? each * blockIdx.x + min((int64_t)blockIdx.x, extra) : total;
     const int64_t stop = some ? at + each + (blockIdx.x < extra ? 1 : 0) : total;
@@ -337,8 +341,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
             at = 0;
           }
           const uint32_t row = key & (P - 1);
-          codes[i] = *reinterpret_cast<const uint4*>(unit_codes + (uint64_t)at * page_codes + row * R);
-          par[i] = *reinterpret_cast<const uint32_t*>(unit_params + (uint64_t)at * page_params + row * (4 * NG));
+          codes[i] = __ldg(reinterpret_cast<const uint4*>(unit_codes + (uint64_t)at * page_codes + row * R));
+          par[i] = __ldg(reinterpret_cast<const uint32_t*>(unit_params + (uint64_t)at * page_params + row * (4 * NG)));
         }
       };
       // brings this warp's quarter of a tile's codes and params to L2
@@ -497,12 +501,12 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
         const uint32_t lives = __ballot_sync(0xffffffffu, live);
         const int c = lane % CHUNKS;
         uint8_t* const q = smem + (u.wide ? slot * C::TILE_B : 0) + (c / 8) * HALF_B;
-#pragma unroll 4
-        for (int i = 0; i < 32 / AT_ONCE; ++i) {
+#pragma unroll
+        for (int i = 0; i < 32 / AT_ONCE; ++i) {       // (all loads go out at once)
           const int from = i * AT_ONCE + lane / CHUNKS, to = (warp & 3) * 32 + from;
           const int64_t at = __shfl_sync(0xffffffffu, mine, from);
           uint4 v = make_uint4(0, 0, 0, 0);
-          if ((lives >> from) & 1) v = *reinterpret_cast<const uint4*>(a.q + at + 8 * c);
+          if ((lives >> from) & 1) v = __ldg(reinterpret_cast<const uint4*>(a.q + at + 8 * c));
           // dims (0, 4), (1, 5), (2, 6), (3, 7)
           const uint4 o = make_uint4(prmt(v.x, v.z, 0x5410) ^ flip, prmt(v.x, v.z, 0x7632) ^ flip,
                                      prmt(v.y, v.w, 0x5410) ^ flip, prmt(v.y, v.w, 0x7632) ^ flip);
@@ -754,10 +758,14 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
   }
 }
 
-// Joins a unit that fell into several blocks' ranges: a lane has a row, a warp 8 of the dims.
-template <int D>
+// Joins a unit that fell into several blocks' ranges.  A lane has a row, a warp 8 of its dims; with SHARE (few units, so that
+// there are many parts of each) all warps of a block the same 8 dims, and a share of the parts each.
+template <int D, bool SHARE>
 __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p) {
+  constexpr int WARPS = 8, GROUPS = SHARE ? D / 8 : D / 64;     // blocks of a unit's 32 rows
+  __shared__ float shared[SHARE ? WARPS : 1][10][32];
   const AttnParams& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.by_unit && a.cu_q) {
@@ -766,25 +774,28 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p)
     if (qt >= load_seq(a, blockIdx.x / (a.heads * a.qtiles), p.rows).qtiles) return;
   }
   const Meta mm = a.meta[blockIdx.x];
-  const int n = mm.parts, r = (blockIdx.y / (D / 64)) * 32 + (threadIdx.x & 31);
-  const int d = ((blockIdx.y % (D / 64)) * 8 + (threadIdx.x >> 5)) * 8;
-  if (n == 0 || r >= mm.rows) return;
+  const int n = mm.parts, r = (blockIdx.y / GROUPS) * 32 + lane;
+  const int d = ((blockIdx.y % GROUPS) * (SHARE ? 1 : WARPS) + (SHARE ? 0 : warp)) * 8;
+  if (n == 0 || r - lane >= mm.rows) return;
+  const bool live = r < mm.rows;
+  const int row = live ? r : mm.rows - 1;
   auto part = [&](int i) {
     return a.parts + (2 * (int64_t)(mm.block + i) + (i == 0 ? mm.slot : 0)) * p.rows * (D + 4);
   };
   float v[8], sum = 0.0f, mt = M_NONE;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-  for (int i = 0; i < n; i += 4) {
+  constexpr int BY = SHARE ? WARPS : 1;
+  for (int i = SHARE ? warp : 0; i < n; i += 4 * BY) {
     float4 x[4][2];
     float2 ml[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const float* q = part(min(i + u, n - 1));
-      x[u][0] = *reinterpret_cast<const float4*>(q + d * p.rows + 4 * r);
-      x[u][1] = *reinterpret_cast<const float4*>(q + (d + 4) * p.rows + 4 * r);
-      ml[u] = *reinterpret_cast<const float2*>(q + D * p.rows + 2 * r);
-      if (i + u >= n) ml[u] = make_float2(M_NONE, 0.0f);
+      const float* q = part(min(i + u * BY, n - 1));
+      x[u][0] = *reinterpret_cast<const float4*>(q + d * p.rows + 4 * row);
+      x[u][1] = *reinterpret_cast<const float4*>(q + (d + 4) * p.rows + 4 * row);
+      ml[u] = *reinterpret_cast<const float2*>(q + D * p.rows + 2 * row);
+      if (i + u * BY >= n) ml[u] = make_float2(M_NONE, 0.0f);
     }
     const float top = fmaxf(fmaxf(mt, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
     const float f0 = ex2(mt - top);
@@ -794,7 +805,7 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p)
     sum *= f0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      if (i + u >= n) break;
+      if (i + u * BY >= n) break;
       const float f = ex2(ml[u].x - top);
       const float* y = reinterpret_cast<const float*>(x[u]);
 #pragma unroll
@@ -802,6 +813,27 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p)
       sum = fmaf(f, ml[u].y, sum);
     }
   }
+  if constexpr (SHARE) {
+    // the warps' shares, in order
+#pragma unroll
+    for (int e = 0; e < 8; ++e) shared[warp][e][lane] = v[e];
+    shared[warp][8][lane] = mt;
+    shared[warp][9][lane] = sum;
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 0; w < WARPS; ++w) mt = fmaxf(mt, shared[w][8][lane]);
+    sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = w < n ? ex2(shared[w][8][lane] - mt) : 0.0f;
+      sum = fmaf(f, shared[w][9][lane], sum);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = fmaf(f, shared[w][e][lane], v[e]);
+    }
+  }
+  if (!live) return;
   const int tok = (mm.row0 + r) / a.rep, hr = mm.row0 + r - tok * a.rep;
   const int64_t orow = (mm.first + tok) * (int64_t)(a.heads * a.rep) + mm.head * a.rep + hr;
   const float inv = inverse(sum);
@@ -839,8 +871,12 @@ cudaError_t launch_both(const TreeParams& p, cudaStream_t stream) {
   e = launch_tree(kern, dim3((unsigned)grid), TREE_THREADS, C::SMEM, stream, p);
   if (e != cudaSuccess) return e;
   const int64_t units = p.a.B * p.a.qtiles * p.a.heads;
-  return launch_tree(attn_tree_join_kernel<D>, dim3((unsigned)(p.a.by_unit ? units : grid), (unsigned)(p.rows / 32 * (D / 64))), 256, 0,
-                     stream, p);
+  // (a unit has some grid / units parts)
+  if (units <= grid / 4)
+    return launch_tree(attn_tree_join_kernel<D, true>, dim3((unsigned)units, (unsigned)(p.rows / 32 * (D / 8))), 256, 0, stream,
+                       p);
+  return launch_tree(attn_tree_join_kernel<D, false>,
+                     dim3((unsigned)(p.a.by_unit ? units : grid), (unsigned)(p.rows / 32 * (D / 64))), 256, 0, stream, p);
 }
 
 }  // namespace
