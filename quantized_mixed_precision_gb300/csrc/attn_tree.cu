@@ -321,7 +321,13 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
         const int key = u.s.begin + t * KT + lane * 16;
         return key < last_key ? trow[key >> a.page_log2] : 0;
       };
+      auto checked = [&](int page) {       // (when it is needed, long after its load)
+        if ((uint32_t)page < (uint64_t)a.num_pages || last_key == 0) return page;
+        record_error(a.status, BQ_ERR_INVALID_ARG);
+        return 0;
+      };
       int pages = load_pages(u.first), next_pages = load_pages(u.first + 4);
+      pages = checked(pages);
       const uint32_t unit_row = ((values ? a.heads : 0) + u.head) * P, page_rows = 2u * a.heads * P;
       const uint8_t* const unit_codes = a.codes + (unit_row + key_lane) * (uint64_t)R + piece * 16;
       const uint8_t* const unit_params = a.params + (unit_row + key_lane) * (uint64_t)(4 * NG) + par_at;
@@ -332,42 +338,21 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
       auto key_of_step = [&](int t, int i) { return key_first + t * KT + i * LOAD_WARPS * KEYS; };
       auto fetch_codes = [&](int t, int i) {
         const int key = key_of_step(t, i);
-        uint32_t at = __shfl_sync(0xffffffffu, pages, ((key - u.s.begin) / 16 - u.first * (KT / 16)) & 31);
+        const uint32_t at = __shfl_sync(0xffffffffu, pages, ((key - u.s.begin) / 16 - u.first * (KT / 16)) & 31);
         codes[i] = make_uint4(0, 0, 0, 0);
         par[i] = 0;
         if (key + key_lane < last_key) {
-          if (at >= (uint64_t)a.num_pages) {
-            record_error(a.status, BQ_ERR_INVALID_ARG);
-            at = 0;
-          }
           const uint32_t row = key & (P - 1);
           codes[i] = __ldg(reinterpret_cast<const uint4*>(unit_codes + (uint64_t)at * page_codes + row * R));
           par[i] = __ldg(reinterpret_cast<const uint32_t*>(unit_params + (uint64_t)at * page_params + row * (4 * NG)));
         }
       };
-      // brings this warp's quarter of a tile's codes and params to L2
-      auto prefetch = [&](int t, int from) {
-        constexpr int LINES = (KT / LOAD_WARPS) * R / 128;         // of codes: 32 keys' rows, in two blocks of 16
-        const int line = lane < LINES ? lane : 0;
-        const int key = u.s.begin + t * KT + w * (KT / LOAD_WARPS) + (lane < LINES ? line * 128 / R : (lane & 1) * 16);
-        const uint32_t at = __shfl_sync(0xffffffffu, from ? next_pages : pages,
-                                        ((key - u.s.begin) / 16 - u.first * (KT / 16)) & 31);
-        if (lane < LINES + 2 && key < last_key && at < (uint64_t)a.num_pages) {
-          const uint32_t row = key & (P - 1);
-          const uint8_t* const x = lane < LINES
-              ? a.codes + (uint64_t)at * page_codes + (uint64_t)(unit_row + row) * R + (line * 128) % R
-              : a.params + (uint64_t)at * page_params + (uint64_t)(unit_row + row) * (4 * NG);
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(x));
-        }
-      };
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) fetch_codes(u.first, i);
-      prefetch(u.first + 1, 0);
-      prefetch(u.first + 2, 0);
       bool marked = !values;                            // the drafted places that are seen are known
 #pragma unroll 1
       for (int t = u.first; t < u.last; ++t, ++n) {
-        const int stage = n % STAGES, quarter = (t - u.first) & 3;
+        const int stage = n % STAGES;
         const int tile0 = u.s.begin + t * KT;
         if (values && (tile0 + KT > base || tile0 < first_seen)) {
           // values at places that no node sees are zeros: their weights are 0, but they may be NaN
@@ -391,10 +376,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
             }
           }
         }
-        // two tiles ahead to L2, one to registers
-        prefetch(t + 3, quarter >= 1);
-        if (quarter == 3) {
-          pages = next_pages;
+        if (((t - u.first) & 3) == 3) {
+          pages = checked(next_pages);
           next_pages = load_pages(t + 5);
         }
         if (!warp_wait(&empty[stage], ((n / STAGES) & 1) ^ 1, p.timeout_ns, a.status)) {

@@ -1,5 +1,5 @@
-// Native form of the decoder-layer binding (decode.py): checks the tensors of
-// a call, allocates its outputs and makes the C call, in about a microsecond
+// Native form of the decoder-layer binding (decode.py) and of that of the
+// operators on drafted tokens (draft.py): checks the tensors of a call, allocates its outputs and makes the C call, in about a microsecond
 // besides the launch.  A decode step makes these calls for every layer, with
 // kernels of a few microseconds, so that the interpreter's part of a call
 // (10 to 20 us for its dozens of attribute reads) would set their rate.
@@ -21,6 +21,7 @@
 #include <exception>
 
 #include "bq_decode.h"
+#include "bq_draft.h"
 
 namespace {
 
@@ -28,6 +29,10 @@ decltype(&bq_gemm_f16xi4_group) f_gemm = nullptr;
 decltype(&bq_qk_norm_rope_kv4) f_write = nullptr;
 decltype(&bq_attn_kv4) f_attn = nullptr;
 decltype(&bq_attn_kv4_workspace) f_workspace = nullptr;
+decltype(&bq_attn_kv4_tree) f_tree = nullptr;
+decltype(&bq_attn_kv4_tree_workspace) f_tree_workspace = nullptr;
+decltype(&bq_sample) f_sample = nullptr;
+decltype(&bq_kv4_accept) f_accept = nullptr;
 
 // A CUDA tensor argument, or null.
 inline const at::Tensor* tensor(PyObject* o) {
@@ -261,6 +266,194 @@ PyObject* py_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CATCH_ALL
 }
 
+// ---- operators on drafted tokens (draft.py) ----
+
+inline const uint64_t* u64(const at::Tensor* t) { return static_cast<const uint64_t*>(t->data_ptr()); }
+
+// (q, codes, params, block_table, seq_lens, tree, cu_q, max_q, max_len, scale, window, lse, workspace); None where absent
+PyObject* py_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  try {
+    if (n != 13 || !f_tree || !f_tree_workspace) Py_RETURN_NONE;
+    const at::Tensor* q = tensor(a[0]);
+    if (!q || q->dim() != 3 || q->scalar_type() != at::kHalf) Py_RETURN_NONE;
+    const int dev = q->get_device();
+    const int64_t T = q->size(0), hq = q->size(1), D = q->size(2);
+    Pool p;
+    const at::Tensor *table = tensor(a[3]), *lens = tensor(a[4]), *tree = tensor(a[5]), *cu = nullptr;
+    if (!pool(a[1], a[2], D, dev, p) || !whole(table, at::kInt, 2, dev) || !whole(tree, at::kLong, 2, dev))
+      Py_RETURN_NONE;
+    const int64_t B = table->size(0), width = table->size(1), words = tree->size(1);
+    int64_t max_q, max_len = width * p.page, window;
+    if (tree->size(0) != T || B < 1 || !shaped(lens, at::kInt, dev, B) || !integer(a[10], window)) Py_RETURN_NONE;
+    if (a[6] != Py_None) {
+      if (!shaped(cu = tensor(a[6]), at::kInt, dev, B + 1)) Py_RETURN_NONE;
+      max_q = T < 64 * words ? T : 64 * words;
+    } else {
+      if (T % B != 0) Py_RETURN_NONE;
+      max_q = T / B;
+    }
+    if (a[7] != Py_None && (!integer(a[7], max_q) || (!cu && max_q < T / B))) Py_RETURN_NONE;
+    if (a[8] != Py_None && (!integer(a[8], max_len) || max_len > width * p.page)) Py_RETURN_NONE;
+    double scale;
+    if (a[9] == Py_None)
+      scale = 1.0 / std::sqrt((double)D);
+    else if (PyFloat_Check(a[9]))
+      scale = PyFloat_AS_DOUBLE(a[9]);
+    else
+      Py_RETURN_NONE;
+    const int64_t ldq = row_stride(*q);
+    const int lse = PyObject_IsTrue(a[11]);
+    if (ldq < 0 || lse < 0) {
+      PyErr_Clear();
+      Py_RETURN_NONE;
+    }
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(dev));
+    at::Tensor out = fresh({T, hq, D}, *q, at::kHalf), logs, own;
+    if (lse) logs = fresh({T, hq}, *q, at::kFloat);
+    void* ws = nullptr;
+    size_t bytes = 0;
+    if (a[12] == Py_None) {
+      bytes = f_tree_workspace(B, hq, p.heads, D, max_q, max_len);
+      if (bytes) {
+        own = fresh({(int64_t)bytes}, *q, at::kByte);
+        ws = own.data_ptr();
+      }
+    } else {
+      const at::Tensor* w = tensor(a[12]);
+      if (!whole(w, at::kByte, 1, dev)) Py_RETURN_NONE;
+      ws = w->data_ptr();
+      bytes = (size_t)w->numel();
+    }
+    const bq_status st =
+        f_tree(u16(q), ldq, T, hq, p.heads, D, static_cast<const uint8_t*>(p.codes->data_ptr()), u16(p.params), p.pages,
+               p.page, p.group, i32(table), width, i32(lens), u64(tree), words, i32(cu), B, max_q, max_len, (float)scale,
+               window, static_cast<uint16_t*>(out.data_ptr()), lse ? static_cast<float*>(logs.data_ptr()) : nullptr, ws,
+               bytes, raw_stream(dev));
+    if (st != BQ_OK) return PyLong_FromLong(st);
+    PyObject* r = PyTuple_New(2);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(out)));
+    PyTuple_SET_ITEM(r, 1, lse ? THPVariable_Wrap(std::move(logs)) : Py_NewRef(Py_None));
+    return r;
+  }
+  CATCH_ALL
+}
+
+// An optional tensor (size) of the given type: false where it is there and is something else.
+inline bool optional(PyObject* o, at::ScalarType type, int dev, int64_t size, const at::Tensor*& t) {
+  t = nullptr;
+  return o == Py_None || shaped(t = tensor(o), type, dev, size);
+}
+
+// (logits, u, temperature, top_k, top_p, min_p, logprob); None where absent
+PyObject* py_sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  try {
+    if (n != 7 || !f_sample) Py_RETURN_NONE;
+    const at::Tensor *x = tensor(a[0]), *u = tensor(a[1]);
+    if (!x || x->dim() != 2) Py_RETURN_NONE;
+    const at::ScalarType t = x->scalar_type();
+    if (t != at::kHalf && t != at::kFloat && t != at::kBFloat16) Py_RETURN_NONE;
+    const int type = t == at::kHalf ? BQ_LOGITS_F16 : (t == at::kFloat ? BQ_LOGITS_F32 : BQ_LOGITS_BF16);
+    const int dev = x->get_device();
+    const int64_t R = x->size(0), V = x->size(1);
+    int64_t ld = V;
+    if (!x->is_contiguous()) {
+      if (V < 1 || R < 2 || x->stride(1) != 1 || x->stride(0) < V) Py_RETURN_NONE;
+      ld = x->stride(0);
+    }
+    const at::Tensor *heat, *k, *p, *m;
+    if (!shaped(u, at::kFloat, dev, R) || !optional(a[2], at::kFloat, dev, R, heat) ||
+        !optional(a[3], at::kInt, dev, R, k) || !optional(a[4], at::kFloat, dev, R, p) ||
+        !optional(a[5], at::kFloat, dev, R, m))
+      Py_RETURN_NONE;
+    const int logprob = PyObject_IsTrue(a[6]);
+    if (logprob < 0) {
+      PyErr_Clear();
+      Py_RETURN_NONE;
+    }
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(dev));
+    at::Tensor out = fresh({R}, *x, at::kInt), logs;
+    if (logprob) logs = fresh({R}, *x, at::kFloat);
+    const bq_status st = f_sample(x->data_ptr(), type, R, V, ld, f32(u), f32(heat), i32(k), f32(p), f32(m),
+                                  static_cast<int32_t*>(out.data_ptr()),
+                                  logprob ? static_cast<float*>(logs.data_ptr()) : nullptr, raw_stream(dev));
+    if (st != BQ_OK) return PyLong_FromLong(st);
+    PyObject* r = PyTuple_New(2);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(out)));
+    PyTuple_SET_ITEM(r, 1, logprob ? THPVariable_Wrap(std::move(logs)) : Py_NewRef(Py_None));
+    return r;
+  }
+  CATCH_ALL
+}
+
+// (tokens, targets, tree, codes, params, block_table, seq_lens, cu_q, max_q); None where absent
+PyObject* py_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  try {
+    if (n != 9 || !f_accept) Py_RETURN_NONE;
+    const at::Tensor *tokens = tensor(a[0]), *targets = tensor(a[1]), *tree = tensor(a[2]), *codes = tensor(a[3]),
+                     *params = tensor(a[4]), *table = tensor(a[5]), *lens = tensor(a[6]), *cu = nullptr;
+    if (!tokens || tokens->dim() != 1 || !codes || (codes->dim() != 5 && codes->dim() != 6)) Py_RETURN_NONE;
+    const int dev = tokens->get_device();
+    const int64_t T = tokens->size(0), at = codes->dim() - 5, layers = at ? codes->size(0) : 1;
+    if (!shaped(tokens, at::kInt, dev, T) || !shaped(targets, at::kInt, dev, T) || !whole(tree, at::kLong, 2, dev) ||
+        !whole(codes, at::kByte, 5 + at, dev) || !whole(params, at::kHalf, 6 + at, dev) || !whole(table, at::kInt, 2, dev))
+      Py_RETURN_NONE;
+    const int64_t pages = codes->size(at), heads = codes->size(at + 2), page = codes->size(at + 3),
+                  D = 2 * codes->size(at + 4), groups = params->size(at + 4);
+    if (codes->size(at + 1) != 2 || groups < 1 || D % groups != 0 || params->size(at) != pages ||
+        params->size(at + 1) != 2 || params->size(at + 2) != heads || params->size(at + 3) != page ||
+        params->size(at + 5) != 2 || (at && params->size(0) != layers))
+      Py_RETURN_NONE;
+    const int64_t B = table->size(0), width = table->size(1), words = tree->size(1);
+    if (B < 1 || tree->size(0) != T || !shaped(lens, at::kInt, dev, B)) Py_RETURN_NONE;
+    int64_t max_q;
+    if (a[7] != Py_None) {
+      if (!shaped(cu = tensor(a[7]), at::kInt, dev, B + 1)) Py_RETURN_NONE;
+      max_q = T < 64 * words ? T : 64 * words;
+    } else {
+      if (T % B != 0) Py_RETURN_NONE;
+      max_q = T / B;
+    }
+    if (a[8] != Py_None && (!integer(a[8], max_q) || max_q < 0 || (!cu && max_q < T / B))) Py_RETURN_NONE;
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(dev));
+    at::Tensor path = fresh({B, max_q}, *tokens, at::kInt), accepted = fresh({B}, *tokens, at::kInt),
+               last = fresh({B}, *tokens, at::kInt), now = fresh({B}, *tokens, at::kInt);
+    const bq_status st = f_accept(
+        i32(tokens), i32(targets), u64(tree), words, T, i32(cu), B, max_q, i32(table), width, i32(lens), width * page,
+        static_cast<uint8_t*>(codes->data_ptr()), static_cast<uint16_t*>(params->data_ptr()), layers, pages, heads, page, D,
+        D / groups, static_cast<int32_t*>(path.data_ptr()), static_cast<int32_t*>(accepted.data_ptr()),
+        static_cast<int32_t*>(last.data_ptr()), static_cast<int32_t*>(now.data_ptr()), raw_stream(dev));
+    if (st != BQ_OK) return PyLong_FromLong(st);
+    PyObject* r = PyTuple_New(4);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(path)));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(accepted)));
+    PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(std::move(last)));
+    PyTuple_SET_ITEM(r, 3, THPVariable_Wrap(std::move(now)));
+    return r;
+  }
+  CATCH_ALL
+}
+
+// (addresses of bq_attn_kv4_tree, bq_attn_kv4_tree_workspace, bq_sample, bq_kv4_accept)
+PyObject* py_bind_draft(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 4) {
+    PyErr_SetString(PyExc_TypeError, "bind_draft takes four addresses");
+    return nullptr;
+  }
+  void* p[4];
+  for (int i = 0; i < 4; ++i) {
+    p[i] = PyLong_AsVoidPtr(a[i]);
+    if (!p[i] && PyErr_Occurred()) return nullptr;
+  }
+  f_tree = reinterpret_cast<decltype(f_tree)>(p[0]);
+  f_tree_workspace = reinterpret_cast<decltype(f_tree_workspace)>(p[1]);
+  f_sample = reinterpret_cast<decltype(f_sample)>(p[2]);
+  f_accept = reinterpret_cast<decltype(f_accept)>(p[3]);
+  Py_RETURN_NONE;
+}
+
 // (addresses of bq_gemm_f16xi4_group, bq_qk_norm_rope_kv4, bq_attn_kv4, bq_attn_kv4_workspace)
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 4) {
@@ -284,6 +477,10 @@ PyMethodDef methods[] = {
     {"write", reinterpret_cast<PyCFunction>(py_write), METH_FASTCALL, nullptr},
     {"attn", reinterpret_cast<PyCFunction>(py_attn), METH_FASTCALL, nullptr},
     {"bind", reinterpret_cast<PyCFunction>(py_bind), METH_FASTCALL, nullptr},
+    {"tree", reinterpret_cast<PyCFunction>(py_tree), METH_FASTCALL, nullptr},
+    {"sample", reinterpret_cast<PyCFunction>(py_sample), METH_FASTCALL, nullptr},
+    {"accept", reinterpret_cast<PyCFunction>(py_accept), METH_FASTCALL, nullptr},
+    {"bind_draft", reinterpret_cast<PyCFunction>(py_bind_draft), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

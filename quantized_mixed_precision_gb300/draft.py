@@ -3,7 +3,9 @@
 A step that checks a tree of drafted tokens on the 4-bit cache writes their keys and values (``bq_qk_norm_rope_kv4``),
 attends with ``bq_attn_kv4_tree``, chooses a token at every node with ``bq_sample`` and keeps the longest branch that the
 choices confirm with ``bq_kv4_accept``.  The calls are bound like those of decode.py: argument checks, device pointers
-and the current CUDA stream, ``BqError`` on a non-OK status; with ``stream`` a call allocates and runs on that stream.
+and the current CUDA stream, ``BqError`` on a non-OK status; a plain call (no ``out``, no ``stream``) goes through
+csrc/decode_binding.cpp, which returns None for what it does not take as it is; with ``stream`` a call allocates and runs
+on that stream.
 
 A tree is an int64 tensor (T, words), one row a drafted token: bit j % 64 of word j // 64 says that the token sees token j
 of its sequence, its ancestors and itself.  A row of zeros is padding.
@@ -29,6 +31,11 @@ SIGNATURES = {
 }
 
 
+class _NoNative:
+    """Leaves every call to the code here, at 20 to 40 us of host time a call."""
+    tree = sample = accept = staticmethod(lambda *args: None)
+
+
 class _Bound:
     """What every call needs, looked up once."""
 
@@ -45,6 +52,14 @@ class _Bound:
         self.raw_stream, self.device_now = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
         self.attn, self.workspace = lib.bq_attn_kv4_tree, lib.bq_attn_kv4_tree_workspace
         self.sample, self.accept = lib.bq_sample, lib.bq_kv4_accept
+        try:
+            from . import _decode_binding as native
+            bind = native.bind_draft
+        except (ImportError, AttributeError):      # not built, or built for another torch
+            self.native = _NoNative
+        else:
+            bind(*(ctypes.cast(f, _vp).value for f in (self.attn, self.workspace, self.sample, self.accept)))
+            self.native = native
 
 
 _bound = None
@@ -103,6 +118,10 @@ def bq_attn_kv4_tree(q, codes, params, block_table, seq_lens, tree, cu_q=None, m
     bits always.  Other arguments as in bq_attn_kv4; ``max_q`` bounds a sequence's drafted tokens (None: all of q's with
     cu_q, up to what the tree's words hold)."""
     b = _bound or _load()
+    if out is None and stream is None:
+        r = b.native.tree(q, codes, params, block_table, seq_lens, tree, cu_q, max_q, max_len, scale, window, lse, workspace)
+        if r is not None:
+            return r if type(r) is not int else b.bq._check(r, "bq_attn_kv4_tree")
     f16 = b.f16
     _need(q, f16, "q", 3)
     dev = q.get_device()
@@ -152,6 +171,10 @@ def bq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, l
     logit; ``logprob`` is the logarithm of the token's share of what the filters kept.  Rows may be apart by more than
     V."""
     b = _bound or _load()
+    if out is None and stream is None:
+        r = b.native.sample(logits, u, temperature, top_k, top_p, min_p, logprob)
+        if r is not None:
+            return r if type(r) is not int else b.bq._check(r, "bq_sample")
     torch = b.torch
     if not isinstance(logits, torch.Tensor) or logits.dtype not in b.logits:
         raise TypeError("logits must be a CUDA tensor of fp16, bf16 or fp32")
@@ -197,6 +220,10 @@ def bq_kv4_accept(tokens, targets, tree, codes, params, block_table, seq_lens, c
     (5 and 6 dims) or those of all layers (6 and 7 dims, layers first); the drafted places' pages belong to one
     sequence each."""
     b = _bound or _load()
+    if stream is None:
+        r = b.native.accept(tokens, targets, tree, codes, params, block_table, seq_lens, cu_q, max_q)
+        if r is not None:
+            return r if type(r) is not int else b.bq._check(r, "bq_kv4_accept")
     i32 = b.i32
     _need(tokens, i32, "tokens", 1)
     dev = tokens.get_device()
