@@ -26,6 +26,7 @@
 
 #include "bq_device.cuh"
 #include "draft_internal.h"
+#include "kv4_device.cuh"
 
 namespace bq {
 
@@ -37,6 +38,10 @@ constexpr float Y_MOST = FRAC + 2.0f;        // from here on a weight is 0
 constexpr int BINS = 2048, EACH = BINS / THREADS;
 constexpr int LIST = 2048;                   // gathered tokens
 constexpr int QUEUE = 32 * 9;                // of a warp: a step of 8 elements a lane, and less than 32 before it
+// Up to so many first tokens, those are gathered, and the other filters and the choice are made among them alone.  That and a
+// second pass over the row, with top-p: 1 x 50021 fp32 at 50 tokens 26.5 and 36.9 us, 200 34 and 39, 400 42 and 39; 64 x
+// 131072 fp16 at 50 42 and 60, 200 52 and 62, 400 62 and 65, 1000 98 and 68.
+constexpr int FEW = 256;
 constexpr int MOST_BLOCKS = 8;
 
 // Keys of fp32 values: unsigned integers of the same order.
@@ -112,6 +117,42 @@ __device__ __forceinline__ uint64_t weight(float x, const Scale& s, const Table&
   return (uint64_t)m >> (60 - FRAC + n);
 }
 
+// The same for two tokens at once, summed: packed fp32 for all but the integers.  Nothing is decided on the way: a logit that
+// counts for nothing (-inf, NaN, 46 binary orders below the largest) has y = 47, whose weight is shifted out.
+template <bool WIDE>
+__device__ __forceinline__ uint64_t weights2(float x0, float x1, const Scale& s, const Table& t) {
+  const P2 top = p2(s.top, s.top), c = p2(s.c_hi, s.c_hi), one = p2(-1.0f, -1.0f), x = p2(x0, x1);
+  const P2 hi = fma2(x, one, top);                              // (exact products: ordinary differences)
+  const float2 y = f2(mul2(hi, c));
+  const P2 p = p2(fminf(y.x, FRAC + 3.0f), fminf(y.y, FRAC + 3.0f));
+  const P2 minus = fma2(p, one, p2(-0.0f, -0.0f));
+  P2 e = fma2(hi, c, minus);
+  e = fma2(hi, p2(s.c_lo, s.c_lo), e);
+  if constexpr (WIDE) {
+    const P2 b = fma2(hi, one, top);
+    const P2 lo = add2(fma2(add2(b, hi), one, top), fma2(x, one, b));
+    e = fma2(lo, c, e);
+  }
+  constexpr float NEAREST = 393216.0f + 16.0f;                  // ulp 1 / 32; 16 of the shift below with it
+  const P2 a = add2(p, p2(NEAREST, NEAREST));
+  const P2 r = fma2(e, one, add2(add2(a, p2(-NEAREST, -NEAREST)), minus));
+  const float2 af = f2(a);
+  const uint32_t a0 = __float_as_uint(af.x), a1 = __float_as_uint(af.y);
+  P2 d = fma2(r, p2(0.0096181291f, 0.0096181291f), p2(0.055504109f, 0.055504109f));
+  d = fma2(r, d, p2(0.24022651f, 0.24022651f));
+  d = fma2(r, d, p2(0.69314718f, 0.69314718f));
+  d = mul2(r, d);
+  constexpr float WHOLE = 12582912.0f;
+  const P2 v = mul2(d, p2(t.value[a0 & 31], t.value[a1 & 31]));
+  const float2 q = f2(fma2(v, p2(268435456.0f, 268435456.0f), p2(WHOLE, WHOLE)));
+  // (where y was cut to 47, e is what was cut off, and what becomes of it does not matter)
+  auto one_of = [&](uint32_t a, float q, float y) {
+    const int64_t m = (int64_t)t.fixed[a & 31] + ((int64_t)(__float_as_int(q) - __float_as_int(WHOLE)) << 32);
+    return y < FRAC + 2.0f ? (uint64_t)m >> ((a >> 5) & 63) : 0;
+  };
+  return one_of(a0, q.x, y.x) + one_of(a1, q.y, y.y);
+}
+
 // Shared memory of a block
 struct __align__(16) Shared {
   Table table;
@@ -150,6 +191,10 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
+}
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
@@ -248,6 +293,19 @@ struct Row {
       return top;
     }
   }
+  // The largest value of a step that has been fetched
+  __device__ __forceinline__ float largest_of(int s, const uint4& w) const {
+    if (E == 8 && whole(s)) {
+      const uint32_t t = max2(max2(w.x, w.y), max2(w.z, w.w));
+      const T* h = reinterpret_cast<const T*>(&t);
+      return fmaxf(fmaxf(to_float(h[0]), to_float(h[1])), -INFINITY);       // (two NaN: nothing)
+    }
+    float v[E], top = -INFINITY;
+    take(s, w, v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) top = fmaxf(top, v[e]);
+    return top;
+  }
   static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     uint32_t r;
     if constexpr (std::is_same<T, __half>::value) asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -327,8 +385,21 @@ struct Sampler {
     constexpr int E = Row<T>::E;
     uint64_t sum = 0;
     if constexpr (!FEW) {
-      row.each([&](float x, int i) {
-        if (in(x, i)) sum += w_of(x);
+      row.steps([&](int step, const uint4& w) {
+        float v[E];
+        const int i = row.take(step, w, v);
+        // (with a cut many steps have nothing that counts)
+        if (cut.x > -INFINITY) {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (in(v[e], i + e)) sum += w_of(v[e]);
+          return;
+        }
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float x0 = in(v[e], i + e) ? v[e] : -INFINITY, x1 = in(v[e + 1], i + e + 1) ? v[e + 1] : -INFINITY;
+          sum += weights2<WIDE>(x0, x1, s, sh.table);
+        }
       });
     } else {
       int n = 0;
@@ -379,6 +450,109 @@ struct Sampler {
     const uint64_t r = sh.own[own_phase][lane % WARPS];
     own_phase ^= 1;
     return r;
+  }
+
+  // The largest logit of this warp's share, and in the warp's part of the list, in order, all tokens that are not `reach`
+  // (or a little more) below it: of each 32 steps those that the largest so far leaves.  Where there are more than fit,
+  // n is more than MINE.
+  static constexpr int MINE = LIST / WARPS;
+  __device__ __forceinline__ float candidates(float reach, int& n) {
+    constexpr int E = Row<T>::E;
+    float* const lx = sh.list_x + warp * MINE;
+    int32_t* const li = sh.list_i + warp * MINE;
+    float top = -INFINITY, least = -INFINITY;
+    n = 0;
+    uint4 w0 = row.fetch(row.first + lane), w1 = row.fetch(row.first + lane + 32), w2 = row.fetch(row.first + lane + 64);
+    for (int s0 = row.first; s0 < row.last; s0 += 32) {
+      const uint4 w = w0;
+      w0 = w1;
+      w1 = w2;
+      w2 = row.fetch(s0 + lane + 96);
+      const bool live = s0 + lane < row.last;
+      float large = live ? row.largest_of(s0 + lane, w) : -INFINITY;
+      if (!__any_sync(0xffffffffu, large >= least && large > -INFINITY)) continue;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) large = fmaxf(large, __shfl_xor_sync(0xffffffffu, large, o));
+      if (large > top) {
+        top = large;
+        // (rounded down by more than the sum's rounding)
+        least = top + reach - 4.8e-7f * (fabsf(top) + fabsf(reach));
+      }
+      float v[E];
+      int i = 0;
+      uint32_t named = 0;
+      if (live) {
+        i = row.take(s0 + lane, w, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) named |= v[e] >= least && v[e] > -INFINITY ? 1u << e : 0;
+      }
+      const int mine = __popc(named);
+      int at = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += up;
+      }
+      const int all = __shfl_sync(0xffffffffu, at, 31);
+      if (n <= MINE && n + all > MINE) n = keep_from(lx, li, n, least);
+      if (n + all > MINE) {
+        n = MINE + 1;
+        continue;
+      }
+      at += n - mine;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (named >> e & 1) {
+          lx[at] = v[e] + 0.0f;
+          li[at++] = i + e;
+        }
+      n += all;
+      __syncwarp();
+    }
+    return top;
+  }
+  // Drops a warp's tokens below x, in order: how many are left.
+  __device__ __forceinline__ int keep_from(float* lx, int32_t* li, int n, float x) {
+    int left = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      const float v = i < n ? lx[i] : -INFINITY;
+      const int index = i < n ? li[i] : 0;
+      const bool is = i < n && v >= x;
+      const uint32_t vote = __ballot_sync(0xffffffffu, is);
+      __syncwarp();
+      if (is) {
+        const int at = left + __popc(vote & ((1u << lane) - 1));
+        lx[at] = v;
+        li[at] = index;
+      }
+      left += __popc(vote);
+      __syncwarp();
+    }
+    return left;
+  }
+
+  // The index of the first token with logit x in this warp's share, where there is one.
+  __device__ __forceinline__ int first_of(float x) {
+    for (int s0 = row.first; s0 < row.last; s0 += 128) {
+      uint4 w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u] = row.fetch(s0 + lane + 32 * u);
+      int at = row.V;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int step = s0 + lane + 32 * u;
+        if (step >= row.last) continue;
+        float v[Row<T>::E];
+        const int i = row.take(step, w[u], v);
+#pragma unroll
+        for (int e = 0; e < Row<T>::E; ++e)
+          if (v[e] == x) at = min(at, i + e);
+      }
+      at = __reduce_min_sync(0xffffffffu, at);
+      if (at < row.V) return at;
+    }
+    return row.V;
   }
 
   // The index of the m-th (from 1) token with logit x, or V
@@ -455,6 +629,7 @@ struct Sampler {
   // A count of bin b is worth low(b) to high(b).
   template <class L, class H>
   __device__ uint32_t find(float need, L low, H high, int& b0, int& b1, uint32_t& before) {
+    __syncthreads();                         // (the last call's results are read)
     uint32_t n[EACH], count = 0;
     float lo = 0.0f, hi = 0.0f, vl[EACH], vh[EACH];
     static_assert(EACH == 4, "one 16-byte load of counts");
@@ -604,6 +779,17 @@ struct Sampler {
   // a time.
   __device__ uint32_t key_below(int b) const {
     uint32_t lo = KEY_LOWEST, hi = key_of(s.top);
+    // (steps of 2, 4, 8 ... keys on both sides of where the bin should begin come first)
+    const float guess = fminf(s.top - (b - 0.5f) / (bins * s.c_hi), s.top);
+    if (guess > -INFINITY) {
+      const int64_t k = (int64_t)key_of(guess) + (lane < 16 ? -(2ll << (2 * (15 - lane))) : 2ll << (2 * (lane - 16)));
+      const uint32_t at = (uint32_t)max((int64_t)lo + 1, min((int64_t)hi, k));
+      const float y = y_of(value_of(at));
+      const int n = __popc(__ballot_sync(0xffffffffu, !(y < Y_MOST) || bin_of(y) >= b));
+      const uint32_t below = __shfl_sync(0xffffffffu, at, max(n - 1, 0)), above = __shfl_sync(0xffffffffu, at, min(n, 31));
+      if (n > 0) lo = below;
+      if (n < 32) hi = above - 1;
+    }
     while (lo < hi) {
       const uint32_t span = hi - lo;
       auto tried = [&](int j) { return lo + (uint32_t)(((uint64_t)span * (j + 1) + 31) / 32); };
@@ -614,6 +800,51 @@ struct Sampler {
       lo = next;
     }
     return lo;
+  }
+
+  // All tokens from logit x0 on, where they are at most LIST: the number of them in the list.
+  __device__ int gather(float x0) {
+    int* const mine = &sh.n[turn];
+    row.each([&](float x, int i) {
+      if (x < x0 || !kept(cut, x, i)) return;
+      const int at = atomicAdd(mine, 1);
+      if (at < LIST) {
+        sh.list_x[at] = x + 0.0f;
+        sh.list_i[at] = i;
+      }
+    });
+    sync();
+    return collect(mine);
+  }
+
+  // The sum of the weights that `cut` keeps of the list.
+  __device__ uint64_t list_sum(int n) {
+    uint64_t t = 0;
+    for (int i = lane; i < n; i += 32)
+      if (kept(cut, sh.all_x[i], sh.all_i[i])) t += sh.all_w[i];
+    return warp_sum(t);
+  }
+
+  // The list's entry on which `at` falls: the first by index whose running sum passes it.
+  __device__ int list_at(int n, uint64_t at) {
+    int i0 = 0, i1 = row.V - 1;
+    while (i0 < i1) {
+      const int mid = i0 + (int)((int64_t)(i1 - i0) * (warp + 1) / (WARPS + 1));
+      uint64_t t = 0;
+      for (int i = lane; i < n; i += 32)
+        if (sh.all_i[i] <= mid && kept(cut, sh.all_x[i], sh.all_i[i])) t += sh.all_w[i];
+      const uint64_t sums = within(warp_sum(t));
+      const uint32_t past = __ballot_sync(0xffffffffu, lane < WARPS && sums > at);
+      const int w = past ? __ffs(past) - 1 : WARPS;
+      const int was = i0;
+      auto tried = [&](int j) { return was + (int)((int64_t)(i1 - was) * (j + 1) / (WARPS + 1)); };
+      if (w > 0) i0 = tried(w - 1) + 1;
+      if (w < WARPS) i1 = tried(w);
+    }
+    int e = 0;
+    for (int i = lane; i < n; i += 32)
+      if (sh.all_i[i] == i0) e = i;
+    return __reduce_max_sync(0xffffffffu, e);
   }
 
   // The bin whose tokens reach `need`, by exact sums; what lies above it is added to `above`, n is its number of tokens.
@@ -694,7 +925,11 @@ struct Sampler {
     uint64_t over = 0;
     exchange(share, [&](int, uint64_t w) { over += w; });
     need -= MASS ? warp_sum(over) : before;
-    // every block takes the whole list
+    return pick<MASS>(need, collect(mine), row.first * Row<T>::E - row.shift, row.last * Row<T>::E - row.shift);
+  }
+
+  // Every block takes the whole list: the number of its tokens.
+  __device__ int collect(const int* mine) {
     const int have = lane < blocks ? (blocks == 1 ? *mine : (int)ld_cluster_u32(remote(mine, lane))) : 0;
     int upto = have;
 #pragma unroll
@@ -730,19 +965,29 @@ struct Sampler {
       }
     }
     __syncthreads();
+    return n;
+  }
+
+  // The cut where it is among the list's tokens that `cut` keeps; `share` gets those of them from index `from` on and below
+  // `to` that it keeps.
+  template <bool MASS>
+  __device__ Cut pick(uint64_t need, int n, int from, int to) {
+    __syncthreads();                         // (the last call's ties are read)
+    auto mine = [&](int i) { return kept(cut, sh.all_x[i], sh.all_i[i]); };
     auto key = [&](int i) { return key_of(sh.all_x[i]) >> KEY_SHIFT; };
     uint32_t lo = 0xffffffffu, hi = 0;
-    for (int i = lane; i < n; i += 32) {
-      lo = min(lo, key(i));
-      hi = max(hi, key(i));
-    }
+    for (int i = lane; i < n; i += 32)
+      if (mine(i)) {
+        lo = min(lo, key(i));
+        hi = max(hi, key(i));
+      }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     // the lowest key with less than `need` above it: the warps try 16 at a time
     while (lo < hi) {
       const uint32_t mid = lo + (uint32_t)((uint64_t)(hi - lo) * (warp + 1) / (WARPS + 1));
       uint64_t t = 0;
-      for (int i = lane; i < n; i += 32) t += key(i) > mid ? (MASS ? sh.all_w[i] : 1) : 0;
+      for (int i = lane; i < n; i += 32) t += key(i) > mid && mine(i) ? (MASS ? sh.all_w[i] : 1) : 0;
       const uint64_t sums = within(warp_sum(t));
       const uint32_t less = __ballot_sync(0xffffffffu, lane < WARPS && sums < need);
       const int w = less ? __ffs(less) - 1 : WARPS;        // the first that leaves less
@@ -756,9 +1001,10 @@ struct Sampler {
     int ties = 0;
     for (int i0 = 0; i0 < n; i0 += 32) {
       const int i = i0 + lane;
-      const uint32_t k = i < n ? key(i) : 0;
+      const bool live = i < n && mine(i);
+      const uint32_t k = live ? key(i) : 0;
       above += k > lo ? (MASS ? sh.all_w[i] : 1) : 0;
-      const bool is = i < n && k == lo;
+      const bool is = live && k == lo;
       const uint32_t vote = __ballot_sync(0xffffffffu, is);
       // (every warp writes the same)
       if (is) sh.tie[ties + __popc(vote & ((1u << lane) - 1))] = i;
@@ -788,8 +1034,6 @@ struct Sampler {
       if (w < WARPS) i1 = tried(w);
     }
     known = Cut{x, i0};
-    // what the list adds to this warp's weights
-    const int from = row.first * Row<T>::E - row.shift, to = row.last * Row<T>::E - row.shift;
     uint64_t more = 0;
     for (int i = lane; i < n; i += 32) {
       const int at = sh.all_i[i];
@@ -799,6 +1043,19 @@ struct Sampler {
     return known;
   }
 };
+
+// w >= m where x >= max + t ln m
+__device__ __forceinline__ Cut least_of(float m, float top, double reach, int V) {
+  const float x = __double2float_ru((double)top + reach);
+  return Cut{fminf(x, top), x > -INFINITY ? V : NONE};
+}
+// Where u falls in a sum of weights
+__device__ __forceinline__ uint64_t part_of_sum(float u, uint64_t total) {
+  return !(u > 0.0f) ? 0 : (u < 1.0f ? times(u, total, false) : total - 1);
+}
+__device__ __forceinline__ float log_share(float top, float x, float heat, uint64_t total) {
+  return (float)(-((double)top - (double)x) / (double)heat - log((double)total / (double)(1ull << FRAC)));
+}
 
 template <class T>
 __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, int blocks) {
@@ -829,10 +1086,15 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   }
 
   Sampler<T> p(sh, row, blocks, rank);
-  // ---- the largest logit, and the smallest where steps of y will be counted ----
+  // ---- the largest logit, and the smallest where steps of y will be counted; with min-p and without top-p the tokens that
+  // min-p may keep come with it ----
   float top = -INFINITY, least = INFINITY;
-  const bool counts = (k > 0 && k < V) || (share > 0.0f && share < 1.0f);
-  if (counts) {
+  const bool some = heat > 0.0f && m > 0.0f && m <= 1.0f && !(share < 1.0f);
+  const bool counts = heat > 0.0f && !some && ((k > 0 && k < V) || (share > 0.0f && share < 1.0f));
+  int listed = 0;
+  if (some) {
+    top = p.candidates(heat * logf(m), listed);
+  } else if (counts) {
     row.each([&](float x, int) {
       top = fmaxf(top, x);
       least = fminf(least, x > -INFINITY ? x : INFINITY);
@@ -845,31 +1107,99 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
   }
-  p.exchange((uint64_t)__float_as_uint(top) << 32 | __float_as_uint(least), [&](int, uint64_t w) {
-    top = fmaxf(top, __uint_as_float((uint32_t)(w >> 32)));
-    least = fminf(least, __uint_as_float((uint32_t)w));
+  // (a warp whose list is too short says so by a smallest logit of NaN)
+  if (listed > Sampler<T>::MINE) least = __int_as_float(0x7fffffff);
+  float tops[MOST_BLOCKS * WARPS / 32];
+  bool fit = true;
+#pragma unroll
+  for (int q = 0; q < MOST_BLOCKS * WARPS / 32; ++q) tops[q] = -INFINITY;
+  p.exchange((uint64_t)__float_as_uint(top) << 32 | __float_as_uint(least), [&](int i, uint64_t w) {
+    const float t = __uint_as_float((uint32_t)(w >> 32)), l = __uint_as_float((uint32_t)w);
+#pragma unroll
+    for (int q = 0; q < MOST_BLOCKS * WARPS / 32; ++q)
+      if (i / 32 == q) tops[q] = t;
+    top = fmaxf(top, t);
+    fit = fit && l == l;
+    least = fminf(least, l);
   });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
   }
-  top += 0.0f;                               // (-0 is 0)
+  fit = __all_sync(0xffffffffu, fit);
   if (top == -INFINITY || !(heat > 0.0f) || top == INFINITY) {
-    // nothing to take, or the largest
-    const int at = top == -INFINITY ? -1 : p.nth(top, 1);
-    if (rank == 0 && tid == 0) {
-      a.tokens[r] = at;
-      if (a.logprob) a.logprob[r] = at < 0 ? -INFINITY : 0.0f;
+    // nothing to take, or the largest, which the first warp with it looks for
+    int who = 0x7fffffff;
+#pragma unroll
+    for (int q = MOST_BLOCKS * WARPS / 32 - 1; q >= 0; --q)
+      if (32 * q + lane < blocks * WARPS && tops[q] == top) who = 32 * q + lane;
+    who = __reduce_min_sync(0xffffffffu, who);
+    if (rank * WARPS + warp == who) {
+      const int at = top == -INFINITY ? -1 : p.first_of(top);
+      if (lane == 0) {
+        a.tokens[r] = at;
+        if (a.logprob) a.logprob[r] = at < 0 ? -INFINITY : 0.0f;
+      }
     }
     p.sync();
     return;
   }
+  top += 0.0f;                               // (-0 is 0)
   p.s.top = top;
   p.s.c_hi = sh.c_hi;
   p.s.c_lo = sh.c_lo;
   p.cut = Cut{-INFINITY, NONE};
-  const float range = counts ? fminf(p.y_of(least), Y_MOST) : 0.0f;
+  if (some && fit) {
+    // what min-p keeps, by warp and so in order, goes to the first block's list
+    const Cut cut = least_of(m, top, sh.reach, V);
+    float* const lx = sh.list_x + warp * Sampler<T>::MINE;
+    int32_t* const li = sh.list_i + warp * Sampler<T>::MINE;
+    const int mine = p.keep_from(lx, li, listed, cut.x);
+    uint64_t before = 0, all = 0;
+    p.exchange((uint64_t)mine, [&](int i, uint64_t w) {
+      before += i < rank * WARPS + warp ? w : 0;
+      all += w;
+    });
+    before = warp_sum(before);
+    all = warp_sum(all);
+    if (all <= THREADS) {
+      for (int i = lane; i < mine; i += 32) {
+        const uint32_t at = (uint32_t)before + i;
+        if (rank == 0) {
+          sh.all_x[at] = lx[i];
+          sh.all_i[at] = li[i];
+        } else {
+          st_cluster_u32(p.remote(&sh.all_x[at], 0), __float_as_uint(lx[i]));
+          st_cluster_u32(p.remote(&sh.all_i[at], 0), (uint32_t)li[i]);
+        }
+      }
+      p.sync();
+      if (rank != 0) return;
+      const int n = (int)all;
+      if (k > 0 && k < n) p.cut = p.template pick<false>(k, n, 0, 0);
+      const float x = tid < n ? sh.all_x[tid] : -INFINITY;
+      const int index = tid < n ? sh.all_i[tid] : 0;
+      const uint64_t w = tid < n && kept(p.cut, x, index) ? p.w_of(x) : 0;
+      uint64_t upto = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += up;
+      }
+      const uint64_t sums = p.within(__shfl_sync(0xffffffffu, upto, 31));
+      const uint64_t first = warp_sum(lane < warp ? sums : 0), total = warp_sum(lane < WARPS ? sums : 0);
+      const uint64_t at = part_of_sum(u, total);
+      if (at < first + upto && at >= first + upto - w) {
+        a.tokens[r] = index;
+        if (a.logprob) a.logprob[r] = log_share(top, x, heat, total);
+      }
+      return;
+    }
+    __syncthreads();
+  }
+  // (with min-p the smallest logit is not known: the steps are those of the whole range)
+  const float range = counts ? fminf(p.y_of(least), Y_MOST) : (some ? Y_MOST : 0.0f);
   p.bins = range > 1e-30f ? (BINS - 1) / range : 0.0f;
   p.slope = range > 1e-30f ? -4096 * 0.69314718f / p.bins : 0.0f;
 
@@ -883,8 +1213,31 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
       }
     });
     n = p.row_sum(n);
+    if (n > (uint64_t)k && k <= FEW) {
+      // few enough to go on with them alone: every block has all of them, and the first one decides
+      int b0, b1;
+      uint32_t before;
+      const uint32_t here = p.find((float)k, [](int) { return 1.0f; }, [](int) { return 1.0f; }, b0, b1, before);
+      if (before + here <= FEW) {
+        const int have = p.gather(value_of(p.key_below(b1 + 1) + 1));
+        p.cut = p.template pick<false>(k, have, 0, 0);
+        if (share <= 0.0f) p.cut = strictest(p.cut, p.template pick<false>(1, have, 0, 0));
+        else if (share < 1.0f)
+          p.cut = strictest(p.cut, p.template pick<true>(times(share, p.list_sum(have), true), have, 0, 0));
+        if (m > 1.0f) p.cut = strictest(p.cut, p.template pick<false>(1, have, 0, 0));
+        else if (m > 0.0f) p.cut = strictest(p.cut, least_of(m, top, sh.reach, V));
+        const uint64_t total = p.list_sum(have);
+        const int e = p.list_at(have, part_of_sum(u, total));
+        if (rank == 0 && tid == 0) {
+          a.tokens[r] = sh.all_i[e];
+          if (a.logprob) a.logprob[r] = log_share(top, sh.all_x[e], heat, total);
+        }
+        p.sync();                              // (the others may still read this block's shared memory)
+        return;
+      }
+    }
     if (n > (uint64_t)k) p.cut = p.template descend<false>(k);
-    if (counts) p.clear();
+    if (share < 1.0f) p.clear();
   }
   if (share <= 0.0f) {
     p.cut = Cut{top, p.nth(top, 1)};
@@ -902,9 +1255,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   if (m > 1.0f) {
     p.cut = strictest(p.cut, Cut{top, p.nth(top, 1)});
   } else if (m > 0.0f) {
-    // w >= m where x >= max + t ln m
-    const float x = __double2float_ru((double)top + sh.reach);
-    p.cut = strictest(p.cut, Cut{fminf(x, top), x > -INFINITY ? V : NONE});
+    p.cut = strictest(p.cut, least_of(m, top, sh.reach, V));
   }
 
   // ---- kept weights by warp, and the one that u falls on ----
@@ -919,7 +1270,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   });
   before = warp_sum(before);
   total = warp_sum(total);
-  uint64_t at = !(u > 0.0f) ? 0 : (u < 1.0f ? times(u, total, false) : total - 1);
+  uint64_t at = part_of_sum(u, total);
   if (at >= before && at < before + mine) {
     at -= before;
     for (int s0 = row.first; s0 < row.last; s0 += 32) {
@@ -949,9 +1300,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
             if (!done && at < run) {
               done = true;
               a.tokens[r] = i + e;
-              if (a.logprob)
-                a.logprob[r] = (float)(-((double)top - (double)v[e]) / (double)heat -
-                                       log((double)total / (double)(1ull << FRAC)));
+              if (a.logprob) a.logprob[r] = log_share(top, v[e], heat, total);
             }
           }
         }

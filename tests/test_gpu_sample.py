@@ -165,6 +165,22 @@ def test_rows_do_not_depend_on_one_another():
         assert torch.equal(call(slice(a, b)), whole[a:b])
 
 
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("v", [300, 5000, 70001])
+def test_small_k_with_other_filters(dtype, v):
+    """First k of a few to more than a list holds, each with top-p and min-p at every strictness."""
+    r = 48
+    rng = np.random.default_rng(v)
+    k = np.resize([1, 2, 3, 17, 50, 255, 999, 1024, 1025, 2047, 2048, 4000], r)
+    p = np.resize([1.0, 0.0, 0.3, 0.9, 0.999], r)
+    m = np.resize([0.0, 0.0, 0.05, 1.0, 0.5, 2.0, 0.0], r)
+    for std in (0.05, 2.0):
+        x = logits(v, r, v, dtype, std)
+        check(x, rng.random(r), t=rng.uniform(0.5, 1.5, r), k=k, p=p, m=m)
+        check(x, rng.random(r), k=k)
+        check(x, rng.random(r), k=k, m=m)
+
+
 def test_no_rows_and_no_tokens():
     x = torch.zeros((0, 10), device="cuda")
     assert bq.bq_sample(x, torch.zeros(0, device="cuda"))[0].shape == (0,)
