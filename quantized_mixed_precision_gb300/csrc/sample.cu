@@ -43,6 +43,7 @@ constexpr int QUEUE = 32 * 9;                // of a warp: a step of 8 elements 
 // 131072 fp16 at 50 42 and 60, 200 52 and 62, 400 62 and 65, 1000 98 and 68.
 constexpr int FEW = 256;
 constexpr int MOST_BLOCKS = 8;
+constexpr int LIGHT = 4;                     // steps on their way in passes that do little
 
 // Keys of fp32 values: unsigned integers of the same order.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -173,6 +174,7 @@ struct __align__(16) Shared {
   uint16_t tie[LIST];              // entries of the list
   float queue[WARPS][QUEUE];       // tokens of a warp whose weights are to be summed
   int n[2];                        // gathered by the block, two lists in turn
+  uint32_t largest;                // key of the largest logit so far
   float c_hi, c_lo;
   double reach;                    // temperature times ln of min_p
   int found;
@@ -259,15 +261,19 @@ struct Row {
     }
     return i;
   }
-  // f(step, its 16 bytes) for this lane's steps: two steps are fetched ahead, for the latency's sake
-  template <class F>
+  // f(step, its 16 bytes) for this lane's steps, AHEAD of which are on their way, for the latency's sake
+  template <int AHEAD, class F>
   __device__ __forceinline__ void steps(F f) const {
-    uint4 w0 = fetch(first + lane), w1 = fetch(first + lane + 32);
-    for (int s = first + lane; s < last; s += 32) {
-      const uint4 w2 = fetch(s + 64);
-      f(s, w0);
-      w0 = w1;
-      w1 = w2;
+    uint4 w[AHEAD];
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) w[q] = fetch(first + lane + 32 * q);
+    for (int s = first + lane; s < last; s += 32 * AHEAD) {
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) {
+        const uint4 now = w[q];
+        w[q] = fetch(s + 32 * (AHEAD + q));
+        if (s + 32 * q < last) f(s + 32 * q, now);
+      }
     }
   }
   // The largest value of this thread's elements
@@ -276,7 +282,7 @@ struct Row {
     if constexpr (E == 8) {
       // two at a time: NaN gives way to the other value
       uint32_t t = std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
-      steps([&](int s, const uint4& w) {
+      steps<LIGHT>([&](int s, const uint4& w) {
         if (whole(s)) {
           t = max2(max2(t, w.x), max2(max2(w.y, w.z), w.w));
         } else {
@@ -314,7 +320,7 @@ struct Row {
   }
   template <class F>
   __device__ __forceinline__ void each(F f) const {
-    steps([&](int s, const uint4& w) {
+    steps<2>([&](int s, const uint4& w) {
       float v[E];
       const int i = take(s, w, v);
 #pragma unroll
@@ -385,7 +391,7 @@ struct Sampler {
     constexpr int E = Row<T>::E;
     uint64_t sum = 0;
     if constexpr (!FEW) {
-      row.steps([&](int step, const uint4& w) {
+      row.template steps<2>([&](int step, const uint4& w) {
         float v[E];
         const int i = row.take(step, w, v);
         // (with a cut many steps have nothing that counts)
@@ -452,7 +458,7 @@ struct Sampler {
     return r;
   }
 
-  // The largest logit of this warp's share, and in the warp's part of the list, in order, all tokens that are not `reach`
+  // The largest logit of the block's that this warp knows of, and in the warp's part of the list, in order, all tokens that are not `reach`
   // (or a little more) below it: of each 32 steps those that the largest so far leaves.  Where there are more than fit,
   // n is more than MINE.
   static constexpr int MINE = LIST / WARPS;
@@ -462,6 +468,7 @@ struct Sampler {
     int32_t* const li = sh.list_i + warp * MINE;
     float top = -INFINITY, least = -INFINITY;
     n = 0;
+    auto below = [&](float top) { return top + reach - 4.8e-7f * (fabsf(top) + fabsf(reach)); };
     uint4 w0 = row.fetch(row.first + lane), w1 = row.fetch(row.first + lane + 32), w2 = row.fetch(row.first + lane + 64);
     for (int s0 = row.first; s0 < row.last; s0 += 32) {
       const uint4 w = w0;
@@ -470,13 +477,19 @@ struct Sampler {
       w2 = row.fetch(s0 + lane + 96);
       const bool live = s0 + lane < row.last;
       float large = live ? row.largest_of(s0 + lane, w) : -INFINITY;
+      // (the block's largest so far leaves fewer than the warp's own)
+      const uint32_t seen = *reinterpret_cast<volatile uint32_t*>(&sh.largest);
+      if (seen > key_of(top)) {
+        top = value_of(seen);
+        least = below(top);
+      }
       if (!__any_sync(0xffffffffu, large >= least && large > -INFINITY)) continue;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) large = fmaxf(large, __shfl_xor_sync(0xffffffffu, large, o));
       if (large > top) {
         top = large;
-        // (rounded down by more than the sum's rounding)
-        least = top + reach - 4.8e-7f * (fabsf(top) + fabsf(reach));
+        least = below(top);                  // (rounded down by more than the sum's rounding)
+        if (lane == 0) atomicMax(&sh.largest, key_of(top + 0.0f));
       }
       float v[E];
       int i = 0;
@@ -1079,6 +1092,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   // (64-bit arithmetic is slow here: one thread's part for the block)
   if (tid == THREADS - 1) {
     sh.n[0] = sh.n[1] = 0;
+    sh.largest = KEY_LOWEST;
     const double c = fmin(1.4426950408889634 / (double)heat, 1e30);
     sh.c_hi = (float)c;
     sh.c_lo = (float)(c - (double)sh.c_hi);
@@ -1093,6 +1107,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   const bool counts = heat > 0.0f && !some && ((k > 0 && k < V) || (share > 0.0f && share < 1.0f));
   int listed = 0;
   if (some) {
+    __syncthreads();
     top = p.candidates(heat * logf(m), listed);
   } else if (counts) {
     row.each([&](float x, int) {
@@ -1135,8 +1150,10 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
     for (int q = MOST_BLOCKS * WARPS / 32 - 1; q >= 0; --q)
       if (32 * q + lane < blocks * WARPS && tops[q] == top) who = 32 * q + lane;
     who = __reduce_min_sync(0xffffffffu, who);
+    // (with `some` a warp's is the largest that it knows of: all look)
+    const int found = some && top > -INFINITY ? p.nth(top, 1) : -1;
     if (rank * WARPS + warp == who) {
-      const int at = top == -INFINITY ? -1 : p.first_of(top);
+      const int at = top == -INFINITY ? -1 : (some ? found : p.first_of(top));
       if (lane == 0) {
         a.tokens[r] = at;
         if (a.logprob) a.logprob[r] = at < 0 ? -INFINITY : 0.0f;

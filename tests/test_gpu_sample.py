@@ -123,6 +123,25 @@ def test_infinities_and_nan(dtype):
         check(x, us, k=[1] * 7)
 
 
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_min_p_alone(dtype):
+    """From a few kept tokens to all of them, rows of infinities among them, with and without top-k."""
+    for v in (5, 4000, 70001):
+        for std in (0.01, 0.5, 3.0):
+            x = logits(v, 24, v, dtype, std)
+            x[1] = float("-inf")
+            x[2, v // 2] = float("inf")
+            x[3, v - 1] = float("inf")
+            x[4, : v // 2] = float("nan")
+            x[5] = x[5].sort().values                 # the largest last: all before it were the largest once
+            x[6] = x[6].sort(descending=True).values
+            x[7] = 1.0
+            u = np.random.default_rng(v).random(24)
+            m = np.resize([0.001, 0.05, 0.3, 0.9, 1.0], 24)
+            check(x, u, m=m)
+            check(x, u, t=np.resize([0.3, 1.0, 2.0], 24), m=m, k=np.resize([0, 1, 5, 40, 3000], 24))
+
+
 def test_settings_at_the_edges():
     inf, nan = float("inf"), float("nan")
     x = logits(6, 12, 777, "f16")
