@@ -864,8 +864,10 @@ cudaError_t launch_both(const TreeParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-bool attn_tree_tc_applies(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_len) {
-  return D <= 128 && q_heads / kv_heads * max_q > 32 && max_len > 0;
+bool attn_tree_tc_applies(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_len) {
+  const int64_t rows = q_heads / kv_heads * max_q;
+  if (D > 128 || rows <= 32 || max_len == 0) return false;
+  return max_len > DIRECT_LEN || B * kv_heads * ((rows + 7) / 8) > 3 * sm_count();
 }
 
 size_t attn_tree_tc_workspace(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q) {

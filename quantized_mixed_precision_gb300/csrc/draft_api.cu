@@ -41,7 +41,7 @@ size_t bq_attn_kv4_tree_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, 
   if (B > MAX_ROWS || q_heads > MAX_HEADS || D > 256 || max_q > 64 * MAX_WORDS || max_len > MAX_LEN) return 0;
   // (the call takes the smaller of max_q and T: enough for either form)
   const size_t rows = attn_tree_rows_workspace(q_heads, kv_heads, D, max_q, max_len);
-  const size_t tc = attn_tree_tc_applies(q_heads, kv_heads, D, max_q, max_len)
+  const size_t tc = attn_tree_tc_applies(B, q_heads, kv_heads, D, max_q, max_len)
                         ? attn_tree_tc_workspace(q_heads, kv_heads, D, max_q) : 0;
   return rows > tc ? rows : tc;
 }
@@ -96,7 +96,7 @@ bq_status bq_attn_kv4_tree(const uint16_t* q, int64_t ld_q, int64_t T, int64_t q
   a.lse = lse;
   a.workspace = workspace;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (attn_tree_tc_applies(q_heads, kv_heads, D, max_q, max_len))
+  if (attn_tree_tc_applies(B, q_heads, kv_heads, D, max_q, max_len))
     return from_cuda(launch_attn_tree_tc(a, tree, (int)words, s));
   return from_cuda(launch_attn_tree_rows(a, tree, (int)words, s));
 }

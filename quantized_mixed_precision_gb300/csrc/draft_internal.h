@@ -13,7 +13,7 @@ size_t attn_tree_rows_workspace(int64_t q_heads, int64_t kv_heads, int64_t D, in
 cudaError_t launch_attn_tree_rows(const AttnKv4Args& a, const uint64_t* tree, int words, cudaStream_t stream);
 
 // Many of them, on tcgen05: whether that is the better fit (a rule of sizes alone).
-bool attn_tree_tc_applies(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_len);
+bool attn_tree_tc_applies(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_len);
 size_t attn_tree_tc_workspace(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q);
 cudaError_t launch_attn_tree_tc(const AttnKv4Args& a, const uint64_t* tree, int words, cudaStream_t stream);
 
