@@ -35,8 +35,8 @@ constexpr int KT = 128;                     // keys of a tile
 constexpr int SLOT_ROWS = 128;
 constexpr int SOFT_WARPS = 8, LOAD_WARPS = 4;     // of both slots; of keys, and of values
 constexpr int MMA_WARP = SOFT_WARPS + 2 * LOAD_WARPS, TREE_WARPS = MMA_WARP + 4, TREE_THREADS = 32 * TREE_WARPS;
-// Registers of a thread, by warpgroup: 96 at the launch (5 * 96 = 480), then 144, 144, 72, 72 and 48.
-constexpr int SOFT_REGS = 144, LOAD_REGS = 72, MMA_REGS = 48;
+// Registers of a thread, by warpgroup: 96 at the launch (5 * 96 = 480), then 136, 136, 80, 80 and 48.
+constexpr int SOFT_REGS = 136, LOAD_REGS = 80, MMA_REGS = 48;
 constexpr int STAGES = 2;                   // tiles of keys, and of values, in shared memory
 constexpr int HALF_B = KT * 128;            // 64 dims of a tile
 constexpr uint64_t DRAIN_NS = 2000000000ull;
@@ -103,6 +103,29 @@ struct Walk {
   }
 };
 
+// warp_wait that sleeps up to 16 us at a time, so that the waiting warps' polls do not take issue slots from those that convert.
+__device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns, int* status) {
+  uint32_t ok = mbar_test_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+      if (globaltimer_ns() - t0 >= timeout_ns) {
+        record_error(status, BQ_ERR_TIMEOUT);
+        break;
+      }
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(16000u)
+          : "memory");
+      if (ok) break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
 // 16 columns of 32 lanes from registers
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -138,31 +161,49 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w));
 }
 
-// Four words of codes (32 dims of a key) as fp16 values: each is fp16_rne(low + step * code), as bq_qk_norm_rope_kv4 hands
-// it out; where 15 steps pass fp16's range it is held to the largest.
-__device__ __forceinline__ void store_values(const uint32_t (&to)[4], uint32_t off, const uint4& codes, uint32_t par) {
-  const uint32_t step = prmt(par, par, 0x1010), low = prmt(par, par, 0x3232);
+// A word of codes (8 dims of a key) as fp16 values, each fp16_rne(low + step * code), as bq_qk_norm_rope_kv4 hands it out
+__device__ __forceinline__ void word_values(uint32_t w, uint32_t step, uint32_t low, uint32_t (&h)[4]) {
+  const uint32_t y = w >> 8;
+  h[0] = hsub2_u32((w & CODE_LO) | H2_MAGIC, H2_MAGIC);
+  h[1] = hfma2_u32((w & CODE_HI) | H2_MAGIC, H2_INV16, 0xd400d400u);        // (1024 + 16 u) / 16 - 64
+  h[2] = hsub2_u32((y & CODE_LO) | H2_MAGIC, H2_MAGIC);
+  h[3] = hfma2_u32((y & CODE_HI) | H2_MAGIC, H2_INV16, 0xd400d400u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = hfma2_u32(h[i], step, low);
+}
+
+// Whether params hold values beyond fp16's range
+__device__ __forceinline__ bool beyond(uint32_t par) {
   const float2 f = unpack_h2(par);
-  const bool large = fabsf(fmaf(15.0f, f.x, f.y)) > 65504.0f;
+  return fabsf(fmaf(15.0f, f.x, f.y)) > 65504.0f;
+}
+
+// The same for four words (32 dims), to their chunks of a key's row, at to ^ 16 j
+__device__ __forceinline__ void store_values(uint32_t to, uint32_t off, const uint4& codes, uint32_t par) {
+  const uint32_t step = prmt(par, par, 0x1010), low = prmt(par, par, 0x3232);
+  uint32_t h[4];
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
+    word_values(w[j], step, low, h);
+    st_shared_v4((to ^ (j << 4)) + off, h[0], h[1], h[2], h[3]);
+  }
+}
+
+// ... with values beyond fp16's range held to its largest
+__device__ __forceinline__ void store_held(uint32_t to, uint32_t off, uint4 codes, uint32_t par) {
+  const uint32_t step = prmt(par, par, 0x1010), low = prmt(par, par, 0x3232);
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j) {
     uint32_t h[4];
-    const uint32_t y = w[j] >> 8;
-    h[0] = hsub2_u32((w[j] & CODE_LO) | H2_MAGIC, H2_MAGIC);
-    h[1] = hfma2_u32((w[j] & CODE_HI) | H2_MAGIC, H2_INV16, 0xd400d400u);        // (1024 + 16 u) / 16 - 64
-    h[2] = hsub2_u32((y & CODE_LO) | H2_MAGIC, H2_MAGIC);
-    h[3] = hfma2_u32((y & CODE_HI) | H2_MAGIC, H2_INV16, 0xd400d400u);
+    word_values(codes.x, step, low, h);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = hfma2_u32(h[i], step, low);
-    if (large) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(0x7bff7bffu));
-        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(0xfbfffbffu));
-      }
+    for (int i = 0; i < 4; ++i) {
+      asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(0x7bff7bffu));
+      asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(0xfbfffbffu));
     }
-    st_shared_v4(to[j] + off, h[0], h[1], h[2], h[3]);
+    st_shared_v4((to ^ (j << 4)) + off, h[0], h[1], h[2], h[3]);
+    codes = make_uint4(codes.y, codes.z, codes.w, codes.x);
   }
 }
 
@@ -300,12 +341,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
     const int P = 1 << a.page_log2;
     uint64_t* const full = values ? v_full : k_full;
     uint64_t* const empty = values ? v_empty : k_empty;
-    // this lane's four places in a tile's first step: its piece's chunks of a key's row, swizzled
-    uint32_t to[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      to[j] = smem_u32(smem) + (values ? C::OFF_V : C::OFF_K) + (piece >> 1) * HALF_B + (w * KEYS + key_lane) * 128 +
-              ((((piece & 1) * 4 + j) ^ (key_lane & 7)) << 4);
+    // this lane's first place in a tile's first step: its piece's first chunk of a key's row, swizzled
+    const uint32_t to = smem_u32(smem) + (values ? C::OFF_V : C::OFF_K) + (piece >> 1) * HALF_B +
+                        (w * KEYS + key_lane) * 128 + ((((piece & 1) * 4) ^ (key_lane & 7)) << 4);
     const int par_at = piece * 32 / (D / NG) * 4;       // of a key's params
     uint32_t* const seen = reinterpret_cast<uint32_t*>(smem + C::OFF_SEEN) + 32 * w;
     int n = 0;                                          // tiles so far
@@ -380,15 +418,26 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
           pages = checked(next_pages);
           next_pages = load_pages(t + 5);
         }
-        if (!warp_wait(&empty[stage], ((n / STAGES) & 1) ^ 1, p.timeout_ns, a.status)) {
+        if (!sleep_wait(&empty[stage], ((n / STAGES) & 1) ^ 1, p.timeout_ns, a.status)) {
           ok = false;
           break;
         }
-        // (the next tile's codes go into the registers of those that are done with)
+        bool hold = false;
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-          store_values(to, stage * C::TILE_B + i * LOAD_WARPS * KEYS * 128, codes[i], par[i]);
-          fetch_codes(t + 1, i);
+        for (int i = 0; i < STEPS; ++i) hold = hold || beyond(par[i]);
+        if (__any_sync(0xffffffffu, hold)) {
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i) {
+            store_held(to, stage * C::TILE_B + i * LOAD_WARPS * KEYS * 128, codes[i], par[i]);
+            fetch_codes(t + 1, i);
+          }
+        } else {
+          // (the next tile's codes go into the registers of those that are done with)
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i) {
+            store_values(to, stage * C::TILE_B + i * LOAD_WARPS * KEYS * 128, codes[i], par[i]);
+            fetch_codes(t + 1, i);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -403,7 +452,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
     int n = 0, units = 0;                               // tiles and units so far
     uint32_t turned = 0;                                // bit s: parity of the tiles whose weights were waited for in slot s
     for (;;) {
-      if (!ok || !warp_wait(q_full, units & 1, p.timeout_ns, a.status)) break;
+      if (!ok || !sleep_wait(q_full, units & 1, p.timeout_ns, a.status)) break;
       ++units;
       tc_fence_after();
       const int count = next_unit[0];
@@ -415,7 +464,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
       auto scores = [&](int s, int i) {
         const int t = n + tile_of(s, i), stage = t % STAGES;
         if (!wide || s == 0) {
-          if (!warp_wait(&k_full[stage], (t / STAGES) & 1, p.timeout_ns, a.status)) return false;
+          if (!sleep_wait(&k_full[stage], (t / STAGES) & 1, p.timeout_ns, a.status)) return false;
           tc_fence_after();
         }
         if (elect_one()) {
@@ -436,8 +485,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
           const int mine = tile_of(s, i);
           if (mine >= count) continue;
           const int t = n + mine, stage = t % STAGES;
-          if (!wide || s == 0) ok = warp_wait(&v_full[stage], (t / STAGES) & 1, p.timeout_ns, a.status);
-          ok = ok && warp_wait(&p_full[s], (turned >> s) & 1, p.timeout_ns, a.status);
+          if (!wide || s == 0) ok = sleep_wait(&v_full[stage], (t / STAGES) & 1, p.timeout_ns, a.status);
+          ok = ok && sleep_wait(&p_full[s], (turned >> s) & 1, p.timeout_ns, a.status);
           if (!ok) break;
           turned ^= 1u << s;
           tc_fence_after();
@@ -469,9 +518,30 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
     const float scale = fmaxf(fabsf(a.scale) * LOG2E, 1e-37f);     // (not 0: a score that is not seen is -inf)
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     int n = 0, ends[2] = {0, 0}, joins = 0;             // tiles of this slot, units that each slot had a part in, and joined ones
-    while (ok && walk.next(p, u)) {
+    while (walk.next(p, u)) {
       const int count = u.last - u.first;
       const int turns = u.wide ? count : (count + 1 - slot) / 2;
+      const bool whole = u.first == 0 && u.last == u.tiles;
+      // what the join needs, before anything is waited for: a block that gives up says of its further units that there is
+      // nothing to join
+      if (u.first == 0 && tid == 0 && (!whole || a.by_unit)) {
+        Meta mm{};
+        if (!whole && ok) {
+          const int64_t each = shares[0], extra = shares[1];
+          const int64_t last = u.u0 + u.tiles - 1, big = (each + 1) * extra;
+          const int64_t owner = last < big ? last / (each + 1) : extra + (last - big) / each;
+          mm.parts = (int32_t)(owner - blockIdx.x + 1);
+          mm.block = (int32_t)blockIdx.x;
+          mm.slot = u.u0 != start.at ? 1 : 0;
+          mm.head = u.head;
+          mm.row0 = u.row0;
+          mm.rows = u.rows;
+          mm.first = u.s.first;
+        }
+        const int qt = u.row0 / p.rows;
+        a.meta[a.by_unit ? (u.b * a.qtiles + qt) * a.heads + u.head : (int64_t)blockIdx.x] = mm;
+      }
+      if (!ok) continue;
       // ---- queries ----
       const int row = u.row0 + (u.wide ? slot * SLOT_ROWS : 0) + r;      // of the sequence's
       const bool live = row < u.row0 + u.rows;
@@ -514,7 +584,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
       const bool idle = !__any_sync(0xffffffffu, live);
       float m = -INFINITY, l = 0.0f;
       for (int i = 0; i < turns; ++i, ++n) {
-        if (!warp_wait(&s_full[slot], n & 1, p.timeout_ns, a.status)) {
+        if (!sleep_wait(&s_full[slot], n & 1, p.timeout_ns, a.status)) {
           ok = false;
           break;
         }
@@ -625,19 +695,18 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[slot]);
       }
-      if (!ok) break;
+      if (!ok) continue;
       // ---- the unit's end ----
-      const bool whole = u.first == 0 && u.last == u.tiles;
       bool had[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         had[s] = u.wide || (count + 1 - s) / 2 > 0;
         if (had[s] && (s == slot || !u.wide)) {
-          ok = ok && warp_wait(&o_done[s], ends[s] & 1, p.timeout_ns, a.status);
+          ok = ok && sleep_wait(&o_done[s], ends[s] & 1, p.timeout_ns, a.status);
         }
         if (had[s]) ++ends[s];
       }
-      if (!ok) break;
+      if (!ok) continue;
       tc_fence_after();
       float f[2] = {slot == 0 ? 1.0f : 0.0f, slot == 0 ? 0.0f : 1.0f};
       if (!u.wide) {
@@ -645,9 +714,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
         shared_ml[slot * SLOT_ROWS + r] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(x_full);
-        if (!warp_wait(x_full, joins++ & 1, p.timeout_ns, a.status)) {
+        if (!sleep_wait(x_full, joins++ & 1, p.timeout_ns, a.status)) {
           ok = false;
-          break;
+          continue;
         }
         const float2 x0 = shared_ml[r], x1 = shared_ml[SLOT_ROWS + r];
         m = fmaxf(x0.x, x1.x);
@@ -707,23 +776,6 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
             a.lse[orow] = log_sum(top, l);
           }
         }
-      }
-      if (u.first == 0 && tid == 0 && (!whole || a.by_unit)) {
-        Meta mm{};
-        if (!whole) {
-          const int64_t each = shares[0], extra = shares[1];
-          const int64_t last = u.u0 + u.tiles - 1, big = (each + 1) * extra;
-          const int64_t owner = last < big ? last / (each + 1) : extra + (last - big) / each;
-          mm.parts = (int32_t)(owner - blockIdx.x + 1);
-          mm.block = (int32_t)blockIdx.x;
-          mm.slot = u.u0 != start.at ? 1 : 0;
-          mm.head = u.head;
-          mm.row0 = u.row0;
-          mm.rows = u.rows;
-          mm.first = u.s.first;
-        }
-        const int qt = u.row0 / p.rows;
-        a.meta[a.by_unit ? (u.b * a.qtiles + qt) * a.heads + u.head : (int64_t)blockIdx.x] = mm;
       }
     }
     if (ok) {

@@ -256,3 +256,127 @@ def test_a_chain_matches_plain_attention():
     want, wlse = bq.bq_attn_kv4(dev(c["q"]), dev(c["codes"]), dev(c["params"]), dev(c["table"]), dev(c["lens"]),
                                 cu_q=dev(c["cu"]), max_q=n, lse=True)
     assert (out.float() - want.float()).abs().max() <= 4e-3 and (lse - wlse).abs().max() <= 2e-2
+
+
+@pytest.mark.parametrize("columns", [None, 64])
+def test_values_beyond_fp16(columns):
+    """Rows that see themselves alone give their own value.  A short cache's blocks (no table beyond what the sequence needs)
+    keep values as they are: the weight times the step is rounded (2**-11 of |v| + 2 |low|) and so is the result, which
+    fp16 may not hold.  A long one's round the values themselves, held to fp16's largest."""
+    n = 40
+    c = make(23, [n], [n], 4, 1, 128, 16, 64, stale=False)
+    c["params"][..., 0], c["params"][..., 1] = 9000.0, -65000.0
+    c["params"][:, 0] = 0.01                       # keys as they are elsewhere
+    if columns:
+        c["table"] = np.pad(c["table"], [(0, 0), (0, columns - c["table"].shape[1])])
+    out, _ = run(c, [np.eye(n, dtype=bool)])
+    from oracle.decode_oracle import cache_values
+    x, low = cache_values(c["codes"], c["params"], c["table"][0], n)
+    want = x[1, 0][:, None]
+    got = host(out).astype(np.float64)
+    if columns:
+        want = np.clip(want, -65504, 65504)
+        tol = 2.0 ** -10 * np.abs(want)            # two roundings: the value's and the result's
+    else:
+        assert (got[np.broadcast_to(want > 65520, got.shape)] > 65000).all()
+        got = np.where(np.isinf(got), want, got)
+        tol = 2.0 ** -11 * (2 * np.abs(want) + 2 * low[0][:, None])
+    assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 5.0])
+@pytest.mark.parametrize("n", [4, 40])
+def test_scales(scale, n):
+    c = make(24, [300 + n], [n], 4, 1, 128, 16, 64, qstd=0.3)
+    check(c, trees(24, [n]), scale=scale)
+
+
+@pytest.mark.parametrize("n", [5, 40])
+def test_large_scores_and_a_late_maximum(n):
+    """The running maximum rises by hundreds on the way, and what came before fades."""
+    c = make(25, [1200], [n], 4, 1, 128, 16, 64, stale=False)
+    rows = c["table"][0, np.arange(1200) // 16], np.arange(1200) % 16
+    grow = np.linspace(0.2, 6.0, 1200).astype(np.float16)
+    for g in range(2):
+        for e in range(2):
+            v = c["params"][rows[0], 0, :, rows[1], g, e]
+            c["params"][rows[0], 0, :, rows[1], g, e] = v * grow[:, None]
+    check(c, trees(25, [n]))
+
+
+def test_constant_values_over_a_long_cache():
+    """Weights sum to 1: a constant value comes out as it is, whatever the length."""
+    n, length = 40, 30000
+    c = make(26, [length], [n], 4, 1, 128, 64, 128, stale=False)
+    c["params"][:, 1, :, :, :, 0], c["params"][:, 1, :, :, :, 1] = 0.0, 3.0
+    out, _ = run(c, trees(26, [n]))
+    # weights are rounded to fp16 (2**-11 of each at most, either way), their sum is not
+    assert (out.float() - 3.0).abs().max() <= 3.0 * (2.0 ** -11 + 2.0 ** -11)
+
+
+def test_many_short_sequences_and_many_units():
+    rng = np.random.default_rng(27)
+    ns = [int(x) for x in rng.integers(0, 60, 90)]
+    c = make(27, [n + int(x) for n, x in zip(ns, rng.integers(0, 200, 90))], ns, 8, 2, 64, 16, 32)
+    check(c, trees(27, ns, padding=0.2))
+    ns = [17] * 40
+    check(make(28, [n + 600 + 40 * i for i, n in enumerate(ns)], ns, 16, 4, 128, 64, 64), trees(28, ns), uniform=True)
+
+
+@pytest.mark.parametrize("n", [12, 40, 80])
+def test_calls_at_the_same_time(n):
+    """Two streams, each with its own workspace and outputs, over one cache."""
+    c = make(29, [2500, 1300], [n, n], 8, 2, 128, 32, 64)
+    masks = trees(29, [n, n])
+    want, _ = run(c, masks)
+    args = [dev(c[k]) for k in ("q", "codes", "params", "table", "lens")]
+    bits = tree_tensor(masks)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(bq.bq_attn_kv4_tree(*args, bits)[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_the_wait_limit():
+    """A limit of nothing gives up at the first wait, reports it and leaves the device usable."""
+    n = 40
+    c = make(30, [3000, 900], [n, n], 8, 2, 128, 32, 64)
+    masks = trees(30, [n, n])
+    want, _ = run(c, masks)
+    old = bq.bq_set_wait_timeout_ns(0)
+    try:
+        run(c, masks)
+        assert bq.bq_device_status(reset=True) == bq.BQ_ERR_TIMEOUT
+    finally:
+        bq.bq_set_wait_timeout_ns(old)
+    again, _ = run(c, masks)
+    assert torch.equal(again, want)
+
+
+def test_refusals():
+    c = make(31, [60, 60], [8, 8], 4, 2, 128, 16, 64)
+    q, codes, params, table, lens = (dev(c[k]) for k in ("q", "codes", "params", "table", "lens"))
+    bits = tree_tensor(trees(31, [8, 8]))
+
+    def call(**kw):
+        a = dict(q=q, codes=codes, params=params, block_table=table, seq_lens=lens, tree=bits, **{})
+        a.update(kw)
+        return bq.bq_attn_kv4_tree(**a)
+    for kw in (dict(q=q.float()), dict(tree=bits.int()), dict(seq_lens=lens.long()), dict(codes=codes.char()),
+               dict(cu_q=dev(c["cu"]).long())):
+        with pytest.raises(TypeError):
+            call(**kw)
+    for kw in (dict(tree=bits[:5]), dict(tree=bits[:, 0]), dict(seq_lens=lens[:1]), dict(max_q=7), dict(max_len=10 ** 6),
+               dict(cu_q=dev(c["cu"])[:2]), dict(q=q[:15], tree=bits[:15]), dict(q=q.expand(2, 16, 4, 128)[0, :, :, ::2]),
+               dict(out=q[:3]), dict(q=q[:1].expand(16, 4, 128))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(bq.BqError):
+        call(window=-1)
+    with pytest.raises(bq.BqError):
+        call(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"), block_table=table.repeat(1, 20))
