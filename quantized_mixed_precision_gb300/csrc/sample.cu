@@ -243,10 +243,11 @@ struct Row {
     first = min(warp * per, steps);
     last = min(first + per, steps);
   }
-  // The 16 bytes of step s, where they are all of the row
+  // The 16 bytes of step s, where they are all of the row.  (An ordinary load: one of read-only data may be moved in front
+  // of the wait for the kernel before, which writes the logits.)
   __device__ __forceinline__ bool whole(int s) const { return s * E >= shift && s * E - shift + E <= V; }
   __device__ __forceinline__ uint4 fetch(int s) const {
-    return s < last && whole(s) ? __ldg(base + s) : make_uint4(0, 0, 0, 0);
+    return s < last && whole(s) ? base[s] : make_uint4(0, 0, 0, 0);
   }
   // Elements of step s, which has been fetched: index of the first, values (-inf where there is none)
   __device__ __forceinline__ int take(int s, const uint4& w, float (&v)[E]) const {
