@@ -72,7 +72,8 @@ constexpr float VF_MOST = 1073741824.0f;   // 2**30: the smallest step, 2**-24, 
 // join needs of the sequence
 struct Meta {
   int32_t parts;       // 0: nothing to join
-  int32_t block, slot;
+  int32_t block;
+  int16_t slot, nodes; // nodes: of the sequence, with TREE
   int32_t head, row0, rows;
   int64_t first;
 };
@@ -107,9 +108,11 @@ struct AttnParams {
 __device__ __forceinline__ bool tree_sees(const AttnParams& a, int64_t token, int i) {
   return (__ldg(a.tree + token * a.words + (i >> 6)) >> (i & 63)) & 1;
 }
-__device__ __forceinline__ int tree_depth(const AttnParams& a, int64_t token) {
+// (of `nodes` nodes: bits from there on do not count)
+__device__ __forceinline__ int tree_depth(const AttnParams& a, int64_t token, int nodes) {
   int n = 0;
-  for (int w = 0; w < a.words; ++w) n += __popcll(__ldg(a.tree + token * a.words + w));
+  for (int w = 0; 64 * w < nodes; ++w)
+    n += __popcll(__ldg(a.tree + token * a.words + w) << max(0, 64 * w + 64 - nodes));
   return n;
 }
 
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
     auto last_key = [&](int r) { return (TREE ? 0 : s.len - s.n) + (row0 + min(r, rows - 1)) / a.rep; };
     auto first_key = [&](int hi) {
       if (a.window == 0) return 0;
-      const int64_t p = TREE ? (int64_t)s.len - s.n + tree_depth(a, s.first + hi) : (int64_t)hi + 1;
+      const int64_t p = TREE ? (int64_t)s.len - s.n + tree_depth(a, s.first + hi, s.n) : (int64_t)hi + 1;
       return (int)max((int64_t)0, p - a.window);
     };
     constexpr int NR = C::WIDE ? 1 : NT;
@@ -922,7 +925,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
       if (whole) {
         const int tok = (row0 + r) / a.rep, hr = row0 + r - tok * a.rep;
         const int64_t orow = (s.first + tok) * (int64_t)(a.heads * a.rep) + head * a.rep + hr;
-        if (TREE && tree_depth(a, s.first + tok) == 0) {
+        if (TREE && tree_depth(a, s.first + tok, s.n) == 0) {
           v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           sum = 0.0f;
         }
@@ -951,6 +954,7 @@ __global__ void __launch_bounds__(AW * 32, Cfg<D, NG, NT>::BLOCKS) attn_kv4_kern
         mm.parts = (int32_t)(owner - blockIdx.x + 1);
         mm.block = (int32_t)blockIdx.x;
         mm.slot = at != at0 ? 1 : 0;
+        mm.nodes = TREE ? (int16_t)s.n : 0;
         mm.head = head;
         mm.row0 = row0;
         mm.rows = rows;
@@ -985,7 +989,7 @@ __global__ void __launch_bounds__(256) attn_kv4_join_kernel(const AttnParams a) 
   auto store = [&](int r, float4 v, float sum, float mt) {
     const int tok = (row0 + r) / a.rep, hr = row0 + r - tok * a.rep;
     const int64_t orow = (mm.first + tok) * (int64_t)(a.heads * a.rep) + mm.head * a.rep + hr;
-    if (TREE && tree_depth(a, mm.first + tok) == 0) {
+    if (TREE && tree_depth(a, mm.first + tok, mm.nodes) == 0) {
       v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       sum = 0.0f;
     }

@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
 
       const int len = u.s.len, base = len - u.s.n;
       const int64_t token = u.s.first + tok;
-      const int depth = live ? tree_depth(a, token) : 0;
+      const int depth = live ? tree_depth(a, token, u.s.n) : 0;
       const int lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)base + depth - a.window) : 0;
       // every row sees the keys from all_begin to base
       const int all_begin = a.window > 0 ? (int)max((int64_t)0, (int64_t)len - a.window) : 0;

@@ -156,6 +156,27 @@ def test_masks_that_are_no_tree(n):
     assert torch.equal(out[dev(np.concatenate(live))], want[dev(np.concatenate(live))])
 
 
+@pytest.mark.parametrize("words", [1, 2])
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("n,columns", [(6, None), (6, 64), (40, None), (40, 64)])
+def test_bits_of_nodes_that_do_not_exist(n, columns, window, words):
+    """They are ignored: the same results, padding's zeros and the window's depth too."""
+    ns = [n, n - 1, max(1, n // 2)]
+    masks = trees(n, ns, padding=0.3)
+    masks[0][0] = False
+    c = make(26, [n + 30, 400, 130], ns, 8, 2, 128, 16, 64)
+    if columns:
+        c["table"] = np.pad(c["table"], [(0, 0), (0, columns - c["table"].shape[1])])
+    want, wlse = check(c, masks, window=window, words=words)
+    tree = O.words_of(masks, words).view(np.uint64)
+    for b, k in enumerate(ns):
+        past = np.array([(2 ** 64 - 1) << max(0, k - 64 * w) & (2 ** 64 - 1) for w in range(words)], np.uint64)
+        tree[c["cu"][b]:c["cu"][b + 1]] |= past
+    out, lse = bq.bq_attn_kv4_tree(dev(c["q"]), dev(c["codes"]), dev(c["params"]), dev(c["table"]), dev(c["lens"]),
+                                   dev(tree.view(np.int64)), cu_q=dev(c["cu"]), max_q=n, window=window, lse=True)
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
 @pytest.mark.parametrize("window", [1, 7, 64, 100, 1000])
 @pytest.mark.parametrize("n", [6, 40])
 def test_window(window, n):
