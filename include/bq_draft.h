@@ -91,12 +91,13 @@ bq_status bq_attn_kv4_tree(const uint16_t* q, int64_t ld_q, int64_t T, int64_t q
  *   and so does a row whose largest logit is +inf; logprob is then 0.
  *   k <= 0, p >= 1 (or NaN) and m <= 0 (or NaN) keep all; p <= 0 and m > 1
  *   keep the first one.
+ *   A logit that lies more than fp32's range below the largest has weight 0.
  *   -inf and NaN logits are never taken; a row of nothing else gives token -1
  *   and logprob -inf.
- *   Weights are held to 29 bits and 2**-44 of the largest, and summed exactly:
- *   the choice is that of the formula but where u times the sum, or a limit,
- *   lies within some 1e-10 of a border.  The same inputs give the same token,
- *   whatever the other rows are.
+ *   Weights are held to 2**-28 of themselves and 2**-44 of the largest, and
+ *   summed exactly: the choice is that of the formula but where u times the
+ *   sum, or a limit, lies within 2**-28 of the sum of a border.  The same
+ *   inputs give the same token, whatever the other rows are.
  *
  *   logits       device, R rows of V contiguous elements of type ltype
  *                (BQ_LOGITS_*), leading dimension ld >= V, element alignment

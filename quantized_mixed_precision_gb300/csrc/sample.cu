@@ -1097,7 +1097,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
     const double c = fmin(1.4426950408889634 / (double)heat, 1e30);
     sh.c_hi = (float)c;
     sh.c_lo = (float)(c - (double)sh.c_hi);
-    sh.reach = m > 0.0f && m <= 1.0f ? (double)heat * log((double)m) : 0.0;
+    // (an infinite temperature makes all weights 1, which min-p of 1 keeps)
+    sh.reach = m > 0.0f && m <= 1.0f ? (heat < INFINITY ? (double)heat * log((double)m) : -INFINITY) : 0.0;
   }
 
   Sampler<T> p(sh, row, blocks, rank);
@@ -1109,7 +1110,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   int listed = 0;
   if (some) {
     __syncthreads();
-    top = p.candidates(heat * logf(m), listed);
+    top = p.candidates(heat < INFINITY ? heat * logf(m) : -INFINITY, listed);
   } else if (counts) {
     row.each([&](float x, int) {
       top = fmaxf(top, x);

@@ -159,6 +159,16 @@ def test_settings_at_the_edges():
     assert flat.tolist() == [int(v * 777) for v in np.float32(u)] and (lp + np.log(777)).abs().max() < 1e-6
 
 
+@pytest.mark.parametrize("v", [777, 20000])
+def test_infinite_temperature_with_limits(v):
+    x = logits(7, 8, v, "f16")
+    u = np.linspace(0.01, 0.99, 8)
+    t = [float("inf")] * 8
+    check(x, u, t=t, m=[1.0, 0.5, 1e-30, 2.0, 1.0, 1.0, 0.9, 0.0])
+    check(x, u, t=t, m=[1.0, 0.5, 1e-30, 2.0, 1.0, 1.0, 0.9, 0.0], k=[0, 3, 100, 5, 1, 50, v, 2 * v])
+    check(x, u, t=t, m=[1.0, 0.5, 1e-30, 2.0, 1.0, 1.0, 0.9, 0.0], p=[0.3, 0.001, 0.77, 0.5, 0.9, 1.0, 0.0, 0.6])
+
+
 @pytest.mark.parametrize("dtype", sorted(TYPES))
 @pytest.mark.parametrize("shift", [0, 1, 3, 5])
 def test_strides_and_alignment(dtype, shift):
