@@ -37,7 +37,7 @@ constexpr int FRAC = 44;                     // bits of a weight below the large
 constexpr float Y_MOST = FRAC + 2.0f;        // from here on a weight is 0
 constexpr int BINS = 2048, EACH = BINS / THREADS;
 constexpr int LIST = 2048;                   // gathered tokens
-constexpr int QUEUE = 32 * 9;                // of a warp: a step of 8 elements a lane, and less than 32 before it
+constexpr int QUEUE = 16;                    // of a lane: a step of 8 elements, and 8 before it
 // Up to so many first tokens, those are gathered, and the other filters and the choice are made among them alone.  That and a
 // second pass over the row, with top-p: 1 x 50021 fp32 at 50 tokens 26.5 and 36.9 us, 200 34 and 39, 400 42 and 39; 64 x
 // 131072 fp16 at 50 42 and 60, 200 52 and 62, 400 62 and 65, 1000 98 and 68.
@@ -172,12 +172,12 @@ struct __align__(16) Shared {
   };
   uint64_t all_w[LIST];
   uint16_t tie[LIST];              // entries of the list
-  float queue[WARPS][QUEUE];       // tokens of a warp whose weights are to be summed
+  float queue[WARPS][QUEUE][32];   // tokens of a lane whose weights are to be summed
   int n[2];                        // gathered by the block, two lists in turn
   uint32_t largest;                // key of the largest logit so far
   float c_hi, c_lo;
   double reach;                    // temperature times ln of min_p
-  int found;
+  int found;                       // the warp of the block with the chosen token (-1: none)
   uint64_t reached;
   uint32_t scan[WARPS];
   float scan_lo[WARPS], scan_hi[WARPS];
@@ -233,22 +233,25 @@ struct Row {
   const uint4* base;       // the boundary at or before it
   int V, shift;            // elements from there to the row
   int first, last;         // this warp's steps
+  int per, all;            // steps of a warp, and of the row
   int lane;
 
   __device__ Row(const T* x_, int V_, int warp, int warps, int lane_) : x(x_), V(V_), lane(lane_) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(x);
     base = reinterpret_cast<const uint4*>(a & ~uintptr_t(15));
     shift = (int)((a & 15) / sizeof(T));
-    const int steps = (V + shift + E - 1) / E, per = (steps + warps - 1) / warps;
-    first = min(warp * per, steps);
-    last = min(first + per, steps);
+    all = (V + shift + E - 1) / E;
+    per = (all + warps - 1) / warps;
+    first = min(warp * per, all);
+    last = min(first + per, all);
   }
   // The 16 bytes of step s, where they are all of the row.  (An ordinary load: one of read-only data may be moved in front
   // of the wait for the kernel before, which writes the logits.)
   __device__ __forceinline__ bool whole(int s) const { return s * E >= shift && s * E - shift + E <= V; }
-  __device__ __forceinline__ uint4 fetch(int s) const {
-    return s < last && whole(s) ? base[s] : make_uint4(0, 0, 0, 0);
+  __device__ __forceinline__ uint4 fetch(int s, int end) const {
+    return s < end && whole(s) ? base[s] : make_uint4(0, 0, 0, 0);
   }
+  __device__ __forceinline__ uint4 fetch(int s) const { return fetch(s, last); }
   // Elements of step s, which has been fetched: index of the first, values (-inf where there is none)
   __device__ __forceinline__ int take(int s, const uint4& w, float (&v)[E]) const {
     const int i = s * E - shift;
@@ -360,13 +363,6 @@ struct Sampler {
     constexpr float WHOLE = 8388608.0f;
     return min(__float_as_int(fmaf(y, bins, WHOLE)) - __float_as_int(WHOLE), BINS - 1);
   }
-  // The weight of a token in bin b as a part of 4096 of the bin's largest, 2**-((b - 1/2) / bins): a bin is at most 1.6 %
-  // wide, and a straight line is good to 2**-13 over it.  (2**19 of them fit 32 bits.)
-  __device__ __forceinline__ uint32_t part_of(float y, int b) const {
-    const float f = __fadd_rn(fmaf(y, bins, -(float)b), 0.5f);
-    return (uint32_t)__float2int_rn(fmaf(f, slope, 4096.0f));
-  }
-
   // Every warp's share of a sum, exchanged: f(share of warp i of the row) for this lane's i.  One barrier; the next
   // exchange may follow at once.
   template <class F>
@@ -384,9 +380,9 @@ struct Sampler {
     exchange(warp_sum(v), [&](int, uint64_t w) { t += w; });
     return warp_sum(t);
   }
-  // The weights of this warp's tokens that `in` names, as each lane's share.  A token's weight is some 30 instructions:
-  // where few are named, a lane with one would have the others wait, so that they wait in a queue until every lane has
-  // one (FEW).
+  // The weights of this warp's tokens that `in` names, as each lane's share.  A token's weight is some 20 instructions:
+  // where few are named, a lane with one would have the others wait, so that they wait in a lane's queue until one of those
+  // is half full (FEW).
   template <bool FEW, class F>
   __device__ __forceinline__ uint64_t weigh(F in) {
     constexpr int E = Row<T>::E;
@@ -395,13 +391,6 @@ struct Sampler {
       row.template steps<2>([&](int step, const uint4& w) {
         float v[E];
         const int i = row.take(step, w, v);
-        // (with a cut many steps have nothing that counts)
-        if (cut.x > -INFINITY) {
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (in(v[e], i + e)) sum += w_of(v[e]);
-          return;
-        }
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
           const float x0 = in(v[e], i + e) ? v[e] : -INFINITY, x1 = in(v[e + 1], i + e + 1) ? v[e + 1] : -INFINITY;
@@ -410,44 +399,60 @@ struct Sampler {
       });
     } else {
       int n = 0;
-      float* const q = sh.queue[warp];
+      float(*const q)[32] = sh.queue[warp];
+      // two tokens of every lane that has some
+      auto two = [&] {
+        const float x0 = n > 0 ? q[n - 1][lane] : -INFINITY, x1 = n > 1 ? q[n - 2][lane] : -INFINITY;
+        n = max(n - 2, 0);
+        sum += weights2<WIDE>(x0, x1, s, sh.table);
+      };
       uint4 w0 = row.fetch(row.first + lane), w1 = row.fetch(row.first + lane + 32);
       for (int s0 = row.first; s0 < row.last; s0 += 32) {
         const uint4 w2 = row.fetch(s0 + lane + 64);
-        float v[E];
-        int i = 0;
-        uint32_t named = 0;
         if (s0 + lane < row.last) {
-          i = row.take(s0 + lane, w0, v);
+          float v[E];
+          const int i = row.take(s0 + lane, w0, v);
 #pragma unroll
-          for (int e = 0; e < E; ++e) named |= in(v[e], i + e) ? 1u << e : 0;
+          for (int e = 0; e < E; ++e)
+            if (in(v[e], i + e)) q[n++][lane] = v[e];
         }
-        // places by lane: an inclusive sum of the lanes' numbers
-        const int mine = __popc(named);
-        int at = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int up = __shfl_up_sync(0xffffffffu, at, o);
-          if (lane >= o) at += up;
-        }
-        const int all = __shfl_sync(0xffffffffu, at, 31);
-        at += n - mine;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (named >> e & 1) q[at++] = v[e];
-        n += all;
-        __syncwarp();
-        while (n >= 32) {
-          n -= 32;
-          sum += w_of(q[n + lane]);
-        }
-        __syncwarp();
+        while (__any_sync(0xffffffffu, n > QUEUE - E)) two();
         w0 = w1;
         w1 = w2;
       }
-      if (lane < n) sum += w_of(q[lane]);
-      __syncwarp();
+      while (__any_sync(0xffffffffu, n > 0)) two();
     }
+    return sum;
+  }
+  // The weights of what `cut` keeps, as each lane's share, and in `hist` their sums by bin: a token's as a part of 4096 of
+  // the bin's largest, 2**-((b - 1/2) / bins).  (A bin is at most 1.6 % wide, and a straight line is good to 2**-13 over it;
+  // 2**19 of them fit 32 bits.)  Two at a time, with packed fp32.
+  __device__ __forceinline__ uint64_t weigh_and_count() {
+    constexpr int E = Row<T>::E;
+    constexpr float WHOLE = 8388608.0f, NEAREST = 12582912.0f;
+    const float middle = 4096.0f + 0.5f * slope;
+    uint64_t sum = 0;
+    row.template steps<2>([&](int step, const uint4& w) {
+      float v[E];
+      const int i = row.take(step, w, v);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float x0 = kept(cut, v[e], i + e) ? v[e] : -INFINITY, x1 = kept(cut, v[e + 1], i + e + 1) ? v[e + 1] : -INFINITY;
+        sum += weights2<WIDE>(x0, x1, s, sh.table);
+        const P2 y = mul2(fma2(p2(x0, x1), p2(-1.0f, -1.0f), p2(s.top, s.top)), p2(s.c_hi, s.c_hi));      // y_of
+        const P2 b = fma2(y, p2(bins, bins), p2(WHOLE, WHOLE));
+        const P2 f = fma2(y, p2(bins, bins), fma2(b, p2(-1.0f, -1.0f), p2(WHOLE, WHOLE)));
+        const float2 part = f2(add2(fma2(f, p2(slope, slope), p2(middle, middle)), p2(NEAREST, NEAREST)));
+        const float2 at = f2(b), where = f2(y);
+        auto count = [&](float y, float at, float part) {
+          if (y < Y_MOST)
+            atomicAdd(&sh.hist[min(__float_as_int(at) - __float_as_int(WHOLE), BINS - 1)],
+                      __float_as_int(part) - __float_as_int(NEAREST));
+        };
+        count(where.x, at.x, part.x);
+        count(where.y, at.y, part.y);
+      }
+    });
     return sum;
   }
   // A round of exchanges within the block: every warp's value, lane i has warp i's.  One barrier.
@@ -1093,6 +1098,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   // (64-bit arithmetic is slow here: one thread's part for the block)
   if (tid == THREADS - 1) {
     sh.n[0] = sh.n[1] = 0;
+    sh.found = -1;
     sh.largest = KEY_LOWEST;
     const double c = fmin(1.4426950408889634 / (double)heat, 1e30);
     sh.c_hi = (float)c;
@@ -1261,14 +1267,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   if (share <= 0.0f) {
     p.cut = Cut{top, p.nth(top, 1)};
   } else if (share < 1.0f) {
-    uint64_t w = p.row_sum(p.template weigh<false>([&](float x, int i) {
-      if (!kept(p.cut, x, i)) return false;
-      const float y = p.y_of(x);
-      if (!(y < Y_MOST)) return false;
-      const int b = p.bin_of(y);
-      atomicAdd(&sh.hist[b], p.part_of(y, b));
-      return true;
-    }));
+    const uint64_t w = p.row_sum(p.weigh_and_count());
     p.cut = strictest(p.cut, p.template descend<true>(times(share, w, true)));
   }
   if (m > 1.0f) {
@@ -1289,43 +1288,67 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   });
   before = warp_sum(before);
   total = warp_sum(total);
+  // the warp with it leaves its steps to its block's warps, an equal part each
   uint64_t at = part_of_sum(u, total);
-  if (at >= before && at < before + mine) {
-    at -= before;
-    for (int s0 = row.first; s0 < row.last; s0 += 32) {
-      constexpr int E = Row<T>::E;
+  if (lane == 0 && at >= before && at < before + mine) {
+    sh.found = warp;
+    sh.reached = at - before;
+  }
+  __syncthreads();
+  if (sh.found >= 0) {
+    constexpr int E = Row<T>::E;
+    const int from = (rank * WARPS + sh.found) * row.per, to = min(from + row.per, row.all);
+    const int part = (to - from + WARPS - 1) / WARPS, s1 = min(from + (warp + 1) * part, to);
+    const int s0 = min(from + warp * part, s1);
+    uint64_t w = 0;
+    for (int step = s0 + lane; step < s1; step += 32) {
       float v[E];
-      int i = 0;
-      uint64_t w = 0;
-      if (s0 + lane < row.last) {
-        i = row.take(s0 + lane, row.fetch(s0 + lane), v);
+      const int i = row.take(step, row.fetch(step, s1), v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) w += kept(p.cut, v[e], i + e) ? p.w_of(v[e]) : 0;
-      }
-      uint64_t sum = w;
+      for (int e = 0; e < E; ++e) v[e] = kept(p.cut, v[e], i + e) ? v[e] : -INFINITY;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t up = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += up;
-      }
-      const uint64_t step = __shfl_sync(0xffffffffu, sum, 31);
-      if (at < step) {
-        if (at < sum && at >= sum - w) {
-          uint64_t run = sum - w;
-          bool done = false;
+      for (int e = 0; e < E; e += 2) w += weights2<Sampler<T>::WIDE>(v[e], v[e + 1], p.s, sh.table);
+    }
+    w = warp_sum(w);
+    at = sh.reached;
+    const uint64_t sums = p.within(w);
+    before = warp_sum(lane < warp ? sums : 0);
+    if (at >= before && at < before + w) {
+      at -= before;
+      for (int step = s0 + lane; step - lane < s1; step += 32) {
+        float v[E];
+        int i = 0;
+        uint64_t w = 0;
+        if (step < s1) {
+          i = row.take(step, row.fetch(step, s1), v);
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            run += kept(p.cut, v[e], i + e) ? p.w_of(v[e]) : 0;
-            if (!done && at < run) {
-              done = true;
-              a.tokens[r] = i + e;
-              if (a.logprob) a.logprob[r] = log_share(top, v[e], heat, total);
+          for (int e = 0; e < E; ++e) w += kept(p.cut, v[e], i + e) ? p.w_of(v[e]) : 0;
+        }
+        uint64_t sum = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint64_t up = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += up;
+        }
+        const uint64_t all = __shfl_sync(0xffffffffu, sum, 31);
+        if (at < all) {
+          if (at < sum && at >= sum - w) {
+            uint64_t run = sum - w;
+            bool done = false;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              run += kept(p.cut, v[e], i + e) ? p.w_of(v[e]) : 0;
+              if (!done && at < run) {
+                done = true;
+                a.tokens[r] = i + e;
+                if (a.logprob) a.logprob[r] = log_share(top, v[e], heat, total);
+              }
             }
           }
+          break;
         }
-        break;
+        at -= all;
       }
-      at -= step;
     }
   }
   p.sync();                                  // (the others may still read this block's shared memory)
