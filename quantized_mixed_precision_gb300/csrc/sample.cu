@@ -79,9 +79,9 @@ __constant__ uint64_t ROOTS[32] = {
     0xa5fed6a9b15138full, 0xa27043030c49682ull, 0x9ef5326091a111bull, 0x9b8d39b9d54e554ull,
     0x9837f0518db8a97ull, 0x94f4efa8fef7096ull, 0x91c3d373ab11c33ull, 0x8ea4398b45cd53cull,
     0x8b95c1e3ea8bd6eull, 0x88980e8092da852ull, 0x85aac367cc487b1ull, 0x82cd8698ac2ba1dull};
-// The same in shared memory, and as fp32.
+// The same in shared memory, and as fp32.  (32 words each: lanes that read different ones never meet in a bank.)
 struct Table {
-  uint64_t fixed[32];
+  uint32_t lo[32], hi[32];
   float value[32];
 };
 
@@ -114,18 +114,19 @@ __device__ __forceinline__ uint64_t weight(float x, const Scale& s, const Table&
   const int j = k & 31, n = k >> 5;
   constexpr float WHOLE = 12582912.0f;                          // 1.5 * 2**23: its ulp is 1
   const float q = fmaf(__fmul_rn(d, t.value[j]), 268435456.0f, WHOLE);
-  const int64_t m = (int64_t)t.fixed[j] + ((int64_t)(__float_as_int(q) - __float_as_int(WHOLE)) << 32);
-  return (uint64_t)m >> (60 - FRAC + n);
+  const uint32_t m = t.hi[j] + (uint32_t)(__float_as_int(q) - __float_as_int(WHOLE));
+  return ((uint64_t)m << 32 | t.lo[j]) >> (60 - FRAC + n);
 }
 
 // The same for two tokens at once, summed: packed fp32 for all but the integers.  Nothing is decided on the way: a logit that
-// counts for nothing (-inf, NaN, 46 binary orders below the largest) has y = 47, whose weight is shifted out.
+// counts for nothing (-inf, NaN, 46 binary orders below the largest) has its weight shifted out, those from 64 orders on by
+// more than 64 bits, so that it does not matter what was made of them.
 template <bool WIDE>
 __device__ __forceinline__ uint64_t weights2(float x0, float x1, const Scale& s, const Table& t) {
   const P2 top = p2(s.top, s.top), c = p2(s.c_hi, s.c_hi), one = p2(-1.0f, -1.0f), x = p2(x0, x1);
   const P2 hi = fma2(x, one, top);                              // (exact products: ordinary differences)
   const float2 y = f2(mul2(hi, c));
-  const P2 p = p2(fminf(y.x, FRAC + 3.0f), fminf(y.y, FRAC + 3.0f));
+  const P2 p = p2(fminf(y.x, 64.0f), fminf(y.y, 64.0f));
   const P2 minus = fma2(p, one, p2(-0.0f, -0.0f));
   P2 e = fma2(hi, c, minus);
   e = fma2(hi, p2(s.c_lo, s.c_lo), e);
@@ -146,12 +147,15 @@ __device__ __forceinline__ uint64_t weights2(float x0, float x1, const Scale& s,
   constexpr float WHOLE = 12582912.0f;
   const P2 v = mul2(d, p2(t.value[a0 & 31], t.value[a1 & 31]));
   const float2 q = f2(fma2(v, p2(268435456.0f, 268435456.0f), p2(WHOLE, WHOLE)));
-  // (where y was cut to 47, e is what was cut off, and what becomes of it does not matter)
-  auto one_of = [&](uint32_t a, float q, float y) {
-    const int64_t m = (int64_t)t.fixed[a & 31] + ((int64_t)(__float_as_int(q) - __float_as_int(WHOLE)) << 32);
-    return y < FRAC + 2.0f ? (uint64_t)m >> ((a >> 5) & 63) : 0;
+  auto one_of = [&](uint32_t a, float q) {
+    const uint32_t j = a & 31, m = t.hi[j] + (uint32_t)(__float_as_int(q) - __float_as_int(WHOLE));
+    uint64_t w;
+    asm("{\n\t.reg .b64 m;\n\tmov.b64 m, {%1, %2};\n\tshr.u64 %0, m, %3;\n\t}"      // (0 for 64 bits or more)
+        : "=l"(w)
+        : "r"(t.lo[j]), "r"(m), "r"((a >> 5) & 127));
+    return w;
   };
-  return one_of(a0, q.x, y.x) + one_of(a1, q.y, y.y);
+  return one_of(a0, q.x) + one_of(a1, q.y);
 }
 
 // Shared memory of a block
@@ -380,53 +384,54 @@ struct Sampler {
     exchange(warp_sum(v), [&](int, uint64_t w) { t += w; });
     return warp_sum(t);
   }
-  // The weights of this warp's tokens that `in` names, as each lane's share.  A token's weight is some 20 instructions:
-  // where few are named, a lane with one would have the others wait, so that they wait in a lane's queue until one of those
-  // is half full (FEW).
-  template <bool FEW, class F>
+  // The weights of all of this warp's tokens, as each lane's share
+  __device__ __forceinline__ uint64_t weigh_all() {
+    constexpr int E = Row<T>::E;
+    uint64_t sum = 0;
+    row.template steps<2>([&](int step, const uint4& w) {
+      float v[E];
+      row.take(step, w, v);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) sum += weights2<WIDE>(v[e], v[e + 1], s, sh.table);
+    });
+    return sum;
+  }
+  // The same of those that `in` names.  A token's weight is some 20 instructions: where few are named, a lane with one would
+  // have the others wait, so that they wait in a lane's queue until one of those is half full.
+  template <class F>
   __device__ __forceinline__ uint64_t weigh(F in) {
     constexpr int E = Row<T>::E;
     uint64_t sum = 0;
-    if constexpr (!FEW) {
-      row.template steps<2>([&](int step, const uint4& w) {
+    int n = 0;
+    float(*const q)[32] = sh.queue[warp];
+    // two tokens of every lane that has some
+    auto two = [&] {
+      const float x0 = n > 0 ? q[n - 1][lane] : -INFINITY, x1 = n > 1 ? q[n - 2][lane] : -INFINITY;
+      n = max(n - 2, 0);
+      sum += weights2<WIDE>(x0, x1, s, sh.table);
+    };
+    uint4 w0 = row.fetch(row.first + lane), w1 = row.fetch(row.first + lane + 32);
+    for (int s0 = row.first; s0 < row.last; s0 += 32) {
+      const uint4 w2 = row.fetch(s0 + lane + 64);
+      if (s0 + lane < row.last) {
         float v[E];
-        const int i = row.take(step, w, v);
+        const int i = row.take(s0 + lane, w0, v);
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float x0 = in(v[e], i + e) ? v[e] : -INFINITY, x1 = in(v[e + 1], i + e + 1) ? v[e + 1] : -INFINITY;
-          sum += weights2<WIDE>(x0, x1, s, sh.table);
-        }
-      });
-    } else {
-      int n = 0;
-      float(*const q)[32] = sh.queue[warp];
-      // two tokens of every lane that has some
-      auto two = [&] {
-        const float x0 = n > 0 ? q[n - 1][lane] : -INFINITY, x1 = n > 1 ? q[n - 2][lane] : -INFINITY;
-        n = max(n - 2, 0);
-        sum += weights2<WIDE>(x0, x1, s, sh.table);
-      };
-      uint4 w0 = row.fetch(row.first + lane), w1 = row.fetch(row.first + lane + 32);
-      for (int s0 = row.first; s0 < row.last; s0 += 32) {
-        const uint4 w2 = row.fetch(s0 + lane + 64);
-        if (s0 + lane < row.last) {
-          float v[E];
-          const int i = row.take(s0 + lane, w0, v);
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (in(v[e], i + e)) q[n++][lane] = v[e];
-        }
-        while (__any_sync(0xffffffffu, n > QUEUE - E)) two();
-        w0 = w1;
-        w1 = w2;
+        for (int e = 0; e < E; ++e)
+          if (in(v[e], i + e)) q[n++][lane] = v[e];
       }
-      while (__any_sync(0xffffffffu, n > 0)) two();
+      while (__any_sync(0xffffffffu, n > QUEUE - E)) two();
+      w0 = w1;
+      w1 = w2;
     }
+    while (__any_sync(0xffffffffu, n > 0)) two();
     return sum;
   }
   // The weights of what `cut` keeps, as each lane's share, and in `hist` their sums by bin: a token's as a part of 4096 of
   // the bin's largest, 2**-((b - 1/2) / bins).  (A bin is at most 1.6 % wide, and a straight line is good to 2**-13 over it;
   // 2**19 of them fit 32 bits.)  Two at a time, with packed fp32.
+  // (ALL: nothing is cut off, and what weighs nothing needs no look.)
+  template <bool ALL>
   __device__ __forceinline__ uint64_t weigh_and_count() {
     constexpr int E = Row<T>::E;
     constexpr float WHOLE = 8388608.0f, NEAREST = 12582912.0f;
@@ -437,7 +442,8 @@ struct Sampler {
       const int i = row.take(step, w, v);
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
-        const float x0 = kept(cut, v[e], i + e) ? v[e] : -INFINITY, x1 = kept(cut, v[e + 1], i + e + 1) ? v[e + 1] : -INFINITY;
+        const float x0 = ALL || kept(cut, v[e], i + e) ? v[e] : -INFINITY;
+        const float x1 = ALL || kept(cut, v[e + 1], i + e + 1) ? v[e + 1] : -INFINITY;
         sum += weights2<WIDE>(x0, x1, s, sh.table);
         const P2 y = mul2(fma2(p2(x0, x1), p2(-1.0f, -1.0f), p2(s.top, s.top)), p2(s.c_hi, s.c_hi));      // y_of
         const P2 b = fma2(y, p2(bins, bins), p2(WHOLE, WHOLE));
@@ -940,7 +946,7 @@ struct Sampler {
       }
       return false;
     };
-    share = warp_sum(weigh<true>(gather));
+    share = warp_sum(weigh(gather));
     uint64_t over = 0;
     exchange(share, [&](int, uint64_t w) { over += w; });
     need -= MASS ? warp_sum(over) : before;
@@ -1088,7 +1094,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   const int V = (int)a.V;
   const Row<T> row(static_cast<const T*>(a.logits) + r * a.ld, V, rank * WARPS + warp, blocks * WARPS, lane);
   if (tid < 32) {
-    sh.table.fixed[tid] = ROOTS[tid];
+    sh.table.lo[tid] = (uint32_t)ROOTS[tid];
+    sh.table.hi[tid] = (uint32_t)(ROOTS[tid] >> 32);
     sh.table.value[tid] = (float)ROOTS[tid] * (1.0f / 1152921504606846976.0f);     // 2**60
   }
   for (int i = tid; i < BINS; i += THREADS) sh.hist[i] = 0;
@@ -1267,7 +1274,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   if (share <= 0.0f) {
     p.cut = Cut{top, p.nth(top, 1)};
   } else if (share < 1.0f) {
-    const uint64_t w = p.row_sum(p.weigh_and_count());
+    const uint64_t w = p.row_sum(p.cut.x > -INFINITY ? p.template weigh_and_count<false>() : p.template weigh_and_count<true>());
     p.cut = strictest(p.cut, p.template descend<true>(times(share, w, true)));
   }
   if (m > 1.0f) {
@@ -1280,7 +1287,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   auto in = [&](float x, int i) { return kept(p.cut, x, i); };
   uint64_t mine = p.share;
   if (p.cut.x != p.known.x || p.cut.last != p.known.last)
-    mine = warp_sum(p.cut.x > -INFINITY ? p.template weigh<true>(in) : p.template weigh<false>(in));
+    mine = warp_sum(p.cut.x > -INFINITY ? p.weigh(in) : p.weigh_all());
   uint64_t before = 0, total = 0;
   p.exchange(mine, [&](int i, uint64_t w) {
     before += i < rank * WARPS + warp ? w : 0;
