@@ -23,6 +23,15 @@
 //
 // The tiles of all units are dealt out to the blocks in equal contiguous ranges; a
 // unit that falls into several is joined by a second kernel.
+//
+// What bounds it.  A tile takes a block some 4300 cycles, with 128 rows as with 256:
+// the products need 1000 or 2000 of them (and as much again where the tensor
+// cores wait for shared memory that the converters write), the exponentials as
+// many, and a slot's scores, weights and product wait for each other.  64 nodes on
+// 131071 keys, 256 rows a kv head: 131 us, 56 % of the measured rate of the tensor
+// cores; 16 sequences of up to 16384: 173 us, 45 %; 32 nodes on up to 4099 keys, 128
+// rows: 54 us, of which some 10 are start and join.  Memory is not the limit (1.1 TB/s).
+// Twice as many converting warps gave 55 us.
 #include "attn_kv4.cuh"
 #include "draft_internal.h"
 #include "gemm_common.cuh"
@@ -919,10 +928,15 @@ cudaError_t launch_both(const TreeParams& p, cudaStream_t stream) {
 
 }  // namespace
 
+// More than 32 rows a kv head; of a short cache's, whose direct form has no scan and no join, more than six blocks of 8 rows an
+// SM.  That form and this one, in us: 16 sequences of 4096 keys, 8 kv heads, D 128: 16 rows 37 and 56, 32 rows 58 and 56,
+// 48 rows 90 and 56, 128 rows 167 and 61; 1 of 32768: 24 rows 36 and 37, 48 rows 51 and 37; 8 of 3000, 4 kv heads, D 64:
+// 28 rows 22 and 22, 42 rows 26 and 22; 1 of 500: 128 rows 8.0 and 17.6; 16 of 500: 48 rows (768 blocks) 15.5 and 18.3, 64 rows
+// (1024) 21 and 18.4, 128 rows 40 and 19.4.  (D = 256 has no room for its outputs beside two slots of scores.)
 bool attn_tree_tc_applies(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_len) {
   const int64_t rows = q_heads / kv_heads * max_q;
   if (D > 128 || rows <= 32 || max_len == 0) return false;
-  return max_len > DIRECT_LEN || B * kv_heads * ((rows + 7) / 8) > 3 * sm_count();
+  return max_len > DIRECT_LEN || B * kv_heads * ((rows + 7) / 8) > 6 * sm_count();
 }
 
 size_t attn_tree_tc_workspace(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q) {

@@ -12,7 +12,8 @@
 //
 // What bounds it: latency (loads of the tree, of tokens, of targets at
 // parents, of pages, of lines, one behind the other); the lines themselves are
-// a few MB.
+// a few MB.  64 trees of 64 nodes in the caches of 32 layers take 11 us (0.8 TB/s of lines),
+// 13 trees in 7 layers 7.5, which is the host's part of a call.
 #include "bq_device.cuh"
 #include "draft_internal.h"
 #include "kv4_device.cuh"

@@ -21,6 +21,16 @@
 // A cluster of 1 to 8 blocks takes a row: its sums, counts and gathered tokens are
 // exchanged through distributed shared memory, and every block decides for
 // itself, on the same numbers.
+//
+// What bounds it.  Many rows: instructions, above all those of the integer pipe (some 30
+// of them a token, 512 x 131072 fp16 without limits 103 us, the
+// largest alone 35; a copy of the logits' bytes would take 20).  With top-p the
+// weights are formed a second time for what may be kept, beside the counts (64 x
+// 131072 fp16 67 us, 37 x 50021 fp32 with all kinds of limits 46).  With min-p its tokens come
+// with the pass for the largest, 57 us at 512 x 131072 fp16, and where they are
+// thousands the kept ones' weights with another (89 us with such rows among them).
+// Few rows: a dozen of the cluster's barriers, one behind the other (1 x 32768, all
+// limits: 24 to 31 us, by the first tokens asked for).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -39,11 +49,11 @@ constexpr int BINS = 2048, EACH = BINS / THREADS;
 constexpr int LIST = 2048;                   // gathered tokens
 constexpr int QUEUE = 16;                    // of a lane: a step of 8 elements, and 8 before it
 // Up to so many first tokens, those are gathered, and the other filters and the choice are made among them alone.  That and a
-// second pass over the row, with top-p: 1 x 50021 fp32 at 50 tokens 26.5 and 36.9 us, 200 34 and 39, 400 42 and 39; 64 x
-// 131072 fp16 at 50 42 and 60, 200 52 and 62, 400 62 and 65, 1000 98 and 68.
+// second pass over the row, with top-p: 1 x 50021 fp32 at 50 tokens 27 and 37 us, 200 35 and 38, 400 42 and 38; 64 x
+// 131072 fp16 at 50 43 and 65, 200 53 and 67, 400 63 and 69, 1000 99 and 71.
 constexpr int FEW = 256;
 constexpr int MOST_BLOCKS = 8;
-constexpr int LIGHT = 4;                     // steps on their way in passes that do little
+constexpr int LIGHT = 4;                     // steps on their way in passes that do little (greedy, 512 x 131072 fp16: 35 us; with 2, 49)
 
 // Keys of fp32 values: unsigned integers of the same order.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -1361,16 +1371,24 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(const SampleArgs a, 
   p.sync();                                  // (the others may still read this block's shared memory)
 }
 
-// Blocks that share a row: as many as keep the GPU busy (two blocks an SM), each with 4096 logits or more.
-inline int row_blocks(int64_t R, int64_t V) {
+// Blocks that share a row: as many as give an SM one, each with 4096 logits or more; and two an SM where they read 128 KB or
+// more each.  Top-p, two an SM and one, in us: 64 x 131072 fp32 (128 KB) 63 and 68, fp16 (64 KB) 56 and 54; 128 x 32768
+// fp32 39 and 38, fp16 36 and 33.  Not where clusters might have to wait for a place among SMs that are near each other: 37
+// clusters of 8, which are 296 blocks, take 54 us at 50021 logits, 37 of 4 take 37.
+inline int row_blocks(int64_t R, int64_t V, int size) {
   int blocks = 1;
-  while (blocks < MOST_BLOCKS && R * blocks * 2 <= 2 * sm_count() && V >= blocks * 2 * 4096) blocks *= 2;
+  while (blocks < MOST_BLOCKS && V >= blocks * 2 * 4096) {
+    const int64_t all = R * blocks * 2;
+    const bool two = blocks * 2 <= MOST_BLOCKS / 2 && V * size >= blocks * 2 * (128 << 10) && 4 * all <= 7 * sm_count();
+    if (all > sm_count() && !two) break;
+    blocks *= 2;
+  }
   return blocks;
 }
 
 template <class T>
 cudaError_t launch(const SampleArgs& a, cudaStream_t stream) {
-  const int blocks = row_blocks(a.R, a.V);
+  const int blocks = row_blocks(a.R, a.V, sizeof(T));
   cudaError_t e = set_smem_once(sample_kernel<T>, (int)sizeof(Shared));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
