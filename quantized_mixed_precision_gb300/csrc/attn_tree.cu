@@ -28,10 +28,10 @@
 // the products need 1000 or 2000 of them (and as much again where the tensor
 // cores wait for shared memory that the converters write), the exponentials as
 // many, and a slot's scores, weights and product wait for each other.  64 nodes on
-// 131071 keys, 256 rows a kv head: 131 us, 56 % of the measured rate of the tensor
-// cores; 16 sequences of up to 16384: 173 us, 45 %; 32 nodes on up to 4099 keys, 128
-// rows: 54 us, of which some 10 are start and join.  Memory is not the limit (1.1 TB/s).
-// Twice as many converting warps gave 55 us.
+// 131071 keys, 256 rows a kv head: 132 us, 56 % of the measured rate of the tensor
+// cores; 16 sequences of up to 16384: 174 us, 45 %; 32 nodes on up to 4099 keys, 128
+// rows: 55 us, of which some 10 are start and join.  Memory is not the limit (1.1 TB/s).
+// Twice as many converting warps gave 55 us, codes on their way for a tile more 56.
 #include "attn_kv4.cuh"
 #include "draft_internal.h"
 #include "gemm_common.cuh"
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1) attn_tree_kernel(const TreePa
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // (Below, inputs are loaded as read-only data.  None of those loads can move in front of the wait: their addresses depend on
   // lengths and pages that are loaded behind it.  As ordinary loads of queries and bits alone, which stay in order with
-  // the stores around them, 16 sequences of 4k keys with 32 nodes take 71 us, not 54.)
+  // the stores around them, 16 sequences of 4k keys with 32 nodes take 71 us, not 55.)
 
   // ---- which tiles are ours: equal shares, not less than `least` tiles each ----
   {

@@ -22,15 +22,16 @@
 // exchanged through distributed shared memory, and every block decides for
 // itself, on the same numbers.
 //
-// What bounds it.  Many rows: instructions, above all those of the integer pipe (some 30
-// of them a token, 512 x 131072 fp16 without limits 103 us, the
-// largest alone 35; a copy of the logits' bytes would take 20).  With top-p the
-// weights are formed a second time for what may be kept, beside the counts (64 x
-// 131072 fp16 67 us, 37 x 50021 fp32 with all kinds of limits 46).  With min-p its tokens come
-// with the pass for the largest, 57 us at 512 x 131072 fp16, and where they are
-// thousands the kept ones' weights with another (89 us with such rows among them).
-// Few rows: a dozen of the cluster's barriers, one behind the other (1 x 32768, all
-// limits: 24 to 31 us, by the first tokens asked for).
+// What bounds it.  Many rows: instructions, some 30 a token, above all those of
+// the integer pipe (512 x 131072 fp16 without limits 103 us, the largest alone 35;
+// a copy of the logits' bytes would take 20).  With top-p the weights of what may
+// be kept are formed a second time, beside the counts (64 x 131072 fp16 67 to 70
+// us, four warps a scheduler, issue 39 %; 37 x 50021 fp32 with all kinds of limits
+// 46).  With min-p its tokens come with the pass for the largest, 57 us at 512 x
+// 131072 fp16, and where they are thousands the kept ones' weights with another
+// (87 us with such rows among them).  Few rows: a dozen of the cluster's barriers,
+// one behind the other (1 x 32768, all limits: 24 to 31 us, by the first tokens
+// asked for).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
