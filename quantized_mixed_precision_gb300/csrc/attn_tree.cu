@@ -11,7 +11,7 @@
 // key, which is K-major for the first product and MN-major for the second.
 // (Their rounding to fp16 is a choice: results lie 5e-4 to 6e-4 from the formula's, of which the keys' rounding is 3.4e-4, the
 // values' and the weights' 1.7e-4 each and the results' own 2.1e-4.  Exact codes, as in the form for few rows, which is
-// 2.7e-4 off, would need a sum of products a group, and tensor memory is full; that form takes 3 to 4 times as long here.)
+// 2.7e-4 off, would need a sum of products a group, and tensor memory is full; that form takes 2 to 4 times as long here.)
 // The pairs of a word come out as dims (0, 4), (1, 5), (2, 6), (3, 7); queries are stored in
 // that order, and outputs are put back.
 //
